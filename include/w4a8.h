@@ -292,6 +292,107 @@ w4a8_status_t w4a16_gemm(const w4a8_f16 *x, const uint8_t *w4, const float *w_sc
                          int32_t group_size, w4a8_f16 *y, int64_t M, int64_t N, int64_t K,
                          w4a8_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * The attention block between the qkv and the output product of a decoder
+ * layer: rotary positions, a paged key/value cache held in 4 bits, and
+ * attention over it.  The pages stop at the linear layers; these operators
+ * take the fp16 rows linear() writes ([T, (q + 2 kv) heads, head_dim]) and
+ * return fp16 rows linear() takes, and the cache uses the int4 rule above.
+ *
+ * Strides are in elements and multiples of 8; the heads of a token are
+ * contiguous ([heads, head_dim]), tokens may lie further apart than that
+ * (views into the qkv rows).  T == 0 is a valid empty call.
+ * ------------------------------------------------------------------------ */
+
+/* Rotary positions with 1 to 3 axes (time, height, width of a token of an
+ * image or a video; one axis for text).  x fp16 [T, heads, head_dim], token
+ * stride x_stride; positions int64 [axes, T]; inv_freq fp32 [rotary_dim / 2].
+ * With half = rotary_dim / 2, pair i = (x[i], x[i + half]) of every head turns
+ * by the angle a = positions[axis(i), t] * inv_freq[i]:
+ *     y[i] = x[i] cos a - x[i + half] sin a,  y[i + half] = x[i + half] cos a + x[i] sin a
+ * and the elements from rotary_dim on are copied.  sections: HOST array of
+ * `axes` counts, each >= 0, whose sum is half: how many pairs each axis turns.  axis(i) is, with
+ * interleaved == 0, the axis whose run of sections[a] consecutive pairs holds
+ * i; otherwise i mod axes while (i div axes) < sections[i mod axes], and axis
+ * 0 for the pairs left over.  The angle is formed and reduced in fp64, cosine
+ * and sine and the products are fp32, each output is rounded once: as exact
+ * as fp32 for |positions| < 2^31.  out fp16, same shape, token stride
+ * out_stride; out may be x itself (same stride), no other overlap.
+ * head_dim % 8 == 0, head_dim <= 1024, rotary_dim % 16 == 0, 0 < rotary_dim <= head_dim. */
+w4a8_status_t rotary_axes(const w4a8_f16 *x, int64_t x_stride, const int64_t *positions,
+                          const float *inv_freq, int64_t T, int32_t heads, int32_t head_dim,
+                          int32_t rotary_dim, int32_t axes, const int32_t *sections,
+                          int32_t interleaved, w4a8_f16 *out, int64_t out_stride,
+                          w4a8_stream_t stream);
+
+/* A paged key/value cache in 4 bits (caller-owned device buffers):
+ *   k, v              uint8 [pages, kv_heads, page_size, head_dim / 2]
+ *   k_scale, v_scale  fp32  [pages, kv_heads, page_size, head_dim / group_size]
+ * One token of one head is a row of int4 codes (the rule above, qmax = 7, over
+ * group_size consecutive elements).  Its natural bytes hold element 2j in the
+ * low and 2j + 1 in the high nibble of byte j; they are stored transposed, so
+ * that a lane's bytes of every 32-element step of a matrix product lie side
+ * by side: with n = head_dim / 32, natural 4-byte word 4g + b of a K row is
+ * stored as word b n + g, and natural byte 16 g + r of a V row as byte r n + g.
+ * Slot s of the cache is row s % page_size of page s / page_size.
+ * head_dim 64, 128 or 256; group_size 32, 64, 128 or 256 with group_size <=
+ * head_dim <= 4 group_size; page_size a power of two in [16, 2^20]; all four
+ * buffers 16-byte aligned. */
+typedef struct {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t pages;
+    int32_t kv_heads, page_size, head_dim, group_size;
+} kv4_cache_t;
+
+/* Quantize T tokens' keys and values as they are written: row t of k and v
+ * (fp16 [T, kv_heads, head_dim], token strides k_stride and v_stride) goes to
+ * slot slots[t] (int64 [T]).  Slots outside [0, pages * page_size) write
+ * nothing (padding rows carry -1; their values may be anything); the others
+ * have to differ, and their values to be finite. */
+w4a8_status_t kv4_write(const w4a8_f16 *k, int64_t k_stride, const w4a8_f16 *v, int64_t v_stride,
+                        const int64_t *slots, int64_t T, const kv4_cache_t *cache,
+                        w4a8_stream_t stream);
+
+/* Read T tokens back: k, v fp16 [T, kv_heads, head_dim] (contiguous) =
+ * fp16(fl32(code * scale)) of slot slots[t]; zeros for slots outside the cache. */
+w4a8_status_t kv4_read(const kv4_cache_t *cache, const int64_t *slots, int64_t T, w4a8_f16 *k,
+                       w4a8_f16 *v, w4a8_stream_t stream);
+
+/* Bytes of device workspace kv4_attention() needs for these sizes. */
+size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t T,
+                                    int64_t sequences, int32_t max_q);
+
+/* Attention of T query tokens of `sequences` sequences over the cache.
+ *   q            fp16 [T, q_heads, head_dim], token stride q_stride; q_heads % kv_heads == 0,
+ *                query head h reads kv head h / (q_heads / kv_heads)
+ *   page_table   int32 [sequences, max_pages]: page of tokens [p page_size, (p + 1) page_size)
+ *   kv_lens      int32 [sequences]: tokens in the cache, the queries' own among them
+ *   q_starts     int32 [sequences + 1]: sequence b's queries are rows q_starts[b] up to
+ *                q_starts[b + 1]; NULL: one query a sequence (T == sequences)
+ *   max_q        no sequence has more queries than this (rows past it are not computed)
+ * With n = kv_lens[b] and m queries, query i of sequence b stands at position
+ * p = n - m + i and sees the keys j < n; with `causal` only j <= p, and with
+ * window > 0 (causal only) only j > p - window.  Over the keys seen,
+ *     s_j = scale * sum_d q[d] k_j[d],  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
+ * where k_j, v_j are the values code * scale.  A query that sees nothing gets
+ * out = 0 and lse = -infinity.  Scores, maxima, sums and outputs are held in
+ * fp32; the codes enter the fp16 matrix products exactly, and the one rounding
+ * besides the output's is that of the weights softmax * v_scale to fp16.
+ * out fp16 [T, q_heads, head_dim] contiguous; lse fp32 [T, q_heads] or NULL.
+ * What the device-side tables hold is bounded, not trusted: kv_lens are cut to
+ * [0, max_pages * page_size], tokens of pages outside [0, pages) are not seen,
+ * queries outside [0, T) are not computed; nothing that is not seen has any
+ * influence, whatever its bytes are.  workspace: device buffer of
+ * kv4_attention_workspace_size() bytes, 256-byte aligned; each call writes
+ * what it reads there. */
+w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int32_t q_heads,
+                            const kv4_cache_t *cache, const int32_t *page_table,
+                            int32_t max_pages, const int32_t *kv_lens, const int32_t *q_starts,
+                            int64_t sequences, int32_t max_q, int32_t causal, int32_t window,
+                            float scale, w4a8_f16 *out, float *lse, void *workspace,
+                            size_t workspace_bytes, w4a8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,6 +10,12 @@ library's HIP kernels; nothing here computes.
     y = w8a8_gemm_pc(xq, xs, wq, sw)               # fp16 [M, N]
     y = linear(Mode.W8A8_PC, x, wq, sw)            # the whole layer, MV when M == 1
     y = w8a8_mv_pg(x1, wq, sw, 128)                # decode with per-group scales
+
+Between the qkv and the output product of a decoder layer:
+
+    rotary_axes(qk, positions, inv_freq, sections) # rotary positions, one to three axes
+    kv4_write(k, v, slots, cache)                  # keys and values to 4 bits, into a paged KV4Cache
+    o = kv4_attention(q, cache, page_table, kv_lens)
 """
 from __future__ import annotations
 
@@ -19,6 +25,8 @@ from .ops import (gemm_tile_config, int8_mv, is_available, linear, linear_noallo
                   quantize_act, quantize_weight_int8, w4a8_gemm, w4a8_gemm_partials,
                   w4a8_mv, w8a8_gemm_i32, w8a8_gemm_pc, w8a8_gemm_pg, w8a8_gemm_pg_partials,
                   w8a8_mv_pg, w8a16_gemm, w4a16_gemm)
+from .kv4 import (KV4Cache, kv4_attention, kv4_attention_workspace, kv4_attention_workspace_size,
+                  kv4_read, kv4_write, rotary_axes)
 
 __all__ = [
     "LIB_PATH", "GemmOp", "Mode", "Status", "gemm_tile_config", "W4A8Error", "check", "lib", "int8_mv", "is_available",
@@ -26,4 +34,6 @@ __all__ = [
     "quantize_weight_int8", "w4a8_gemm", "w4a8_gemm_partials", "w8a8_gemm_i32",
     "w8a8_gemm_pc", "w8a8_gemm_pg", "w8a8_gemm_pg_partials", "w4a8_mv", "w8a8_mv_pg",
     "w8a16_gemm", "w4a16_gemm",
+    "KV4Cache", "kv4_attention", "kv4_attention_workspace", "kv4_attention_workspace_size",
+    "kv4_read", "kv4_write", "rotary_axes",
 ]

@@ -40,6 +40,13 @@ _SIGNATURES = {
     "w4a8_gemm_partials": [_vp, _vp, _i32, _vp, _i64, _i64, _i64, _vp],
     "w8a16_gemm": [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp],
     "w4a16_gemm": [_vp, _vp, _vp, _i32, _vp, _i64, _i64, _i64, _vp],
+    "rotary_axes": [_vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _i32, ctypes.POINTER(_i32), _i32,
+                    _vp, _i64, _vp],
+    "kv4_write": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp],
+    "kv4_read": [_vp, _vp, _i64, _vp, _vp, _vp],
+    "kv4_attention_workspace_size": [_i32, _i32, _i32, _i64, _i64, _i32],
+    "kv4_attention": [_vp, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _i64, _i32, _i32, _i32,
+                      ctypes.c_float, _vp, _vp, _vp, _sz, _vp],
     "gemm_tile_config": [ctypes.c_int, _i64, _i64, _i64, _i32, ctypes.POINTER(_i64)],
 }
 _RESTYPES = {
@@ -47,7 +54,14 @@ _RESTYPES = {
     "w4a8_status_string": ctypes.c_char_p,
     "w4a8_last_error": ctypes.c_char_p,
     "linear_workspace_size": _sz,
+    "kv4_attention_workspace_size": _sz,
 }
+
+
+class CacheStruct(ctypes.Structure):
+    """kv4_cache_t."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("pages", _i64),
+                ("kv_heads", _i32), ("page_size", _i32), ("head_dim", _i32), ("group_size", _i32)]
 
 
 class Status(enum.IntEnum):

@@ -8,6 +8,7 @@
 
 #include "../../include/w4a8.h"
 #include "kernels.hpp"
+#include "kv4.hpp"
 
 using namespace w4a8;
 
@@ -42,6 +43,7 @@ constexpr int64_t kMaxMFew = 4;
 constexpr int64_t kMaxFewCodes = 65536;       // M * K bytes
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Per device ordinal: its compute-unit count if it is a gfx950, 0 if it is
@@ -359,6 +361,95 @@ w4a8_status_t linear_run(const char *fn, w4a8_mode_t mode, const w4a8_f16 *x, in
         return run_w4(fn, xq, xs, static_cast<const uint8_t *>(w), w_scale, group_size, y, M,
                       N, K, stream);
     }
+}
+
+// ---- the attention block
+
+bool stride_ok(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0 && stride <= (int64_t(1) << 40); }
+
+w4a8_status_t check_rotary(const char *fn, const void *x, int64_t x_stride, const int64_t *positions,
+                           const float *inv_freq, int64_t T, int32_t heads, int32_t head_dim,
+                           int32_t rotary_dim, int32_t axes, const int32_t *sections,
+                           const void *out, int64_t out_stride)
+{
+    if (T < 0 || T > kMaxDim || heads < 0 || heads > 65535)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: sizes out of range (T=%lld heads=%d)", fn,
+                    (long long)T, (int)heads);
+    if (head_dim <= 0 || head_dim % 8 != 0 || head_dim > 1024)
+        return fail(W4A8_ERR_SHAPE, "%s: head_dim=%d must be a multiple of 8 in [8, 1024]", fn,
+                    (int)head_dim);
+    if (rotary_dim <= 0 || rotary_dim % 16 != 0 || rotary_dim > head_dim)
+        return fail(W4A8_ERR_SHAPE, "%s: rotary_dim=%d must be a positive multiple of 16 up to "
+                    "head_dim=%d", fn, (int)rotary_dim, (int)head_dim);
+    if (axes < 1 || axes > 3)
+        return fail(W4A8_ERR_SHAPE, "%s: axes=%d must be 1, 2 or 3", fn, (int)axes);
+    if (!sections)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: null sections", fn);
+    int64_t sum = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (sections[a] < 0)
+            return fail(W4A8_ERR_SHAPE, "%s: sections[%d]=%d is negative", fn, a, (int)sections[a]);
+        sum += sections[a];
+    }
+    if (sum != rotary_dim / 2)
+        return fail(W4A8_ERR_SHAPE, "%s: the sections sum to %lld, not to rotary_dim / 2 = %d", fn,
+                    (long long)sum, (int)(rotary_dim / 2));
+    if (T == 0 || heads == 0)
+        return W4A8_OK;
+    if (!x || !positions || !inv_freq || !out)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: null pointer", fn);
+    const int64_t row = (int64_t)heads * head_dim;
+    if (!stride_ok(x_stride, row) || !stride_ok(out_stride, row))
+        return fail(W4A8_ERR_SHAPE, "%s: token strides must be multiples of 8, at least %lld", fn,
+                    (long long)row);
+    if (x == out && x_stride != out_stride)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: in place, the strides must be equal", fn);
+    if (!aligned16(x) || !aligned16(out) || !aligned8(positions) || !aligned4(inv_freq))
+        return fail(W4A8_ERR_ALIGNMENT, "%s: misaligned tensor", fn);
+    return W4A8_OK;
+}
+
+// The cache's geometry and buffers.
+w4a8_status_t check_cache(const char *fn, const kv4_cache_t *c)
+{
+    if (!c)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: null cache", fn);
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+        return fail(W4A8_ERR_SHAPE, "%s: head_dim=%d must be 64, 128 or 256", fn, (int)c->head_dim);
+    const int g = c->group_size;
+    if ((g != 32 && g != 64 && g != 128 && g != 256) || g > c->head_dim || c->head_dim > 4 * g)
+        return fail(W4A8_ERR_SHAPE, "%s: group_size=%d must be 32, 64, 128 or 256, at most "
+                    "head_dim=%d and at least a quarter of it", fn, g, (int)c->head_dim);
+    const int p = c->page_size;
+    if (p < 16 || p > (1 << 20) || (p & (p - 1)) != 0)
+        return fail(W4A8_ERR_SHAPE, "%s: page_size=%d must be a power of two in [16, 2^20]", fn, p);
+    if (c->kv_heads < 1 || c->kv_heads > 65535)
+        return fail(W4A8_ERR_SHAPE, "%s: kv_heads=%d out of range", fn, (int)c->kv_heads);
+    if (c->pages < 1 || c->pages > kMaxDim)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: pages=%lld out of range", fn, (long long)c->pages);
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: null cache buffer", fn);
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale))
+        return fail(W4A8_ERR_ALIGNMENT, "%s: cache buffers must be 16-byte aligned", fn);
+    return W4A8_OK;
+}
+
+Kv4Cache make_cache(const kv4_cache_t *c)
+{
+    Kv4Cache r;
+    r.k = c->k; r.v = c->v; r.ks = c->k_scale; r.vs = c->v_scale;
+    r.pages = c->pages;
+    r.heads = c->kv_heads; r.shift = __builtin_ctz((unsigned)c->page_size);
+    r.D = c->head_dim; r.G = c->group_size;
+    return r;
+}
+
+// T tokens of a cache: one lane takes 8 elements, 2^31 workgroups of 256 at most.
+w4a8_status_t check_tokens(const char *fn, int64_t T, const kv4_cache_t *c)
+{
+    if (T < 0 || T > kMaxDim || T * c->kv_heads > kMaxDim)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: T=%lld out of range", fn, (long long)T);
+    return W4A8_OK;
 }
 
 }  // namespace
@@ -698,6 +789,147 @@ w4a8_status_t gemm_tile_config(w4a8_gemm_op_t op, int64_t M, int64_t N, int64_t 
     out[4] = t.tiles;
     out[5] = t.per_cu;
     return ok();
+}
+
+w4a8_status_t rotary_axes(const w4a8_f16 *x, int64_t x_stride, const int64_t *positions,
+                          const float *inv_freq, int64_t T, int32_t heads, int32_t head_dim,
+                          int32_t rotary_dim, int32_t axes, const int32_t *sections,
+                          int32_t interleaved, w4a8_f16 *out, int64_t out_stride,
+                          w4a8_stream_t stream)
+{
+    const char *fn = "rotary_axes";
+    w4a8_status_t st = check_rotary(fn, x, x_stride, positions, inv_freq, T, heads, head_dim,
+                                    rotary_dim, axes, sections, out, out_stride);
+    if (st != W4A8_OK)
+        return st;
+    if (T == 0 || heads == 0)
+        return ok();
+    st = check_device();
+    if (st != W4A8_OK)
+        return st;
+    launch_rotary(x, x_stride, positions, inv_freq, T, heads, head_dim, rotary_dim, axes, sections,
+                  interleaved != 0, out, out_stride, (hipStream_t)stream);
+    return check_launch(fn);
+}
+
+w4a8_status_t kv4_write(const w4a8_f16 *k, int64_t k_stride, const w4a8_f16 *v, int64_t v_stride,
+                        const int64_t *slots, int64_t T, const kv4_cache_t *cache,
+                        w4a8_stream_t stream)
+{
+    const char *fn = "kv4_write";
+    w4a8_status_t st = check_cache(fn, cache);
+    if (st == W4A8_OK)
+        st = check_tokens(fn, T, cache);
+    if (st != W4A8_OK)
+        return st;
+    if (T == 0)
+        return ok();
+    if (!k || !v || !slots)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: null pointer", fn);
+    const int64_t row = (int64_t)cache->kv_heads * cache->head_dim;
+    if (!stride_ok(k_stride, row) || !stride_ok(v_stride, row))
+        return fail(W4A8_ERR_SHAPE, "%s: token strides must be multiples of 8, at least %lld", fn,
+                    (long long)row);
+    if (!aligned16(k) || !aligned16(v) || !aligned8(slots))
+        return fail(W4A8_ERR_ALIGNMENT, "%s: misaligned tensor", fn);
+    st = check_device();
+    if (st != W4A8_OK)
+        return st;
+    launch_kv4_write(k, k_stride, v, v_stride, slots, T, make_cache(cache), (hipStream_t)stream);
+    return check_launch(fn);
+}
+
+w4a8_status_t kv4_read(const kv4_cache_t *cache, const int64_t *slots, int64_t T, w4a8_f16 *k,
+                       w4a8_f16 *v, w4a8_stream_t stream)
+{
+    const char *fn = "kv4_read";
+    w4a8_status_t st = check_cache(fn, cache);
+    if (st == W4A8_OK)
+        st = check_tokens(fn, T, cache);
+    if (st != W4A8_OK)
+        return st;
+    if (T == 0)
+        return ok();
+    if (!k || !v || !slots)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(k) || !aligned16(v) || !aligned8(slots))
+        return fail(W4A8_ERR_ALIGNMENT, "%s: misaligned tensor", fn);
+    st = check_device();
+    if (st != W4A8_OK)
+        return st;
+    launch_kv4_read(make_cache(cache), slots, T, k, v, (hipStream_t)stream);
+    return check_launch(fn);
+}
+
+size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t T,
+                                    int64_t sequences, int32_t max_q)
+{
+    if (q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 || T <= 0 ||
+        sequences <= 0 || max_q <= 0)
+        return 0;
+    return kv4_attention_workspace(q_heads, kv_heads, head_dim, T, sequences, max_q);
+}
+
+w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int32_t q_heads,
+                            const kv4_cache_t *cache, const int32_t *page_table,
+                            int32_t max_pages, const int32_t *kv_lens, const int32_t *q_starts,
+                            int64_t sequences, int32_t max_q, int32_t causal, int32_t window,
+                            float scale, w4a8_f16 *out, float *lse, void *workspace,
+                            size_t workspace_bytes, w4a8_stream_t stream)
+{
+    const char *fn = "kv4_attention";
+    w4a8_status_t st = check_cache(fn, cache);
+    if (st != W4A8_OK)
+        return st;
+    if (T < 0 || sequences < 0 || T > kMaxDim || sequences > (1 << 20) || max_q < 0 ||
+        q_heads < 1 || q_heads > 65535 || T * q_heads > kMaxDim || max_pages < 0)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: sizes out of range (T=%lld q_heads=%d sequences=%lld "
+                    "max_q=%d max_pages=%d)", fn, (long long)T, (int)q_heads, (long long)sequences,
+                    (int)max_q, (int)max_pages);
+    if (q_heads % cache->kv_heads != 0)
+        return fail(W4A8_ERR_SHAPE, "%s: q_heads=%d is not a multiple of kv_heads=%d", fn,
+                    (int)q_heads, (int)cache->kv_heads);
+    if (((int64_t)max_pages * cache->page_size) > kMaxDim)
+        return fail(W4A8_ERR_SHAPE, "%s: max_pages=%d pages of %d tokens exceed 2^31 - 1 tokens", fn,
+                    (int)max_pages, (int)cache->page_size);
+    if (window < 0 || (window > 0 && !causal))
+        return fail(W4A8_ERR_INVALID_ARG, "%s: window=%d needs causal and must not be negative", fn,
+                    (int)window);
+    if (!(scale > 0.0f) || scale > 3.0e38f)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+    if (!q_starts && (T != sequences || (T > 0 && max_q < 1)))
+        return fail(W4A8_ERR_SHAPE, "%s: without q_starts, T=%lld must equal sequences=%lld and "
+                    "max_q be at least 1", fn, (long long)T, (long long)sequences);
+    if (T == 0 || sequences == 0 || max_q == 0)
+        return T == 0 ? ok() : fail(W4A8_ERR_SHAPE, "%s: %lld query rows in no sequence", fn,
+                                    (long long)T);
+    if (!q || !kv_lens || !out || (max_pages > 0 && !page_table))
+        return fail(W4A8_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!stride_ok(q_stride, (int64_t)q_heads * cache->head_dim))
+        return fail(W4A8_ERR_SHAPE, "%s: the token stride must be a multiple of 8, at least %lld",
+                    fn, (long long)q_heads * cache->head_dim);
+    if (!aligned16(q) || !aligned16(out) || !aligned4(page_table) || !aligned4(kv_lens) ||
+        !aligned4(q_starts) || !aligned4(lse))
+        return fail(W4A8_ERR_ALIGNMENT, "%s: misaligned tensor", fn);
+    Kv4AttnArgs a;
+    a.q = q; a.q_stride = q_stride; a.T = T; a.q_heads = q_heads;
+    a.group = q_heads / cache->kv_heads;
+    a.table = page_table; a.max_pages = max_pages; a.kv_lens = kv_lens; a.q_starts = q_starts;
+    a.B = sequences;
+    a.max_q = (int)(max_q < T ? max_q : T);
+    a.causal = causal != 0; a.window = window; a.scale = scale;
+    a.out = out; a.lse = lse; a.workspace = workspace;
+    const size_t need = kv4_attention_workspace_size(q_heads, cache->kv_heads, cache->head_dim, T,
+                                                     sequences, max_q);
+    if (need > 0 && (!workspace || workspace_bytes < need ||
+                     (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+        return fail(W4A8_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) needed, got "
+                    "%zu", fn, need, workspace_bytes);
+    st = check_device(&a.num_cu);
+    if (st != W4A8_OK)
+        return st;
+    launch_kv4_attention(make_cache(cache), a, (hipStream_t)stream);
+    return check_launch(fn);
 }
 
 }  // extern "C"
