@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <random>
 
 #include "../../include/w4a8.h"
 #include "kernels.hpp"
@@ -444,6 +445,15 @@ Kv4Cache make_cache(const kv4_cache_t *c)
     return r;
 }
 
+// A tag per call of kv4_attention for the counters in its workspace: 48 bits
+// over a 16-bit count, other than those of the calls before and, by a random
+// start, of other processes'.
+uint64_t next_tag()
+{
+    static std::atomic<uint64_t> tag{std::random_device{}() ^ ((uint64_t)std::random_device{}() << 20)};
+    return (tag.fetch_add(1, std::memory_order_relaxed) | (uint64_t(1) << 47)) << 16;
+}
+
 // T tokens of a cache: one lane takes 8 elements, 2^31 workgroups of 256 at most.
 w4a8_status_t check_tokens(const char *fn, int64_t T, const kv4_cache_t *c)
 {
@@ -865,9 +875,9 @@ size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t h
                                     int64_t sequences, int32_t max_q)
 {
     if (q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 || T <= 0 ||
-        sequences <= 0 || max_q <= 0)
+        sequences <= 0 || sequences > (1 << 20) || max_q <= 0)
         return 0;
-    return kv4_attention_workspace(q_heads, kv_heads, head_dim, T, sequences, max_q);
+    return kv4_attention_workspace(q_heads, kv_heads, head_dim, T, (int)sequences, max_q);
 }
 
 w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int32_t q_heads,
@@ -889,9 +899,10 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
     if (q_heads % cache->kv_heads != 0)
         return fail(W4A8_ERR_SHAPE, "%s: q_heads=%d is not a multiple of kv_heads=%d", fn,
                     (int)q_heads, (int)cache->kv_heads);
-    if (((int64_t)max_pages * cache->page_size) > kMaxDim)
-        return fail(W4A8_ERR_SHAPE, "%s: max_pages=%d pages of %d tokens exceed 2^31 - 1 tokens", fn,
-                    (int)max_pages, (int)cache->page_size);
+    const int64_t most = (int64_t)max_pages * cache->page_size;
+    if (most > (int64_t(1) << 30) || (most / 32 + 1) * sequences * cache->kv_heads > (int64_t(1) << 45))
+        return fail(W4A8_ERR_SHAPE, "%s: max_pages=%d pages of %d tokens are too many (2^30 a "
+                    "sequence, 2^50 in all)", fn, (int)max_pages, (int)cache->page_size);
     if (window < 0 || (window > 0 && !causal))
         return fail(W4A8_ERR_INVALID_ARG, "%s: window=%d needs causal and must not be negative", fn,
                     (int)window);
@@ -915,10 +926,10 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
     a.q = q; a.q_stride = q_stride; a.T = T; a.q_heads = q_heads;
     a.group = q_heads / cache->kv_heads;
     a.table = page_table; a.max_pages = max_pages; a.kv_lens = kv_lens; a.q_starts = q_starts;
-    a.B = sequences;
+    a.B = (int)sequences;
     a.max_q = (int)(max_q < T ? max_q : T);
     a.causal = causal != 0; a.window = window; a.scale = scale;
-    a.out = out; a.lse = lse; a.workspace = workspace;
+    a.out = out; a.lse = lse; a.workspace = workspace; a.tag = next_tag();
     const size_t need = kv4_attention_workspace_size(q_heads, cache->kv_heads, cache->head_dim, T,
                                                      sequences, max_q);
     if (need > 0 && (!workspace || workspace_bytes < need ||

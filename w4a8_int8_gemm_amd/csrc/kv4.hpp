@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "device_common.hpp"
+#include "kv4_index.h"
 
 namespace w4a8 {
 
@@ -31,7 +32,7 @@ struct Kv4AttnArgs {
     int max_pages;
     const int32_t *kv_lens;     // [B]
     const int32_t *q_starts;    // [B + 1] or null (one query a sequence)
-    int64_t B;
+    int B;
     int max_q;
     bool causal;
     int window;                 // 0: none
@@ -39,6 +40,7 @@ struct Kv4AttnArgs {
     uint16_t *out;              // [T, q_heads, D]
     float *lse;                 // [T, q_heads] or null
     void *workspace;
+    uint64_t tag;               // of this call among the counters in the workspace
     int num_cu;
 };
 
@@ -51,48 +53,21 @@ void launch_kv4_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, in
 void launch_kv4_read(const Kv4Cache &c, const int64_t *slots, int64_t T, uint16_t *k, uint16_t *v,
                      hipStream_t st);
 
-size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int64_t B, int max_q);
+size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int B, int max_q);
 void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st);
 
-// A sequence's queries and keys as the device-side tables give them, cut to
-// what the call's buffers hold.
-struct Kv4Seq {
-    int64_t q0;                 // first query row
-    int m;                      // queries
-    int64_t n;                  // keys
-};
-__device__ __forceinline__ Kv4Seq kv4_sequence(const Kv4AttnArgs &a, int shift, int64_t b)
-{
-    Kv4Seq s;
-    const int64_t most = (int64_t)a.max_pages << shift;
-    const int64_t n = a.kv_lens[b];
-    s.n = n < 0 ? 0 : n < most ? n : most;
-    if (a.q_starts) {
-        const int64_t q0 = a.q_starts[b], q1 = a.q_starts[b + 1];
-        s.q0 = q0 < 0 ? 0 : q0;
-        const int64_t end = q1 < a.T ? q1 : a.T;
-        int64_t m = end - s.q0;
-        m = m < 0 ? 0 : m;
-        s.m = (int)(m < a.max_q ? m : a.max_q);
-    } else {
-        s.q0 = b;
-        s.m = b < a.T ? 1 : 0;
-    }
-    return s;
-}
+// Sequences of at most this many query rows a kv head (queries x query heads).
+inline int kv4_decode_limit(int D) { return D < 256 ? 64 : 32; }
+constexpr int kDecodeParts = 512;             // workgroups that share the keys: two per compute unit
+inline size_t kv4_counter_bytes(int64_t B, int heads) { return ((size_t)B * heads * 8 + 255) & ~size_t(255); }
+void launch_kv4_decode(const Kv4Cache &c, const Kv4AttnArgs &a, int rows, hipStream_t st);
 
-// The keys query i of m sees: [lo, hi).
-__device__ __forceinline__ void kv4_visible(const Kv4AttnArgs &a, int64_t n, int m, int i,
-                                            int64_t &lo, int64_t &hi)
+// Sequence b of the call.
+__device__ __forceinline__ Kv4Seq kv4_sequence(const Kv4AttnArgs &a, int shift, int b)
 {
-    lo = 0;
-    hi = n;
-    if (a.causal) {
-        hi = n - m + i + 1;
-        if (a.window > 0 && hi - a.window > 0)
-            lo = hi - a.window;
-        hi = hi < 0 ? 0 : hi;
-    }
+    const int start = a.q_starts ? a.q_starts[b] : b;
+    const int end = a.q_starts ? a.q_starts[b + 1] : b + 1;
+    return kv4_cut(start, end, a.kv_lens[b], (int)a.T, a.max_q, a.max_pages << shift);
 }
 
 }  // namespace w4a8

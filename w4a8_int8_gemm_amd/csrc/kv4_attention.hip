@@ -3,13 +3,11 @@
 // One wavefront per (query row, query head): each lane scores one key of a
 // step of 64, the running maximum and sum of the softmax are kept over the
 // steps, and the lanes then hold the output's elements.
-#include "kv4.hpp"
+#include "kv4_device.hpp"
 
 namespace w4a8 {
 
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float wave_max(float v)
 {
@@ -30,19 +28,19 @@ __device__ __forceinline__ float nibble(uint32_t word, int e)
 }
 
 // grid.x over the rows (sequence, query index), grid.y over the query heads / 4.
-__global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4Cache c, Kv4AttnArgs a)
+__global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4Cache c, Kv4AttnArgs a, int row_limit)
 {
     __shared__ float qs[4][256], ps[4][64];
     __shared__ int64_t rows[4][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t b = blockIdx.x / a.max_q;
+    const int b = blockIdx.x / a.max_q;
     const int i = (int)(blockIdx.x % a.max_q);
     const int h = blockIdx.y * 4 + wave;
     const Kv4Seq s = kv4_sequence(a, c.shift, b);
     const bool active = i < s.m && h < a.q_heads;
-    int64_t lo = 0, hi = 0;
-    if (i < s.m)                 // the same for the four waves: they share the steps' barriers
-        kv4_visible(a, s.n, s.m, i, lo, hi);
+    if ((int64_t)s.m * a.group <= row_limit)
+        return;
+    const int lo = kv4_lo(s.n, s.m, i, a.window), hi = kv4_hi(s.n, s.m, i, a.causal);
     const int D = c.D, n32 = D / 32, NG = D / c.G;
     const int64_t qrow = s.q0 + i;
     const int hk = active ? h / a.group : 0;
@@ -50,14 +48,14 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4Cache c, Kv4AttnA
         for (int d = lane; d < D; d += 64)
             qs[wave][d] = h2f(a.q[qrow * a.q_stride + (int64_t)h * D + d]);
     float m = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int64_t steps = (s.n + 63) / 64;
+    const int64_t steps = ((int64_t)s.n + 63) / 64;
     for (int64_t st = lo / 64; st < steps; ++st) {
         __syncthreads();
         const int64_t j = st * 64 + lane;
         bool seen = active && j >= lo && j < hi;
         int64_t row = 0;
         if (seen) {
-            const int64_t page = a.table[b * a.max_pages + (j >> c.shift)];
+            const int64_t page = a.table[(int64_t)b * a.max_pages + (j >> c.shift)];
             seen = page >= 0 && page < c.pages;
             if (seen)
                 row = c.row(page, hk, (int)(j & ((1 << c.shift) - 1)));
@@ -110,13 +108,32 @@ __global__ __launch_bounds__(256) void kv4_attention_kernel(Kv4Cache c, Kv4AttnA
 
 }  // namespace
 
-size_t kv4_attention_workspace(int, int, int, int64_t, int64_t, int) { return 0; }
+namespace {
+
+// Rows a kv head that the kernel for few rows is launched for: what a sequence
+// can have, or that kernel's limit.
+int decode_rows(int D, int group, int64_t max_q)
+{
+    const int limit = kv4_decode_limit(D);
+    return group * max_q < limit ? (int)(group * max_q) : limit;
+}
+
+}  // namespace
+
+size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int B, int max_q)
+{
+    const int rows = decode_rows(D, q_heads / kv_heads, max_q < T ? max_q : T);
+    return kv4_counter_bytes(B, kv_heads) + (size_t)2 * kDecodeParts * rows * (D + 2) * sizeof(float);
+}
 
 void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st)
 {
-    hipLaunchKernelGGL(kv4_attention_kernel,
-                       dim3((unsigned)(a.B * a.max_q), (unsigned)((a.q_heads + 3) / 4)), dim3(256),
-                       0, st, c, a);
+    const int limit = kv4_decode_limit(c.D);
+    if (a.group <= limit)
+        launch_kv4_decode(c, a, decode_rows(c.D, a.group, a.max_q), st);
+    if ((int64_t)a.group * a.max_q > limit)
+        hipLaunchKernelGGL(kv4_attention_kernel, dim3((unsigned)((int64_t)a.B * a.max_q), (unsigned)((a.q_heads + 3) / 4)),
+                           dim3(256), 0, st, c, a, a.group <= limit ? limit : 0);
 }
 
 }  // namespace w4a8

@@ -1,0 +1,87 @@
+// Integer rules of the attention kernels: what a sequence's entries in the
+// device-side tables mean once they are cut to the call's buffers, which keys
+// a query sees, and how the work is divided over the workgroups.  Plain C++
+// without device code, so that the CPU test suite runs it on hostile tables.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIPCC__)
+#include <hip/hip_runtime.h>
+#define KV4_HD __host__ __device__ __forceinline__
+#else
+#define KV4_HD static inline
+#endif
+
+namespace w4a8 {
+
+// A sequence's queries and keys.
+struct Kv4Seq {
+    int q0;                     // first query row
+    int m;                      // queries, all rows [q0, q0 + m) inside [0, T)
+    int n;                      // keys, all inside the table's pages
+};
+
+// From the tables' entries: `start`, `end` the sequence's rows, `len` its keys
+// (any values); T rows (< 2^31) in the call, at most max_q of them a sequence's; `most`
+// keys in the table's pages (< 2^31).
+KV4_HD Kv4Seq kv4_cut(int start, int end, int len, int T, int max_q, int most)
+{
+    Kv4Seq s;
+    s.n = len < 0 ? 0 : len < most ? len : most;
+    s.q0 = start < 0 ? 0 : start < T ? start : T;
+    end = end < T ? end : T;
+    s.m = end > s.q0 ? end - s.q0 : 0;
+    s.m = s.m < max_q ? s.m : max_q;
+    return s;
+}
+
+// The keys [lo, hi) that query i of m sees among n.
+KV4_HD int kv4_hi(int n, int m, int i, bool causal)
+{
+    const int hi = causal ? n - m + i + 1 : n;
+    return hi < 0 ? 0 : hi;
+}
+KV4_HD int kv4_lo(int n, int m, int i, int window)
+{
+    if (window <= 0)
+        return 0;
+    const int lo = n - m + i + 1 - window;
+    return lo < 0 ? 0 : lo;
+}
+
+// Steps of 32 keys that a sequence's queries need together; one (empty) step
+// where they see nothing, none without queries.
+struct Kv4Steps {
+    int first, count;
+};
+KV4_HD Kv4Steps kv4_steps(const Kv4Seq &s, bool causal, int window)
+{
+    Kv4Steps r = {0, 0};
+    if (s.m == 0)
+        return r;
+    const int hi = kv4_hi(s.n, s.m, s.m - 1, causal), lo = kv4_lo(s.n, s.m, 0, window);
+    r.first = lo / 32;
+    r.count = (int)(((int64_t)hi + 31) / 32) - r.first;
+    r.count = r.count < 1 ? 1 : r.count;
+    return r;
+}
+
+// U units in `parts` contiguous parts: the first unit of part i, and the part
+// that holds unit u.
+KV4_HD int64_t kv4_part_begin(int64_t U, int parts, int64_t i) { return U * i / parts; }
+KV4_HD int kv4_part_of(int64_t U, int parts, int64_t u)
+{
+    return (int)(((u + 1) * parts - 1) / U);
+}
+// Parts used for U units: all of them only where each gets `least` units.
+KV4_HD int kv4_parts(int64_t U, int parts, int least)
+{
+    const int64_t p = (U + least - 1) / least;
+    return p < parts ? (int)p : parts;
+}
+
+// Where a page's 16-token piece lies, and whether the table's entry names a page at all.
+KV4_HD bool kv4_page_ok(int page, int64_t pages) { return page >= 0 && page < pages; }
+
+}  // namespace w4a8
