@@ -11,13 +11,14 @@ void cut(int start, int end, int len, int T, int max_q, int most, int *out)
 }
 int lo(int n, int m, int i, int window) { return kv4_lo(n, m, i, window); }
 int hi(int n, int m, int i, int causal) { return kv4_hi(n, m, i, causal != 0); }
-void steps(int m, int n, int causal, int window, int *out)
+void steps(int m, int n, int causal, int window, int keys, int *out)
 {
-    const Kv4Steps r = kv4_steps(Kv4Seq{0, m, n}, causal != 0, window);
+    const Kv4Steps r = kv4_steps(Kv4Seq{0, m, n}, causal != 0, window, keys);
     out[0] = r.first, out[1] = r.count;
 }
-int64_t part_begin(int64_t U, int parts, int64_t i) { return kv4_part_begin(U, parts, i); }
-int part_of(int64_t U, int parts, int64_t u) { return kv4_part_of(U, parts, u); }
-int parts(int64_t U, int most, int least) { return kv4_parts(U, most, least); }
+int part_limit(int64_t total, int keys) { return kv4_part_limit(total, keys); }
+int split(int count, int parts, int i) { return kv4_split(count, parts, i); }
+int64_t decode_grid(int64_t B, int heads, int64_t most) { return kv4_decode_grid(B, heads, most); }
+int parts_more() { return kPartsMore; }
 int page_ok(int page, int64_t pages) { return kv4_page_ok(page, pages); }
 }

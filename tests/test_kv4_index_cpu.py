@@ -18,10 +18,9 @@ def L(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", os.path.join(HERE, "native", "kv4_index_shim.cpp"),
                     "-o", so], check=True)
     lib = ctypes.CDLL(so)
-    lib.part_begin.restype = ctypes.c_int64
-    lib.part_begin.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int64]
-    lib.part_of.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int64]
-    lib.parts.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int]
+    lib.part_limit.argtypes = [ctypes.c_int64, ctypes.c_int]
+    lib.decode_grid.restype = ctypes.c_int64
+    lib.decode_grid.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int64]
     lib.page_ok.argtypes = [ctypes.c_int, ctypes.c_int64]
     return lib
 
@@ -45,14 +44,15 @@ def test_cut_keeps_what_is_right(L):
     assert cut(L, 3, 3, 0, 20, 4, 128) == (3, 0, 0)
 
 
-def test_visible_ranges_and_steps(L):
+@pytest.mark.parametrize("keys", [32, 64])
+def test_visible_ranges_and_steps(L, keys):
     """Every key that some query sees lies in the steps; there is always a step while there are queries."""
     out = (ctypes.c_int * 2)()
     for n, m, causal, window in itertools.product([0, 1, 31, 32, 33, 64, 100], [0, 1, 2, 31, 40, 150], [0, 1],
                                                   [0, 1, 7, 32, 99]):
         if window and not causal:
             continue
-        L.steps(m, n, causal, window, out)
+        L.steps(m, n, causal, window, keys, out)
         first, count = out
         assert (count == 0) == (m == 0) and first >= 0
         for i in range(m):
@@ -61,30 +61,40 @@ def test_visible_ranges_and_steps(L):
             seen = [j for j in range(n) if (not causal or j <= p) and (not window or j > p - window)]
             assert [j for j in range(n) if lo <= j < hi] == seen
             if seen:
-                assert 32 * first <= seen[0] and seen[-1] < 32 * (first + count)
-        assert 32 * (first + count) <= (n + 31) // 32 * 32 or count == 1
+                assert keys * first <= seen[0] and seen[-1] < keys * (first + count)
+        assert keys * (first + count) <= -(-n // keys) * keys or count == 1
 
 
 def test_steps_at_the_ends(L):
     out = (ctypes.c_int * 2)()
-    L.steps(1, 1 << 30, 1, 0, out)
+    L.steps(1, 1 << 30, 1, 0, 32, out)
     assert tuple(out) == (0, 1 << 25)
-    L.steps(5, 1 << 30, 1, TOP, out)
+    L.steps(5, 1 << 30, 1, TOP, 32, out)
     assert tuple(out) == (0, 1 << 25)
-    L.steps(TOP, 7, 1, 3, out)
+    L.steps(TOP, 7, 1, 3, 64, out)
     assert out[0] == 0 and out[1] == 1
 
 
-def test_parts_cover_the_units_once(L):
+def test_parts_cover_the_steps_and_fit_the_grid(L):
     r = random.Random(1)
-    for _ in range(400):
-        U, most, least = r.choice([1, 5, 37, 1000, 10 ** 6, 1 << 45]) + r.randint(0, 3), r.randint(1, 600), r.randint(1, 40)
-        parts = L.parts(U, most, least)
-        assert 1 <= parts <= most
-        assert L.part_begin(U, parts, 0) == 0 and L.part_begin(U, parts, parts) == U
-        for u in {0, U - 1, U // 2, r.randrange(U)}:
-            i = L.part_of(U, parts, u)
-            assert 0 <= i < parts and L.part_begin(U, parts, i) <= u < L.part_begin(U, parts, i + 1)
+    for _ in range(600):
+        keys = r.choice([32, 64])
+        B, heads, most = r.randint(1, 70), r.randint(1, 40), 16 * r.choice([0, 1, 2, 60, 65, 5000, 1 << 20])
+        counts = [max(1, -(-r.choice([most, r.randint(0, most)]) // keys)) if r.random() < 0.8 else 0 for _ in range(B)]
+        limit = L.part_limit(heads * sum(counts), keys)
+        parts = [-(-n // limit) for n in counts]
+        assert heads * sum(parts) <= L.decode_grid(B, heads, most)
+        assert max(parts) <= L.parts_more() + 1 < 65536            # arrivals are counted in 16 bits
+        for n, k in zip(counts, parts):
+            if n:
+                cuts = [L.split(n, k, i) for i in range(k + 1)]
+                assert cuts[0] == 0 and cuts[-1] == n
+                assert all(0 < b - a <= limit for a, b in zip(cuts, cuts[1:]))
+
+
+def test_parts_at_the_ends(L):
+    assert L.part_limit(0, 32) == 32 and L.part_limit(0, 64) == 16 and L.part_limit(1 << 60, 64) == 0x3fffffff
+    assert L.split(1 << 25, 1025, 1025) == 1 << 25
 
 
 def test_pages(L):

@@ -892,7 +892,8 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
     if (st != W4A8_OK)
         return st;
     if (T < 0 || sequences < 0 || T > kMaxDim || sequences > (1 << 20) || max_q < 0 ||
-        q_heads < 1 || q_heads > 65535 || T * q_heads > kMaxDim || max_pages < 0)
+        q_heads < 1 || q_heads > 65535 || T * q_heads > kMaxDim ||
+        sequences * cache->kv_heads > (1 << 28) || max_pages < 0)
         return fail(W4A8_ERR_INVALID_ARG, "%s: sizes out of range (T=%lld q_heads=%d sequences=%lld "
                     "max_q=%d max_pages=%d)", fn, (long long)T, (int)q_heads, (long long)sequences,
                     (int)max_q, (int)max_pages);

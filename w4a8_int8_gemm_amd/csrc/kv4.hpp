@@ -58,8 +58,9 @@ void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t s
 
 // Sequences of at most this many query rows a kv head (queries x query heads).
 inline int kv4_decode_limit(int D) { return D < 256 ? 64 : 32; }
-constexpr int kDecodeParts = 512;             // workgroups that share the keys: two per compute unit
-inline size_t kv4_counter_bytes(int64_t B, int heads) { return ((size_t)B * heads * 8 + 255) & ~size_t(255); }
+// A counter for each (sequence, head), on lines of their own: arrivals on one line queue up.
+constexpr int kCounterStride = 16;
+inline size_t kv4_counter_bytes(int64_t B, int heads) { return ((size_t)B * heads * kCounterStride * 8 + 255) & ~size_t(255); }
 void launch_kv4_decode(const Kv4Cache &c, const Kv4AttnArgs &a, int rows, hipStream_t st);
 
 // Sequence b of the call.

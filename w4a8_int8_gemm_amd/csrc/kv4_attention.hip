@@ -123,7 +123,7 @@ int decode_rows(int D, int group, int64_t max_q)
 size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int B, int max_q)
 {
     const int rows = decode_rows(D, q_heads / kv_heads, max_q < T ? max_q : T);
-    return kv4_counter_bytes(B, kv_heads) + (size_t)2 * kDecodeParts * rows * (D + 2) * sizeof(float);
+    return kv4_counter_bytes(B, kv_heads) + (size_t)(B * (int64_t)kv_heads + kPartsMore) * rows * (D + 2) * sizeof(float);
 }
 
 void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st)

@@ -6,69 +6,83 @@
 // What bounds it: HBM.  A key and value of one head take D + 8 D / G bytes
 // and 4 D operations per query row.
 //
-// One wavefront takes steps of 32 keys.  S^T = K Q^T on 16x16x32 matrix
-// instructions with the codes as fp16 (exact) and the keys' scales applied to
-// the fp32 scores; the result leaves a lane with one query row and four
-// consecutive keys of each 16, which is, for two pieces of 16, the operand of
-// the second product O^T = V^T P^T as it stands.  The cache's byte order
-// gives a lane its operand bytes side by side: K's as one load of D / 8
-// bytes, V's as D / 32 bytes of each of its eight keys.  The next step's
-// loads are in flight while one is computed.
+// One wavefront takes steps of 64 keys (32 where the registers hold no more).  S^T =
+// K Q^T on 16x16x32 matrix instructions with the codes as fp16 (exact) and the
+// keys' scales applied to the fp32 scores; the result leaves a lane with one
+// query row and four consecutive keys of each 16, which is, for two pieces of
+// 16, the operand of the second product O^T = V^T P^T as it stands.  The
+// cache's byte order gives a lane its operand bytes side by side: K's as one
+// load of D / 8 bytes, V's as D / 32 bytes of each of its keys.  The loads of
+// the next steps are in flight while one is computed.
 //
-// The work is split in units of steps, the same number for every workgroup
-// whatever the sequences' lengths: a workgroup finds its range of (sequence,
-// head, step) from a scan of the lengths, splits each piece of it over its
-// four waves and joins them in LDS.  Where a (sequence, head) lies in several
-// workgroups' ranges each leaves its part in the workspace and the last to
-// arrive joins them in order, so the result does not depend on who that is.
+// The keys of a (sequence, head) are cut into parts of at most `limit` steps,
+// the same limit for all, so that a workgroup (four waves, joined in LDS) has
+// one part whatever the sequences' lengths; a workgroup finds its own from a
+// scan of the lengths.  Where there are several parts each is left in the
+// workspace and the last to arrive joins them in order, so the result does
+// not depend on who that is.
 #include "kv4_device.hpp"
+#include "lds_copy.hpp"
 
 namespace w4a8 {
 
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
 struct Partial {
-    float *base;                // [2 parts][slot_rows][D + 2]
+    float *base;                // [grid][slot_rows][D + 2]
     int slot_rows;
-    uint64_t *counters;         // [B * heads]
-    int parts, least;
+    uint64_t *counters;         // [B * heads][kCounterStride]
+    int grid;
     int row_limit;              // sequences with more rows are left to the other kernel
+    uint32_t over_group;        // ceil(2^16 / group): row / group of rows < 64, group <= 64
 };
 
-// What a lane loads for a step of 32 keys: pieces p = 0, 1 of 16 keys.  Of the
-// scales, which the 16 lanes of a row share, a lane takes one key's: lane
-// 8 p + 4 v + j of a row K's (v = 0) or V's (v = 1) of key 4 (lane / 16) + j.
-template <int N32, int NG> struct Step {
-    uint32_t k[2][N32];                 // key lane % 16: dims 32 i + 8 (lane / 16) ..+7
-    uint32_t v[2][4][(N32 + 3) / 4];    // keys 4 (lane / 16) + j: dims 32 g + 2 (lane % 16) ..+1
-    float sc[NG];
-    bool ok[2];                         // the page exists
+// Pieces of 16 keys in a step: more of them share the softmax's bookkeeping,
+// where the registers hold them.
+template <int D, int RT> constexpr int kPieces = 2;
+
+// What a lane loads for a step of P pieces of 16 keys.  Of the scales, which
+// the 16 lanes of a row share, a lane takes one key's of every second piece:
+// lane 8 x + 4 v + j of a row K's (v = 0) or V's (v = 1) of key
+// 4 (lane / 16) + j of the pieces 2 h + x.
+template <int P, int N32, int NG> struct Step {
+    uint32_t k[P][N32];                 // key lane % 16: dims 32 i + 8 (lane / 16) ..+7
+    uint32_t v[P][4][(N32 + 3) / 4];    // keys 4 (lane / 16) + j: dims 32 g + 2 (lane % 16) ..+1
+    float sc[P / 2][NG];
+    uint32_t ok;                        // bit p: the page of piece p exists
 };
 
-template <int D, int NG>
-__device__ __forceinline__ void load_step(Step<D / 32, NG> &s, const Kv4Cache &c, int head, int page0, int page1,
-                                          int step, int lane)
+// A lane's offsets into a piece's rows.
+struct LaneAt {
+    uint32_t k, v;              // bytes
+    int64_t scale;              // bytes from K's scales of the piece
+    bool odd;                   // scales of the odd pieces
+};
+
+template <int P, int D, int NG>
+__device__ __forceinline__ void load_step(Step<P, D / 32, NG> &s, const Kv4Cache &c, int head, const int (&page)[P],
+                                          int step, const LaneAt &at)
 {
     constexpr int N32 = D / 32;
-    const int r = lane & 15, b = lane >> 4;
-    int64_t rows[2];
+    const char *scales = nullptr;
+    s.ok = 0;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const int page = p ? page1 : page0;
-        s.ok[p] = kv4_page_ok(page, c.pages);
-        const int at = (step * 32 + p * 16) & ((1 << c.shift) - 1);
-        const int64_t row = rows[p] = c.row(s.ok[p] ? page : 0, head, at);
-        const uint8_t *kp = c.k + row * (D / 2) + (uint32_t)(r * (D / 2) + b * (D / 8));
-        const uint8_t *vp = c.v + row * (D / 2) + (uint32_t)(4 * b * (D / 2) + r * N32);
+    for (int p = 0; p < P; ++p) {
+        const bool ok = kv4_page_ok(page[p], c.pages);
+        s.ok |= ok ? 1u << p : 0u;
+        const int64_t row = c.row(ok ? page[p] : 0, head, (step * (16 * P) + p * 16) & ((1 << c.shift) - 1));
+        const uint8_t *kp = c.k + row * (D / 2), *vp = c.v + row * (D / 2);
+        const char *sr = reinterpret_cast<const char *>(c.ks + row * NG);
+        scales = p % 2 && !at.odd ? scales : sr;
         if constexpr (N32 == 2) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(kp);
+            const uint2 w = *reinterpret_cast<const uint2 *>(kp + at.k);
             s.k[p][0] = w.x, s.k[p][1] = w.y;
         } else {
 #pragma unroll
             for (int i = 0; i < N32 / 4; ++i) {
-                const v4u w = reinterpret_cast<const v4u *>(kp)[i];
+                const v4u w = *reinterpret_cast<const v4u *>(kp + (at.k + 16 * i));
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     s.k[p][4 * i + e] = w[e];
@@ -76,7 +90,7 @@ __device__ __forceinline__ void load_step(Step<D / 32, NG> &s, const Kv4Cache &c
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint8_t *q = vp + j * (D / 2);
+            const uint8_t *q = vp + (at.v + j * (D / 2));
             if constexpr (N32 == 2) {
                 s.v[p][j][0] = *reinterpret_cast<const uint16_t *>(q);
             } else if constexpr (N32 == 4) {
@@ -86,26 +100,112 @@ __device__ __forceinline__ void load_step(Step<D / 32, NG> &s, const Kv4Cache &c
                 s.v[p][j][0] = w.x, s.v[p][j][1] = w.y;
             }
         }
-    }
-    const float *base = (r & 4) ? c.vs : c.ks;
-    const float *sp = base + ((r & 8) ? rows[1] : rows[0]) * NG + (4 * b + (r & 3)) * NG;
-    if constexpr (NG == 1) {
-        s.sc[0] = *sp;
-    } else if constexpr (NG == 2) {
-        const float2 w = *reinterpret_cast<const float2 *>(sp);
-        s.sc[0] = w.x, s.sc[1] = w.y;
-    } else {
-        const v4f w = *reinterpret_cast<const v4f *>(sp);
+        if (p % 2 == 0)
+            continue;
+        const float *sp = reinterpret_cast<const float *>(scales + at.scale);
+        if constexpr (NG == 1) {
+            s.sc[p / 2][0] = *sp;
+        } else if constexpr (NG == 2) {
+            const float2 w = *reinterpret_cast<const float2 *>(sp);
+            s.sc[p / 2][0] = w.x, s.sc[p / 2][1] = w.y;
+        } else {
+            const v4f w = *reinterpret_cast<const v4f *>(sp);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            s.sc[e] = w[e];
+            for (int e = 0; e < 4; ++e)
+                s.sc[p / 2][e] = w[e];
+        }
+    }
+}
+
+// A row's output and log of the softmax sum from its joined part.
+template <int D>
+__device__ __forceinline__ void store_row(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int row,
+                                          int d, float4 sum, float ref, float l)
+{
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int i = (int)((uint32_t)row * w.over_group >> 16);
+    const int64_t at = (int64_t)(seq.q0 + i) * a.q_heads + head * a.group + (row - i * a.group);
+    *reinterpret_cast<uint2 *>(a.out + at * D + d) =
+        make_uint2(pack_h2(sum.x * inv, sum.y * inv), pack_h2(sum.z * inv, sum.w * inv));
+    if (a.lse && d == 0)
+        a.lse[at] = l > 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+}
+
+// Joins the parts p0 .. p1 (workgroups) of an item.  A thread takes four dims
+// of a row; where there are more threads, groups of them take every
+// so-many-th part and are joined in LDS.  Parts come from memory at some
+// microseconds' latency, so eight are in flight at a time.
+template <int D>
+__device__ void join_parts(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int rows, int p0, int p1,
+                           float *lds)
+{
+    constexpr int kAhead = 8;
+    const int items = rows * (D / 4);
+    const int groups = items < kThreads ? kThreads / items : 1;
+    const int grp = items < kThreads ? threadIdx.x / items : 0;
+    for (int x0 = 0; x0 < items; x0 += kThreads) {
+        const int x = x0 + (items < kThreads ? threadIdx.x - grp * items : threadIdx.x);
+        const int row = x / (D / 4), d = x % (D / 4) * 4;
+        float R = -INFINITY, L = 0.0f;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (x < items && grp < groups) {
+            for (int p = p0 + grp; p <= p1; p += groups * kAhead) {
+                float2 rl[kAhead], u[kAhead], v[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int pp = min(p + i * groups, p1);
+                    const float *src = w.base + ((int64_t)pp * w.slot_rows + row) * (D + 2);
+                    rl[i] = load_shared(src + D);
+                    u[i] = load_shared(src + d);
+                    v[i] = load_shared(src + d + 2);
+                }
+                float top = R;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    rl[i].y = p + i * groups <= p1 ? rl[i].y : 0.0f;
+                    top = fmaxf(top, rl[i].y > 0.0f ? rl[i].x : -INFINITY);
+                }
+                const float keep = R == -INFINITY ? 0.0f : exp2_hw(R - top);
+                L *= keep;
+                sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const float f = rl[i].y > 0.0f ? exp2_hw(rl[i].x - top) : 0.0f;
+                    L = fmaf(rl[i].y, f, L);
+                    sum.x = fmaf(u[i].x, f, sum.x), sum.y = fmaf(u[i].y, f, sum.y);
+                    sum.z = fmaf(v[i].x, f, sum.z), sum.w = fmaf(v[i].y, f, sum.w);
+                }
+                R = top;
+            }
+        }
+        if (groups > 1) {
+            float *mine = lds + threadIdx.x * 6;
+            mine[0] = R, mine[1] = L, mine[2] = sum.x, mine[3] = sum.y, mine[4] = sum.z, mine[5] = sum.w;
+            __syncthreads();
+            if (grp == 0 && x < items) {
+                for (int g = 1; g < groups; ++g) {
+                    const float *o = lds + (g * items + x) * 6;
+                    const float top = fmaxf(R, o[0]);
+                    const float f0 = R == -INFINITY ? 0.0f : exp2_hw(R - top);
+                    const float f1 = o[0] == -INFINITY ? 0.0f : exp2_hw(o[0] - top);
+                    R = top;
+                    L = L * f0 + o[1] * f1;
+                    sum.x = sum.x * f0 + o[2] * f1, sum.y = sum.y * f0 + o[3] * f1;
+                    sum.z = sum.z * f0 + o[4] * f1, sum.w = sum.w * f0 + o[5] * f1;
+                }
+            }
+        }
+        if (grp == 0 && x < items)
+            store_row<D>(w, a, seq, head, row, d, sum, R, L);
     }
 }
 
 template <int D, int NG, int RT>
-__global__ __launch_bounds__(64 * kWaves, RT == 4 || RT * D == 512 ? 1 : 2) void kv4_decode_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
+__global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv4_decode_kernel(Kv4Cache c, Kv4AttnArgs a,
+                                                                                                 Partial w)
 {
     constexpr int N32 = D / 32, PER = N32 / NG;          // steps of 32 dims, of one group
+    constexpr int P = kPieces<D, RT>, KEYS = 16 * P;     // pieces and keys of a step
     constexpr int LD = D + 4;                            // LDS row: 16 rows of float4 without bank conflicts
     __shared__ float os[kWaves][16][LD];
     __shared__ float refs[kWaves][16 * RT], ls[kWaves][16 * RT];
@@ -114,254 +214,274 @@ __global__ __launch_bounds__(64 * kWaves, RT == 4 || RT * D == 512 ? 1 : 2) void
     const int r = lane & 15, b4 = lane >> 4;
     const int group = a.group, B = a.B;
 
-    // ---- this workgroup's units
-    const auto steps_of = [&](int b, Kv4Seq &s) {
-        s = kv4_sequence(a, c.shift, b);
-        return (int64_t)s.m * group > w.row_limit ? 0 : kv4_steps(s, a.causal, a.window).count;
-    };
-    int64_t total = 0;
-    for (int base = 0; base < B; base += 64) {
-        Kv4Seq s;
-        int64_t n = base + lane < B ? steps_of(base + lane, s) : 0;
-        for (int i = 32; i; i >>= 1)
-            n += __shfl_xor(n, i);
-        total += n;
-    }
-    total = uniform(total);
-    const int64_t U = total * c.heads;
-    if (U == 0)
-        return;
-    const int parts = kv4_parts(U, w.parts, w.least);
-    if ((int)blockIdx.x >= parts)
-        return;
-    int64_t u = kv4_part_begin(U, parts, blockIdx.x);
-    const int64_t u_end = kv4_part_begin(U, parts, blockIdx.x + 1);
-    // the sequence that holds unit u, and the units before it
-    int b = 0;
-    int64_t before = 0;                                  // steps of the sequences before b
-    for (int base = 0; base < B; base += 64) {
-        Kv4Seq s;
-        const int64_t n = base + lane < B ? steps_of(base + lane, s) : 0;
-        int64_t inc = n;
-        for (int i = 1; i < 64; i <<= 1) {
-            const int64_t up = __shfl_up(inc, i);
-            inc += lane >= i ? up : 0;
+    // ---- this workgroup's part: sequences 64 at a time, one a lane
+    Kv4Seq sl;                                           // sequence base + lane
+    int nl;                                              // and its steps
+    const auto lookup = [&](int base) {
+        nl = 0;
+        if (base + lane < B) {
+            sl = kv4_sequence(a, c.shift, base + lane);
+            if ((int64_t)sl.m * group <= w.row_limit)
+                nl = kv4_steps(sl, a.causal, a.window, KEYS).count;
         }
-        const int64_t here = __shfl(inc, 63);
-        if ((before + here) * c.heads > u) {
-            const int at = __ffsll((unsigned long long)__ballot((before + inc) * c.heads > u)) - 1;
-            before += __shfl(inc - n, at);
+    };
+    int64_t steps = 0;                                   // of all sequences
+    for (int base = 0; base < B; base += 64) {
+        lookup(base);
+        steps += group_sum_u32<64>((uint32_t)nl);
+    }
+    const int limit = kv4_part_limit(steps * c.heads, KEYS);
+    int b = -1, count = 0, parts = 0, id = blockIdx.x;   // id: within the sequences from b on
+    Kv4Seq seq = {0, 0, 0};
+    for (int base = 0; base < B; base += 64) {
+        if (B > 64)
+            lookup(base);
+        const int k = (nl + limit - 1) / limit;
+        const int inc = prefix_sum(k * c.heads);
+        const uint64_t past = __ballot(inc > id);
+        if (past) {
+            const int at = __builtin_ctzll(past);
             b = base + at;
+            count = __builtin_amdgcn_readlane(nl, at);
+            parts = __builtin_amdgcn_readlane(k, at);
+            seq.q0 = __builtin_amdgcn_readlane(sl.q0, at);
+            seq.m = __builtin_amdgcn_readlane(sl.m, at);
+            seq.n = __builtin_amdgcn_readlane(sl.n, at);
+            id -= __builtin_amdgcn_readlane(inc, at) - parts * c.heads;
             break;
         }
-        before += here;
+        id -= __builtin_amdgcn_readlane(inc, 63);
     }
-    before = uniform(before);
-    b = __builtin_amdgcn_readfirstlane(b);
+    if (b < 0)
+        return;
+    const int head = (uint32_t)id / (uint32_t)parts, part = id - head * parts;
+    const int rows = seq.m * group;
+    const int first = kv4_steps(seq, a.causal, a.window, KEYS).first;
+    const int64_t item = (int64_t)b * c.heads + head;
+    if (parts > 1 && threadIdx.x == 0)
+        announce(w.counters + item * kCounterStride, a.tag);
 
-    while (u < u_end) {
-        Kv4Seq seq;
-        const int count = (int)steps_of(b, seq);
-        if (count == 0) {
-            ++b;
-            continue;
-        }
-        const int64_t item0 = before * c.heads;          // the sequence's first unit
-        const int head = (int)((u - item0) / count), s0 = (int)((u - item0) % count);
-        const int64_t left = u_end - u;
-        const int s1 = left < count - s0 ? s0 + (int)left : count;
-        const Kv4Steps all = kv4_steps(seq, a.causal, a.window);
-        const int rows = seq.m * group;
+    // ---- this wave's steps (none where there are no keys) and its first loads
+    const int s0 = kv4_split(count, parts, part), s1 = kv4_split(count, parts, part + 1);
+    const int n = seq.n > 0 ? s1 - s0 : 0;
+    const int w0 = first + s0 + n * wave / kWaves, w1 = first + s0 + n * (wave + 1) / kWaves;
+    const int32_t *table = a.table + (int64_t)b * a.max_pages;
+    const int last_piece = (seq.n - 1) >> 4;
+    // the pages of a step's pieces of 16 keys (behind the last key the last page, where nothing is seen)
+    int page[P];
+    const auto pages_of = [&](int step) {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            page[p] = scalar_load(table + ((int64_t)min(step * P + p, last_piece) * 16 >> c.shift));
+    };
+    LaneAt at;
+    at.k = r * (D / 2) + b4 * (D / 8);
+    at.v = 4 * b4 * (D / 2) + r * N32;
+    at.odd = (r & 8) != 0;
+    at.scale = ((r & 4) ? reinterpret_cast<const char *>(c.vs) - reinterpret_cast<const char *>(c.ks) : 0) +
+               (4 * b4 + (r & 3)) * NG * 4;
+    const auto fetch = [&](Step<P, N32, NG> &s, int step) { load_step<P, D, NG>(s, c, head, page, step, at); };
+    Step<P, N32, NG> next;
+    if (w0 < w1) {
+        pages_of(w0);
+        fetch(next, w0);
+        pages_of(w0 + 1);
+    }
 
-        // ---- queries: row lane % 16 of each 16, visible keys [lo, hi)
-        h8 q[RT][N32];
-        int lo[RT], hi[RT];
-        float ref[RT], top[RT], l[RT];
-        v4f o[RT][2 * N32];
-        int lo_most = 0, hi_least = 0x7fffffff;
+    // ---- queries: row lane % 16 of each 16, visible keys [lo, hi)
+    h8 q[RT][N32];
+    int lo[RT], hi[RT];
+    float ref[RT], top[RT], l[RT];
+    v4f o[RT][2 * N32];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            const int row = 16 * t + r;
-            const int rc = row < rows ? row : rows - 1;  // rows past the last repeat it and are not stored
-            const int i = rc / group, hh = rc % group;
-            const uint16_t *qp = a.q + (int64_t)(seq.q0 + i) * a.q_stride + (int64_t)(head * group + hh) * D + 8 * b4;
+    for (int t = 0; t < RT; ++t) {
+        const int row = 16 * t + r;
+        const int rc = row < rows ? row : rows - 1;      // rows past the last repeat it and are not stored
+        const int i = (int)((uint32_t)rc * w.over_group >> 16), hh = rc - i * group;
+        const uint16_t *qp = a.q + (int64_t)(seq.q0 + i) * a.q_stride + (int64_t)(head * group + hh) * D + 8 * b4;
 #pragma unroll
-            for (int k = 0; k < N32; ++k)
-                q[t][k] = order8(*reinterpret_cast<const uint4 *>(qp + 32 * k));
-            lo[t] = kv4_lo(seq.n, seq.m, i, a.window);
-            hi[t] = kv4_hi(seq.n, seq.m, i, a.causal);
-            ref[t] = 0.0f;
-            top[t] = -INFINITY;
-            l[t] = 0.0f;
+        for (int k = 0; k < N32; ++k)
+            q[t][k] = order8(*reinterpret_cast<const uint4 *>(qp + 32 * k));
+        lo[t] = kv4_lo(seq.n, seq.m, i, a.window);
+        hi[t] = kv4_hi(seq.n, seq.m, i, a.causal);
+        ref[t] = 0.0f;
+        top[t] = -INFINITY;
+        l[t] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 2 * N32; ++k)
-                o[t][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        lo_most = kv4_lo(seq.n, seq.m, seq.m - 1, a.window);
-        hi_least = kv4_hi(seq.n, seq.m, 0, a.causal);
-        int scale_exp = kNoScale;
+        for (int k = 0; k < 2 * N32; ++k)
+            o[t][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    const int lo_most = kv4_lo(seq.n, seq.m, seq.m - 1, a.window), hi_least = kv4_hi(seq.n, seq.m, 0, a.causal);
+    int scale_exp = kNoScale;
+    const float score_scale = a.scale * kLog2e;
 
-        // ---- this wave's steps
-        const int n = s1 - s0;
-        const int w0 = all.first + s0 + n * wave / kWaves, w1 = all.first + s0 + n * (wave + 1) / kWaves;
-        const int32_t *table = a.table + (int64_t)b * a.max_pages;
-        const int last_page = seq.n > 0 ? (seq.n - 1) >> c.shift : -1;
-        // pages of 64 pieces of 16 keys from `piece0`, one a lane; -1 past the last key
-        int piece0 = 2 * w0;
-        const auto pages_from = [&](int piece) {
-            const int p = (int)(((int64_t)(piece + lane) * 16) >> c.shift);
-            return p <= last_page ? table[p] : -1;
-        };
-        int pages = w0 < w1 ? pages_from(piece0) : -1;
-        const auto fetch = [&](Step<N32, NG> &s, int step) {
-            if (2 * step - piece0 >= 64) {
-                piece0 = 2 * step;
-                pages = pages_from(piece0);
+    const auto compute = [&](const Step<P, N32, NG> &cur, int step) {
+        const int t0 = step * KEYS;
+        float sc[P / 2][NG], ksc[P / 2][NG];
+#pragma unroll
+        for (int h = 0; h < P / 2; ++h)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                sc[h][g] = cur.sc[h][g];
+                ksc[h][g] = cur.sc[h][g] * score_scale;
             }
-            load_step<D, NG>(s, c, head, __builtin_amdgcn_readlane(pages, 2 * step - piece0),
-                             __builtin_amdgcn_readlane(pages, 2 * step - piece0 + 1), step, lane);
-        };
-        Step<N32, NG> next;
-        if (w0 < w1)
-            fetch(next, w0);
-        for (int step = w0; step < w1; ++step) {
-            Step<N32, NG> cur = next;
-            if (step + 1 < w1)
-                fetch(next, step + 1);
-            const int t0 = step * 32;
-            // scores
-            float ksc[NG];
+        // scores
+        float s[RT][P][4];
+        each<P>([&](auto pc) {
+            constexpr int p = decltype(pc)::value;
+            each<NG>([&](auto gc) {
+                constexpr int g = decltype(gc)::value;
+                v4f acc[RT];
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
-                ksc[g] = cur.sc[g] * (a.scale * kLog2e);
-            float s[RT][2][4];
-            each<2>([&](auto pc) {
-                constexpr int p = decltype(pc)::value;
-                each<NG>([&](auto gc) {
-                    constexpr int g = decltype(gc)::value;
-                    v4f acc[RT];
+                for (int t = 0; t < RT; ++t)
+                    acc[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = g * PER; k < (g + 1) * PER; ++k) {
+                    const h8 kk = codes8(cur.k[p][k]);
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
-                        acc[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, q[t][k], acc[t], 0, 0, 0);
+                }
+                each<4>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    const float f = row_lane<8 * (p % 2) + j>(ksc[p / 2][g]);
 #pragma unroll
-                    for (int k = g * PER; k < (g + 1) * PER; ++k) {
-                        const h8 kk = codes8(cur.k[p][k]);
-#pragma unroll
-                        for (int t = 0; t < RT; ++t)
-                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, q[t][k], acc[t], 0, 0, 0);
-                    }
-                    each<4>([&](auto jc) {
-                        constexpr int j = decltype(jc)::value;
-                        const float f = row_lane<8 * p + j>(ksc[g]);
-#pragma unroll
-                        for (int t = 0; t < RT; ++t)
-                            s[t][p][j] = g == 0 ? acc[t][j] * f : fmaf(acc[t][j], f, s[t][p][j]);
-                    });
+                    for (int t = 0; t < RT; ++t)
+                        s[t][p][j] = g == 0 ? acc[t][j] * f : fmaf(acc[t][j], f, s[t][p][j]);
                 });
             });
-            // a step that not every row sees whole: hide keys, and what garbage stands for them
-            if (!cur.ok[0] || !cur.ok[1] || t0 < lo_most || t0 > hi_least - 32) {
+        });
+        // a step that not every row sees whole: hide keys, and what garbage stands for them
+        if (cur.ok != (1u << P) - 1 || t0 < lo_most || t0 > hi_least - KEYS) {
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < P; ++p) {
+                const bool page_ok = (cur.ok >> p) & 1;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int key = t0 + 16 * p + 4 * b4 + j;
-                        const bool there = cur.ok[p] && key < seq.n;
+                for (int j = 0; j < 4; ++j) {
+                    const int key = t0 + 16 * p + 4 * b4 + j;
+                    const bool there = page_ok && key < seq.n;
 #pragma unroll
-                        for (int t = 0; t < RT; ++t)
-                            s[t][p][j] = there && key >= lo[t] && key < hi[t] ? s[t][p][j] : -INFINITY;
-                    }
+                    for (int t = 0; t < RT; ++t)
+                        s[t][p][j] = there && key >= lo[t] && key < hi[t] ? s[t][p][j] : -INFINITY;
                 }
-                const int mine = t0 + 2 * (r & 8) + 4 * b4 + (r & 3);
-                const bool there = ((r & 8) ? cur.ok[1] : cur.ok[0]) && mine < seq.n;
+            }
+#pragma unroll
+            for (int h = 0; h < P / 2; ++h) {
+                const int mine = t0 + 32 * h + 2 * (r & 8) + 4 * b4 + (r & 3);
+                const bool there = (cur.ok >> (2 * h + (r >> 3)) & 1) && mine < seq.n;
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
-                    cur.sc[g] = there ? cur.sc[g] : 0.0f;
+                    sc[h][g] = there ? sc[h][g] : 0.0f;
             }
-            // the largest value scale so far
-            float big = cur.sc[0];
+        }
+        // the largest value scale so far
+        uint32_t big = 0;
 #pragma unroll
-            for (int g = 1; g < NG; ++g)
-                big = fmaxf(big, cur.sc[g]);
-            big = (r & 4) ? big : 0.0f;
-            big = max_rows(__uint_as_float(group_max_u32<16>(__float_as_uint(big))));
-            scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
-            const float shift = (float)(scale_exp - kHeadroom);
-            h8 wt[RT][NG];
+        for (int h = 0; h < P / 2; ++h)
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                float m = fmaxf(fmaxf(fmaxf(s[t][0][0], s[t][0][1]), fmaxf(s[t][0][2], s[t][0][3])),
-                                fmaxf(fmaxf(s[t][1][0], s[t][1][1]), fmaxf(s[t][1][2], s[t][1][3])));
-                m = fmaxf(top[t], max_rows(m));
-                const float nref = (m == -INFINITY ? 0.0f : m) + shift;
-                if (__ballot(nref != ref[t])) {          // rare after the first steps
-                    const float alpha = top[t] == -INFINITY ? 0.0f : exp2_hw(ref[t] - nref);
-                    l[t] *= alpha;
+            for (int g = 0; g < NG; ++g)
+                big = max(big, __float_as_uint(sc[h][g]));
+        big = max_rows_u32(group_max_u32<16>((r & 4) ? big : 0u));
+        scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
+        const float shift = (float)(scale_exp - kHeadroom);
+        h8 wt[RT][P / 2][NG];
 #pragma unroll
-                    for (int k = 0; k < 2 * N32; ++k)
+        for (int t = 0; t < RT; ++t) {
+            float m = max3(s[t][0][0], s[t][0][1], s[t][0][2]);
+            m = max3(m, s[t][0][3], s[t][1][0]);
+            m = max3(m, s[t][1][1], s[t][1][2]);
+            if constexpr (P == 2) {
+                m = max3(m, s[t][1][3], s[t][1][3]);
+            } else {
+                m = max3(m, s[t][1][3], s[t][2][0]);
+                m = max3(m, s[t][2][1], s[t][2][2]);
+                m = max3(m, s[t][2][3], s[t][3][0]);
+                m = max3(m, s[t][3][1], s[t][3][2]);
+                m = max3(m, s[t][3][3], s[t][3][3]);
+            }
+            m = max_rows(m, top[t]);
+            const float nref = (m == -INFINITY ? 0.0f : m) + shift;
+            if (__ballot(nref != ref[t])) {              // rare after the first steps
+                const float alpha = top[t] == -INFINITY ? 0.0f : exp2_hw(ref[t] - nref);
+                l[t] *= alpha;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[t][k][e] *= alpha;
-                    ref[t] = nref;
-                }
-                top[t] = m;
+                for (int k = 0; k < 2 * N32; ++k)
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
+                    for (int e = 0; e < 4; ++e)
+                        o[t][k][e] *= alpha;
+                ref[t] = nref;
+            }
+            top[t] = m;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        s[t][p][j] = exp2_hw(s[t][p][j] - nref);
-                        l[t] += s[t][p][j];
-                    }
-                // weight times the value's scale, the one rounding to fp16
+            for (int p = 0; p < P; ++p) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[t][p][j] = exp2_hw(s[t][p][j] - nref);
+                l[t] += (s[t][p][0] + s[t][p][1]) + (s[t][p][2] + s[t][p][3]);
+            }
+            // weight times the value's scale, the one rounding to fp16
+            each<P / 2>([&](auto hc) {
+                constexpr int h = decltype(hc)::value;
                 each<NG>([&](auto gc) {
                     constexpr int g = decltype(gc)::value;
                     u32x4 x;
                     each<4>([&](auto ic) {
-                        constexpr int p = decltype(ic)::value / 2, j = decltype(ic)::value % 2 * 2;
-                        x[2 * p + j / 2] = pack_h2(s[t][p][j] * row_lane<8 * p + 4 + j>(cur.sc[g]),
-                                                   s[t][p][j + 1] * row_lane<8 * p + 5 + j>(cur.sc[g]));
+                        constexpr int x2 = decltype(ic)::value / 2, j = decltype(ic)::value % 2 * 2;
+                        x[decltype(ic)::value] = pack_h2(s[t][2 * h + x2][j] * row_lane<8 * x2 + 4 + j>(sc[h][g]),
+                                                         s[t][2 * h + x2][j + 1] * row_lane<8 * x2 + 5 + j>(sc[h][g]));
                     });
-                    wt[t][g] = __builtin_bit_cast(h8, x);
+                    wt[t][h][g] = __builtin_bit_cast(h8, x);
                 });
-            }
-            // O^T += V^T P^T: 16 rows 32 g + 2 r + e of the values for byte g's two nibbles e
+            });
+        }
+        // O^T += V^T P^T: 16 rows 32 g + 2 r + e of the values for byte g's two nibbles e
+        each<P / 2>([&](auto hc) {
+            constexpr int h = decltype(hc)::value;
             each<N32>([&](auto gc) {
                 constexpr int g = decltype(gc)::value;
-                const uint32_t x0 = byte_pair<g % 4>(cur.v[0][0][g / 4], cur.v[0][1][g / 4]);
-                const uint32_t x1 = byte_pair<g % 4>(cur.v[0][2][g / 4], cur.v[0][3][g / 4]);
-                const uint32_t x2 = byte_pair<g % 4>(cur.v[1][0][g / 4], cur.v[1][1][g / 4]);
-                const uint32_t x3 = byte_pair<g % 4>(cur.v[1][2][g / 4], cur.v[1][3][g / 4]);
+                const auto &v0 = cur.v[2 * h], &v1 = cur.v[2 * h + 1];
+                const uint32_t x0 = byte_pair<g % 4>(v0[0][g / 4], v0[1][g / 4]), x1 = byte_pair<g % 4>(v0[2][g / 4], v0[3][g / 4]);
+                const uint32_t x2 = byte_pair<g % 4>(v1[0][g / 4], v1[1][g / 4]), x3 = byte_pair<g % 4>(v1[2][g / 4], v1[3][g / 4]);
                 const u32x4 e0 = {codes_low(x0), codes_low(x1), codes_low(x2), codes_low(x3)};
                 const u32x4 e1 = {codes_high(x0), codes_high(x1), codes_high(x2), codes_high(x3)};
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    o[t][2 * g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, e0), wt[t][g / PER],
-                                                                         o[t][2 * g], 0, 0, 0);
-                    o[t][2 * g + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, e1), wt[t][g / PER],
-                                                                             o[t][2 * g + 1], 0, 0, 0);
+                    const h8 x = wt[t][h][g / PER];
+                    o[t][2 * g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, e0), x, o[t][2 * g], 0, 0, 0);
+                    o[t][2 * g + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, e1), x, o[t][2 * g + 1], 0, 0, 0);
                 }
             });
+        });
+    };
+    // The next step's loads are in flight during one, its pages (scalar loads)
+    // are a step further ahead; other waves hide the rest.  The step stands in
+    // the code once: a short call is bound by fetching instructions, and with
+    // two steps ahead in five copies it took as long.
+    for (int step = w0; step < w1; ++step) {
+        const Step<P, N32, NG> cur = next;
+        if (step + 1 < w1) {
+            fetch(next, step + 1);
+            pages_of(step + 2);
         }
+        compute(cur, step);
+    }
 
-        // ---- join the four waves
+    // ---- join the four waves
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            l[t] = sum_rows(l[t]);
-            if (lane < 16) {
-                refs[wave][16 * t + r] = l[t] > 0.0f ? ref[t] : -INFINITY;
-                ls[wave][16 * t + r] = l[t];
-            }
+    for (int t = 0; t < RT; ++t) {
+        l[t] = sum_rows(l[t]);
+        if (lane < 16) {
+            refs[wave][16 * t + r] = l[t] > 0.0f ? ref[t] : -INFINITY;
+            ls[wave][16 * t + r] = l[t];
         }
-        __syncthreads();
-        const bool whole = s0 == 0 && s1 == count;
-        const int64_t item = (int64_t)b * c.heads + head;
-        const int64_t first_unit = item0 + (int64_t)head * count;
-        // a part that does not begin its item is its workgroup's first
-        float *slot = w.base + (int64_t)(2 * blockIdx.x + (s0 == 0 ? 1 : 0)) * w.slot_rows * (D + 2);
+    }
+    lds_barrier();
+    float *slot = w.base + (int64_t)blockIdx.x * w.slot_rows * (D + 2);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            if (16 * t >= rows)
-                break;
+    for (int t = 0; t < RT; ++t) {
+        if (16 * t >= rows)
+            break;
+        if (16 * t + r < rows) {
             float R = -INFINITY;
 #pragma unroll
             for (int x = 0; x < kWaves; ++x)
@@ -370,101 +490,58 @@ __global__ __launch_bounds__(64 * kWaves, RT == 4 || RT * D == 512 ? 1 : 2) void
 #pragma unroll
             for (int g = 0; g < N32; ++g) {
                 // lane: dims 32 g + 8 b4 + 2 reg + e
-                float4 x, y;
-                x.x = o[t][2 * g][0] * f, x.y = o[t][2 * g + 1][0] * f, x.z = o[t][2 * g][1] * f, x.w = o[t][2 * g + 1][1] * f;
-                y.x = o[t][2 * g][2] * f, y.y = o[t][2 * g + 1][2] * f, y.z = o[t][2 * g][3] * f, y.w = o[t][2 * g + 1][3] * f;
                 float4 *dst = reinterpret_cast<float4 *>(&os[wave][r][32 * g + 8 * b4]);
-                dst[0] = x;
-                dst[1] = y;
+                dst[0] = make_float4(o[t][2 * g][0] * f, o[t][2 * g + 1][0] * f, o[t][2 * g][1] * f, o[t][2 * g + 1][1] * f);
+                dst[1] = make_float4(o[t][2 * g][2] * f, o[t][2 * g + 1][2] * f, o[t][2 * g][3] * f, o[t][2 * g + 1][3] * f);
             }
-            __syncthreads();
-            // a thread: four dims of a row at a time
-            for (int x = threadIdx.x; x < 16 * (D / 4); x += 64 * kWaves) {
-                const int rr = x / (D / 4), d = x % (D / 4) * 4, row = 16 * t + rr;
-                if (row >= rows)
-                    continue;
-                float RR = -INFINITY, L = 0.0f;
+        }
+        lds_barrier();
+        // a thread: four dims of a row at a time
+        const int items = (rows - 16 * t < 16 ? rows - 16 * t : 16) * (D / 4);
+        for (int x = threadIdx.x; x < items; x += kThreads) {
+            const int rr = x / (D / 4), d = x % (D / 4) * 4, row = 16 * t + rr;
+            float RR = -INFINITY, L = 0.0f;
 #pragma unroll
-                for (int y = 0; y < kWaves; ++y)
-                    RR = fmaxf(RR, refs[y][row]);
+            for (int y = 0; y < kWaves; ++y)
+                RR = fmaxf(RR, refs[y][row]);
 #pragma unroll
-                for (int y = 0; y < kWaves; ++y)
-                    L += ls[y][row] > 0.0f ? ls[y][row] * exp2_hw(refs[y][row] - RR) : 0.0f;
-                float4 sum = *reinterpret_cast<const float4 *>(&os[0][rr][d]);
+            for (int y = 0; y < kWaves; ++y)
+                L += ls[y][row] > 0.0f ? ls[y][row] * exp2_hw(refs[y][row] - RR) : 0.0f;
+            float4 sum = *reinterpret_cast<const float4 *>(&os[0][rr][d]);
 #pragma unroll
-                for (int y = 1; y < kWaves; ++y) {
-                    const float4 v = *reinterpret_cast<const float4 *>(&os[y][rr][d]);
-                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-                }
-                if (whole) {
-                    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-                    const int64_t at = (int64_t)(seq.q0 + row / group) * a.q_heads + head * group + row % group;
-                    *reinterpret_cast<uint2 *>(a.out + at * D + d) =
-                        make_uint2(pack_h2(sum.x * inv, sum.y * inv), pack_h2(sum.z * inv, sum.w * inv));
-                    if (a.lse && d == 0)
-                        a.lse[at] = L > 0.0f ? (RR + __builtin_amdgcn_logf(L)) * kLn2 : -INFINITY;
-                } else {
-                    float *dst = slot + (int64_t)row * (D + 2);
-                    store_shared(dst + d, sum.x, sum.y);
-                    store_shared(dst + d + 2, sum.z, sum.w);
-                    if (d == 0)
-                        store_shared(dst + D, RR, L);
-                }
+            for (int y = 1; y < kWaves; ++y) {
+                const float4 v = *reinterpret_cast<const float4 *>(&os[y][rr][d]);
+                sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
             }
-            __syncthreads();
-        }
-        if (!whole) {
-            // ---- join the workgroups: the last to arrive reads all parts in order
-            const int64_t last_unit = first_unit + count - 1;
-            const int p0 = kv4_part_of(U, parts, first_unit), p1 = kv4_part_of(U, parts, last_unit);
-            __builtin_amdgcn_s_waitcnt(0);               // this wave's parts are stored
-            __syncthreads();
-            if (threadIdx.x == 0)
-                last = arrive_last(w.counters + item, a.tag, p1 - p0 + 1) ? 1 : 0;
-            __syncthreads();
-            if (last) {
-                for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * kWaves) {
-                    const int row = x / (D / 4), d = x % (D / 4) * 4;
-                    const auto part = [&](int p) {
-                        const int second = p == p0 ? 1 : 0;
-                        return w.base + ((int64_t)(2 * p + second) * w.slot_rows + row) * (D + 2);
-                    };
-                    float RR = -INFINITY;
-                    for (int p = p0; p <= p1; ++p) {
-                        const float2 x2 = load_shared(part(p) + D);
-                        RR = fmaxf(RR, x2.y > 0.0f ? x2.x : -INFINITY);
-                    }
-                    float L = 0.0f;
-                    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int p = p0; p <= p1; ++p) {
-                        const float2 rl = load_shared(part(p) + D), x0 = load_shared(part(p) + d), x1 = load_shared(part(p) + d + 2);
-                        const float f = rl.y > 0.0f ? exp2_hw(rl.x - RR) : 0.0f;
-                        L = fmaf(rl.y, f, L);
-                        sum.x = fmaf(x0.x, f, sum.x), sum.y = fmaf(x0.y, f, sum.y);
-                        sum.z = fmaf(x1.x, f, sum.z), sum.w = fmaf(x1.y, f, sum.w);
-                    }
-                    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-                    const int64_t at = (int64_t)(seq.q0 + row / group) * a.q_heads + head * group + row % group;
-                    *reinterpret_cast<uint2 *>(a.out + at * D + d) =
-                        make_uint2(pack_h2(sum.x * inv, sum.y * inv), pack_h2(sum.z * inv, sum.w * inv));
-                    if (a.lse && d == 0)
-                        a.lse[at] = L > 0.0f ? (RR + __builtin_amdgcn_logf(L)) * kLn2 : -INFINITY;
-                }
+            if (parts == 1) {
+                store_row<D>(w, a, seq, head, row, d, sum, RR, L);
+            } else {
+                float *dst = slot + row * (D + 2);
+                store_shared(dst + d, sum.x, sum.y);
+                store_shared(dst + d + 2, sum.z, sum.w);
+                if (d == 0)
+                    store_shared(dst + D, RR, L);
             }
-            __syncthreads();                             // `last` is read before it is written again
         }
-        u += s1 - s0;
-        if (u == item0 + (int64_t)c.heads * count) {
-            before += count;
-            ++b;
-        }
+        if (RT > 1)
+            lds_barrier();
+    }
+    if (parts > 1) {
+        // ---- join the workgroups: the last to arrive reads all parts in order
+        __builtin_amdgcn_s_waitcnt(0);                   // this wave's stores are complete
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = arrive(w.counters + item * kCounterStride, parts) ? 1 : 0;
+        __syncthreads();
+        if (last)
+            join_parts<D>(w, a, seq, head, rows, blockIdx.x - part, blockIdx.x - part + parts - 1, &os[0][0][0]);
     }
 }
 
 template <int D, int NG>
 void launch(const Kv4Cache &c, const Kv4AttnArgs &a, const Partial &w, int rows, hipStream_t st)
 {
-    const dim3 grid((unsigned)w.parts), block(64 * kWaves);
+    const dim3 grid((unsigned)w.grid), block(kThreads);
     if (rows <= 16)
         hipLaunchKernelGGL((kv4_decode_kernel<D, NG, 1>), grid, block, 0, st, c, a, w);
     else if (rows <= 32)
@@ -478,10 +555,10 @@ void launch(const Kv4Cache &c, const Kv4AttnArgs &a, const Partial &w, int rows,
 void launch_kv4_decode(const Kv4Cache &c, const Kv4AttnArgs &a, int rows, hipStream_t st)
 {
     Partial w;
-    w.parts = kDecodeParts;
-    w.least = 16;
+    w.grid = (int)kv4_decode_grid(a.B, c.heads, (int64_t)a.max_pages << c.shift);
     w.row_limit = rows;
     w.slot_rows = rows;
+    w.over_group = (65536 + a.group - 1) / a.group;
     w.counters = static_cast<uint64_t *>(a.workspace);
     w.base = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kv4_counter_bytes(a.B, c.heads));
     switch (c.D * 8 + c.D / c.G) {

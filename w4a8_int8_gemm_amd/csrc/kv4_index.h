@@ -50,35 +50,40 @@ KV4_HD int kv4_lo(int n, int m, int i, int window)
     return lo < 0 ? 0 : lo;
 }
 
-// Steps of 32 keys that a sequence's queries need together; one (empty) step
-// where they see nothing, none without queries.
+// Steps of `keys` keys that a sequence's queries need together; one (empty)
+// step where they see nothing, none without queries.
 struct Kv4Steps {
     int first, count;
 };
-KV4_HD Kv4Steps kv4_steps(const Kv4Seq &s, bool causal, int window)
+KV4_HD Kv4Steps kv4_steps(const Kv4Seq &s, bool causal, int window, int keys)
 {
     Kv4Steps r = {0, 0};
     if (s.m == 0)
         return r;
     const int hi = kv4_hi(s.n, s.m, s.m - 1, causal), lo = kv4_lo(s.n, s.m, 0, window);
-    r.first = lo / 32;
-    r.count = (int)(((int64_t)hi + 31) / 32) - r.first;
+    r.first = lo / keys;
+    r.count = (int)(((int64_t)hi + keys - 1) / keys) - r.first;
     r.count = r.count < 1 ? 1 : r.count;
     return r;
 }
 
-// U units in `parts` contiguous parts: the first unit of part i, and the part
-// that holds unit u.
-KV4_HD int64_t kv4_part_begin(int64_t U, int parts, int64_t i) { return U * i / parts; }
-KV4_HD int kv4_part_of(int64_t U, int parts, int64_t u)
+// A (sequence, head) of `count` steps is cut into ceil(count / limit) even
+// parts.  With the limit below there are at most kPartsMore more of them in
+// all than (sequence, head) pairs, for `total` steps of all pairs: two
+// workgroups a compute unit where one sequence has them all, and no part of
+// under kLeastKeys keys is made.
+constexpr int kPartsMore = 512, kLeastKeys = 1024;
+KV4_HD int kv4_part_limit(int64_t total, int keys)
 {
-    return (int)(((u + 1) * parts - 1) / U);
+    const int64_t l = (total + kPartsMore - 1) / kPartsMore, least = kLeastKeys / keys;
+    return l < least ? (int)least : l > 0x3fffffff ? 0x3fffffff : (int)l;
 }
-// Parts used for U units: all of them only where each gets `least` units.
-KV4_HD int kv4_parts(int64_t U, int parts, int least)
+KV4_HD int kv4_split(int count, int parts, int i) { return (int)((int64_t)count * i / parts); }
+// Workgroups for all parts of any lengths up to `most` keys a sequence.
+KV4_HD int64_t kv4_decode_grid(int64_t B, int heads, int64_t most)
 {
-    const int64_t p = (U + least - 1) / least;
-    return p < parts ? (int)p : parts;
+    const int64_t pairs = B * heads, each = most / kLeastKeys + 1;
+    return pairs * (each - 1) < kPartsMore ? pairs * each : pairs + kPartsMore;
 }
 
 // Where a page's 16-token piece lies, and whether the table's entry names a page at all.
