@@ -62,6 +62,8 @@ inline int kv4_decode_limit(int D) { return D < 256 ? 64 : 32; }
 constexpr int kCounterStride = 16;
 inline size_t kv4_counter_bytes(int64_t B, int heads) { return ((size_t)B * heads * kCounterStride * 8 + 255) & ~size_t(255); }
 void launch_kv4_decode(const Kv4Cache &c, const Kv4AttnArgs &a, int rows, hipStream_t st);
+// The other sequences, those with more than row_limit rows a kv head.
+void launch_kv4_prefill(const Kv4Cache &c, const Kv4AttnArgs &a, int row_limit, void *workspace, hipStream_t st);
 
 // Sequence b of the call.
 __device__ __forceinline__ Kv4Seq kv4_sequence(const Kv4AttnArgs &a, int shift, int b)

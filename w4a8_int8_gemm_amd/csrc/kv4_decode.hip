@@ -28,16 +28,6 @@ namespace w4a8 {
 
 namespace {
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
-
-struct Partial {
-    float *base;                // [grid][slot_rows][D + 2]
-    int slot_rows;
-    uint64_t *counters;         // [B * heads][kCounterStride]
-    int grid;
-    int row_limit;              // sequences with more rows are left to the other kernel
-    uint32_t over_group;        // ceil(2^16 / group): row / group of rows < 64, group <= 64
-};
 
 // Pieces of 16 keys in a step: more of them share the softmax's bookkeeping,
 // where the registers hold them.
@@ -114,89 +104,6 @@ __device__ __forceinline__ void load_step(Step<P, D / 32, NG> &s, const Kv4Cache
             for (int e = 0; e < 4; ++e)
                 s.sc[p / 2][e] = w[e];
         }
-    }
-}
-
-// A row's output and log of the softmax sum from its joined part.
-template <int D>
-__device__ __forceinline__ void store_row(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int row,
-                                          int d, float4 sum, float ref, float l)
-{
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int i = (int)((uint32_t)row * w.over_group >> 16);
-    const int64_t at = (int64_t)(seq.q0 + i) * a.q_heads + head * a.group + (row - i * a.group);
-    *reinterpret_cast<uint2 *>(a.out + at * D + d) =
-        make_uint2(pack_h2(sum.x * inv, sum.y * inv), pack_h2(sum.z * inv, sum.w * inv));
-    if (a.lse && d == 0)
-        a.lse[at] = l > 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-}
-
-// Joins the parts p0 .. p1 (workgroups) of an item.  A thread takes four dims
-// of a row; where there are more threads, groups of them take every
-// so-many-th part and are joined in LDS.  Parts come from memory at some
-// microseconds' latency, so eight are in flight at a time.
-template <int D>
-__device__ void join_parts(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int rows, int p0, int p1,
-                           float *lds)
-{
-    constexpr int kAhead = 8;
-    const int items = rows * (D / 4);
-    const int groups = items < kThreads ? kThreads / items : 1;
-    const int grp = items < kThreads ? threadIdx.x / items : 0;
-    for (int x0 = 0; x0 < items; x0 += kThreads) {
-        const int x = x0 + (items < kThreads ? threadIdx.x - grp * items : threadIdx.x);
-        const int row = x / (D / 4), d = x % (D / 4) * 4;
-        float R = -INFINITY, L = 0.0f;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (x < items && grp < groups) {
-            for (int p = p0 + grp; p <= p1; p += groups * kAhead) {
-                float2 rl[kAhead], u[kAhead], v[kAhead];
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const int pp = min(p + i * groups, p1);
-                    const float *src = w.base + ((int64_t)pp * w.slot_rows + row) * (D + 2);
-                    rl[i] = load_shared(src + D);
-                    u[i] = load_shared(src + d);
-                    v[i] = load_shared(src + d + 2);
-                }
-                float top = R;
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    rl[i].y = p + i * groups <= p1 ? rl[i].y : 0.0f;
-                    top = fmaxf(top, rl[i].y > 0.0f ? rl[i].x : -INFINITY);
-                }
-                const float keep = R == -INFINITY ? 0.0f : exp2_hw(R - top);
-                L *= keep;
-                sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const float f = rl[i].y > 0.0f ? exp2_hw(rl[i].x - top) : 0.0f;
-                    L = fmaf(rl[i].y, f, L);
-                    sum.x = fmaf(u[i].x, f, sum.x), sum.y = fmaf(u[i].y, f, sum.y);
-                    sum.z = fmaf(v[i].x, f, sum.z), sum.w = fmaf(v[i].y, f, sum.w);
-                }
-                R = top;
-            }
-        }
-        if (groups > 1) {
-            float *mine = lds + threadIdx.x * 6;
-            mine[0] = R, mine[1] = L, mine[2] = sum.x, mine[3] = sum.y, mine[4] = sum.z, mine[5] = sum.w;
-            __syncthreads();
-            if (grp == 0 && x < items) {
-                for (int g = 1; g < groups; ++g) {
-                    const float *o = lds + (g * items + x) * 6;
-                    const float top = fmaxf(R, o[0]);
-                    const float f0 = R == -INFINITY ? 0.0f : exp2_hw(R - top);
-                    const float f1 = o[0] == -INFINITY ? 0.0f : exp2_hw(o[0] - top);
-                    R = top;
-                    L = L * f0 + o[1] * f1;
-                    sum.x = sum.x * f0 + o[2] * f1, sum.y = sum.y * f0 + o[3] * f1;
-                    sum.z = sum.z * f0 + o[4] * f1, sum.w = sum.w * f0 + o[5] * f1;
-                }
-            }
-        }
-        if (grp == 0 && x < items)
-            store_row<D>(w, a, seq, head, row, d, sum, R, L);
     }
 }
 
@@ -297,7 +204,7 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
     for (int t = 0; t < RT; ++t) {
         const int row = 16 * t + r;
         const int rc = row < rows ? row : rows - 1;      // rows past the last repeat it and are not stored
-        const int i = (int)((uint32_t)rc * w.over_group >> 16), hh = rc - i * group;
+        const int i = query_of(rc, w.over_group, group), hh = rc - i * group;
         const uint16_t *qp = a.q + (int64_t)(seq.q0 + i) * a.q_stride + (int64_t)(head * group + hh) * D + 8 * b4;
 #pragma unroll
         for (int k = 0; k < N32; ++k)
@@ -534,7 +441,7 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
             last = arrive(w.counters + item * kCounterStride, parts) ? 1 : 0;
         __syncthreads();
         if (last)
-            join_parts<D>(w, a, seq, head, rows, blockIdx.x - part, blockIdx.x - part + parts - 1, &os[0][0][0]);
+            join_parts<D>(w, a, seq, head, 0, rows, blockIdx.x - part, parts, &os[0][0][0]);
     }
 }
 
@@ -557,8 +464,9 @@ void launch_kv4_decode(const Kv4Cache &c, const Kv4AttnArgs &a, int rows, hipStr
     Partial w;
     w.grid = (int)kv4_decode_grid(a.B, c.heads, (int64_t)a.max_pages << c.shift);
     w.row_limit = rows;
+    w.slots = w.grid;
     w.slot_rows = rows;
-    w.over_group = (65536 + a.group - 1) / a.group;
+    w.over_group = over_group(a.group);
     w.counters = static_cast<uint64_t *>(a.workspace);
     w.base = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + kv4_counter_bytes(a.B, c.heads));
     switch (c.D * 8 + c.D / c.G) {

@@ -1,0 +1,433 @@
+// Attention of many query rows over the 4-bit cache (include/w4a8.h:
+// kv4_attention): sequences with more rows a kv head than the kernel for few
+// rows takes.
+//
+// What bounds it: the vector unit.  A tile of 64 keys and 32 rows a wave takes
+// 1024 cycles of the matrix unit, and the scores' scaling, maximum, exponential,
+// sum, weight and rounding some 300 vector operations at 4 cycles each, plus
+// the wave's share of turning codes into fp16.
+//
+// A workgroup has 128 rows (queries x query heads of one kv head), 32 a wave,
+// and walks over its keys in tiles of 64.  Two of its waves turn the tile's V
+// and two its K into fp16 in LDS (exact codes; the scales stay apart in fp32),
+// while the next tile's codes are on their way.  S^T = K Q^T on 32x32x16
+// matrix instructions leaves a lane with one query row and runs of four keys,
+// which is the operand of O^T = V^T P^T if V^T's keys lie in that order: they
+// do, eight keys of two such runs in one 16-byte piece.  Rows of both tiles
+// are swizzled so that 16 lanes' pieces cover all banks.
+//
+// Where the rows alone do not fill the chip a (sequence, head, rows) tile's
+// keys are cut into parts of equal width, joined as in the kernel for few rows.
+#include "kv4_device.hpp"
+#include "lds_copy.hpp"
+
+namespace w4a8 {
+
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+constexpr int kRows = 128, kKeys = 64;
+
+// Piece `c` of 16 bytes in a row of N pieces, moved so that the same piece of 16
+// consecutive rows (of N / 2 pairs of rows where a row is half the banks) is
+// on different banks.
+template <int N> __device__ __forceinline__ int swizzle(int row, int c)
+{
+    return N >= 16 ? c ^ (row & 15) : c ^ ((row >> 1) & 7);
+}
+
+template <int D, int NG>
+__global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
+{
+    constexpr int N32 = D / 32, PER = N32 / NG, KC = D / 8, VC = kKeys / 8;
+    __shared__ u32x4 kt[2][kKeys][KC];                   // fp16 codes [key][dim], pieces of 8 dims
+    __shared__ u32x4 vt[2][D][VC];                       // fp16 codes [dim][key], pieces of 8 keys
+    __shared__ float ksc[2][NG][kKeys], vsc[2][NG][kKeys];
+    __shared__ int last;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = a.group, B = a.B;
+
+    // ---- this workgroup's tile of rows and part of the keys, as in the kernel
+    // for few rows; the parts of a sequence's tiles are cut at the same keys
+    Kv4Seq sl;
+    int tl = 0, nl = 0;                                  // tiles of rows, steps of keys
+    const auto lookup = [&](int base) {
+        tl = nl = 0;
+        if (base + lane < B) {
+            sl = kv4_sequence(a, c.shift, base + lane);
+            const int64_t rows = (int64_t)sl.m * group;
+            if (rows > w.row_limit) {
+                tl = (int)((rows + kRows - 1) / kRows);
+                nl = kv4_steps(sl, a.causal, a.window, kKeys).count;
+            }
+        }
+    };
+    int64_t steps = 0;
+    for (int base = 0; base < B; base += 64) {
+        lookup(base);
+        steps += wave_sum64((int64_t)tl * nl);
+    }
+    const int limit = kv4_tile_limit(steps * c.heads, kKeys);
+    int b = -1, tiles = 0, cuts = 0, count = 0, id = blockIdx.x, split = 0;   // split: slots before b's
+    Kv4Seq seq = {0, 0, 0};
+    for (int base = 0; base < B; base += 64) {
+        if (B > 64)
+            lookup(base);
+        const int k = tl ? (nl + limit - 1) / limit : 0;
+        const int inc = prefix_sum(tl * k * c.heads), sinc = prefix_sum(k > 1 ? tl * k * c.heads : 0);
+        const uint64_t past = __ballot(inc > id);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            b = base + at;
+            tiles = __builtin_amdgcn_readlane(tl, at);
+            count = __builtin_amdgcn_readlane(nl, at);
+            cuts = __builtin_amdgcn_readlane(k, at);
+            seq.q0 = __builtin_amdgcn_readlane(sl.q0, at);
+            seq.m = __builtin_amdgcn_readlane(sl.m, at);
+            seq.n = __builtin_amdgcn_readlane(sl.n, at);
+            id -= __builtin_amdgcn_readlane(inc, at) - tiles * cuts * c.heads;
+            split += cuts > 1 ? __builtin_amdgcn_readlane(sinc, at) - tiles * cuts * c.heads : 0;
+            break;
+        }
+        id -= __builtin_amdgcn_readlane(inc, 63);
+        split += __builtin_amdgcn_readlane(sinc, 63);
+    }
+    if (b < 0)
+        return;
+    // Head first, so that neighbours (other chiplets) have other heads' keys;
+    // the last rows, which see the most keys, first.
+    const int head = id % c.heads, part = id / c.heads % cuts, tile = tiles - 1 - id / c.heads / cuts;
+    const int width = (count + cuts - 1) / cuts;
+    const int rows = seq.m * group, row0 = tile * kRows, rows_here = min(kRows, rows - row0);
+    // steps that some row of the tile sees
+    const int i_first = query_of(row0, w.over_group, group), i_last = query_of(row0 + rows_here - 1, w.over_group, group);
+    const int first = kv4_steps(seq, a.causal, a.window, kKeys).first;
+    const int lo_tile = kv4_lo(seq.n, seq.m, i_first, a.window), hi_tile = kv4_hi(seq.n, seq.m, i_last, a.causal);
+    const int begin = lo_tile / kKeys - first, end = max((hi_tile + kKeys - 1) / kKeys - first, begin);
+    // the parts that hold any of them
+    const int part0 = min(begin / width, cuts - 1), part1 = max(part0, end > 0 ? (end - 1) / width : 0);
+    if (part < part0 || part > part1)
+        return;
+    const int parts = part1 - part0 + 1;
+    const int s0 = first + max(begin, part * width), s1 = first + min(end, (part + 1) * width);
+    // slots and counters of the sequence's tiles: [tile][head][part]
+    const int tile_head = tile * c.heads + head;
+    if (cuts > 1 && split + (tile_head + 1) * cuts > w.slots)
+        return;                                          // only where q_starts gives rows to several sequences
+    const int slot0 = split + tile_head * cuts + part0;
+    uint64_t *counter = w.counters + (int64_t)(split + tile_head * cuts) * kCounterStride;
+    if (parts > 1 && threadIdx.x == 0)
+        announce(counter, a.tag);
+
+    // ---- queries: row lane % 32 of the wave's 32
+    const int r32 = lane & 31, h = lane >> 5;
+    const int row = row0 + 32 * wave + r32;
+    const int rc = min(row, rows - 1);
+    const int qi = query_of(rc, w.over_group, group), hh = rc - qi * group;
+    h8 q[D / 16];
+    {
+        const uint16_t *qp = a.q + (int64_t)(seq.q0 + qi) * a.q_stride + (int64_t)(head * group + hh) * D + 8 * h;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+            q[k] = order8(*reinterpret_cast<const uint4 *>(qp + 16 * k));
+    }
+    const int lo = kv4_lo(seq.n, seq.m, qi, a.window), hi = kv4_hi(seq.n, seq.m, qi, a.causal);
+    // of the wave's rows: keys that all see, keys that any sees
+    const int wrow0 = min(row0 + 32 * wave, rows - 1), wrow1 = min(row0 + 32 * wave + 31, rows - 1);
+    const int wi0 = query_of(wrow0, w.over_group, group), wi1 = query_of(wrow1, w.over_group, group);
+    const int lo_any = kv4_lo(seq.n, seq.m, wi0, a.window), lo_all = kv4_lo(seq.n, seq.m, wi1, a.window);
+    const int hi_all = kv4_hi(seq.n, seq.m, wi0, a.causal), hi_any = kv4_hi(seq.n, seq.m, wi1, a.causal);
+
+    // ---- the producer's side of a thread
+    const int32_t *table = a.table + (int64_t)b * a.max_pages;
+    const int last_key = seq.n - 1;
+    const bool for_v = wave < 2;
+    const int u = threadIdx.x & 127;
+    // V: 8 keys of piece u / 16 = (half of 32 keys, 16 of it, run), word u % 16; K: keys u / 4 and 32 more, words u % 4
+    const int vkey = (u >> 5) * 16 + ((u >> 4) & 1) * 4;  // its keys: vkey + 0..3, vkey + 8 + 0..3
+    const int pkey = for_v ? vkey : u >> 2;
+    uint32_t code[8 * (D > 128 ? D / 128 : 1)];
+    float scale[2][NG];
+    int page[2];                                         // of the next tile's keys
+    bool there[2] = {false, false};                      // the loaded tile's
+    const auto pages_of = [&](int step) {
+        const int k0 = min(step * kKeys + pkey, last_key), k1 = min(step * kKeys + pkey + (for_v ? 8 : 32), last_key);
+        page[0] = table[k0 >> c.shift];
+        page[1] = table[k1 >> c.shift];
+    };
+    const auto load_scales = [&](float (&s)[NG], const float *p) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            s[g] = p[g];
+    };
+    const auto fetch = [&](int step) {
+        const int mask = (1 << c.shift) - 1;
+        if (for_v) {
+            const int r = u & 15, key = step * kKeys + vkey;
+            const bool ok = kv4_page_ok(page[0], c.pages);
+            const int64_t at = c.row(ok ? page[0] : 0, head, key & mask);
+            const uint8_t *p = c.v + at * (D / 2) + r * N32;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint8_t *pj = p + (j % 4 + j / 4 * 8) * (D / 2);
+                if constexpr (N32 == 2) {
+                    code[j] = *reinterpret_cast<const uint16_t *>(pj);
+                } else if constexpr (N32 == 4) {
+                    code[j] = *reinterpret_cast<const uint32_t *>(pj);
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(pj);
+                    code[2 * j] = x.x, code[2 * j + 1] = x.y;
+                }
+            }
+            // lanes 0 .. 7 of a piece: its eight keys' scales
+            const int mine = r % 4 + (r >> 2 & 1) * 8;
+            there[0] = ok && key + mine <= last_key;
+            load_scales(scale[0], c.vs + (at + mine) * NG);
+        } else {
+            const int b4 = u & 3;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int key = step * kKeys + (u >> 2) + 32 * x;
+                const bool ok = kv4_page_ok(page[x], c.pages);
+                const int64_t at = c.row(ok ? page[x] : 0, head, key & mask);
+                there[x] = ok && key <= last_key;
+                const uint8_t *p = c.k + at * (D / 2) + b4 * (D / 8);
+                if constexpr (N32 == 2) {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(p);
+                    code[2 * x] = y.x, code[2 * x + 1] = y.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N32 / 4; ++i) {
+                        const v4u y = reinterpret_cast<const v4u *>(p)[i];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            code[N32 * x + 4 * i + e] = y[e];
+                    }
+                }
+                load_scales(scale[x], c.ks + at * NG);
+            }
+        }
+    };
+    // codes to LDS; a hidden key's K scale is -1 and its V scale 0
+    const auto produce = [&](int buf) {
+        if (for_v) {
+            const int r = u & 15, piece = u >> 4;
+            each<N32>([&](auto gc) {
+                constexpr int g = decltype(gc)::value, W = N32 > 4 ? 2 : 1, o = g / 4;
+                const uint32_t x0 = byte_pair<g % 4>(code[0 * W + o], code[1 * W + o]), x1 = byte_pair<g % 4>(code[2 * W + o], code[3 * W + o]);
+                const uint32_t x2 = byte_pair<g % 4>(code[4 * W + o], code[5 * W + o]), x3 = byte_pair<g % 4>(code[6 * W + o], code[7 * W + o]);
+                const int d = 32 * g + 2 * r, at = swizzle<VC>(d, piece);
+                vt[buf][d][at] = (u32x4){codes_low(x0), codes_low(x1), codes_low(x2), codes_low(x3)};
+                vt[buf][d + 1][at] = (u32x4){codes_high(x0), codes_high(x1), codes_high(x2), codes_high(x3)};
+            });
+            if (r < 8) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    vsc[buf][g][vkey + r % 4 + (r >> 2) * 8] = there[0] ? scale[0][g] : 0.0f;
+            }
+        } else {
+            const int b4 = u & 3;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int key = (u >> 2) + 32 * x;
+#pragma unroll
+                for (int i = 0; i < N32; ++i)
+                    kt[buf][key][swizzle<KC>(key, 4 * i + b4)] = __builtin_bit_cast(u32x4, codes8(code[N32 * x + i]));
+                if (b4 == 0) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        ksc[buf][g][key] = there[x] ? scale[x][g] : -1.0f;
+                }
+            }
+        }
+    };
+
+    // ---- the tiles
+    v16f o[N32];
+#pragma unroll
+    for (int g = 0; g < N32; ++g)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            o[g][e] = 0.0f;
+    float ref = 0.0f, top = -INFINITY, l = 0.0f;
+    int scale_exp = kNoScale;
+    const float score_scale = a.scale * kLog2e;
+    // key of lane % 16 in the runs of four that the lane's half has of 32 keys
+    const int lane_key = (lane & 15) / 4 * 8 + 4 * h + (lane & 3);
+
+    const auto compute = [&](int step, int buf) {
+        const int t0 = step * kKeys;
+        if (t0 >= hi_any || t0 + (kKeys - 1) < lo_any)
+            return;
+        float s[2][16];
+        float vs[2][NG];
+        uint32_t big = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float ks[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                ks[g] = ksc[buf][g][32 * x + lane_key];
+                vs[x][g] = vsc[buf][g][32 * x + lane_key];
+                big = max(big, __float_as_uint(vs[x][g]));
+            }
+            const uint64_t gone = __ballot(ks[0] < 0.0f);
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                ks[g] *= score_scale;
+            each<NG>([&](auto gc) {
+                constexpr int g = decltype(gc)::value;
+                v16f acc;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc[e] = 0.0f;
+#pragma unroll
+                for (int k = g * 2 * PER; k < (g + 1) * 2 * PER; ++k)
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        __builtin_bit_cast(h8, kt[buf][32 * x + r32][swizzle<KC>(32 * x + r32, 2 * k + h)]), q[k], acc, 0, 0, 0);
+                each<16>([&](auto ec) {
+                    constexpr int e = decltype(ec)::value;
+                    const float f = row_lane<e>(ks[g]);
+                    s[x][e] = g == 0 ? acc[e] * f : fmaf(acc[e], f, s[x][e]);
+                });
+            });
+            if (t0 < lo_all || t0 + kKeys > hi_all || gone) {
+                each<16>([&](auto ec) {
+                    constexpr int e = decltype(ec)::value;
+                    const int key = t0 + 32 * x + e / 4 * 8 + 4 * h + e % 4;
+                    const float there = row_lane<e>(ks[0]);          // by all lanes: no lane may be off when it is read
+                    s[x][e] = (key >= lo) & (key < hi) & (there >= 0.0f) ? s[x][e] : -INFINITY;
+                });
+            }
+        }
+        big = max_rows_u32(group_max_u32<16>(big));
+        scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
+        float m = s[0][0];
+#pragma unroll
+        for (int e = 1; e < 31; e += 2)
+            m = max3(m, s[e / 16][e % 16], s[(e + 1) / 16][(e + 1) % 16]);
+        m = max3(m, s[1][15], top);
+        m = max_halves(m);
+        const float nref = (m == -INFINITY ? 0.0f : m) + (float)(scale_exp - kHeadroom);
+        if (__ballot(nref != ref)) {
+            const float alpha = top == -INFINITY ? 0.0f : exp2_hw(ref - nref);
+            l *= alpha;
+#pragma unroll
+            for (int g = 0; g < N32; ++g)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    o[g][e] *= alpha;
+            ref = nref;
+        }
+        top = m;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[x][e] = exp2_hw(s[x][e] - nref);
+                sum[e % 4] += s[x][e];
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            each<2>([&](auto mc) {
+                constexpr int m2 = decltype(mc)::value;
+                each<NG>([&](auto gc) {
+                    constexpr int grp = decltype(gc)::value;
+                    u32x4 y;                             // weight times the value's scale, the one rounding to fp16
+                    each<4>([&](auto ic) {
+                        constexpr int e = 8 * m2 + 2 * decltype(ic)::value;
+                        y[decltype(ic)::value] = pack_h2(s[x][e] * row_lane<e>(vs[x][grp]), s[x][e + 1] * row_lane<e + 1>(vs[x][grp]));
+                    });
+#pragma unroll
+                    for (int g = grp * PER; g < (grp + 1) * PER; ++g)
+                        o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                            __builtin_bit_cast(h8, vt[buf][32 * g + r32][swizzle<VC>(32 * g + r32, 4 * x + 2 * m2 + h)]),
+                            __builtin_bit_cast(h8, y), o[g], 0, 0, 0);
+                });
+            });
+        }
+    };
+
+    if (s0 < s1) {
+        pages_of(s0);
+        fetch(s0);
+        pages_of(s0 + 1);
+    }
+    for (int step = s0; step < s1; ++step) {
+        const int buf = (step - s0) & 1;
+        produce(buf);
+        if (step + 1 < s1) {
+            fetch(step + 1);
+            pages_of(step + 2);
+        }
+        lds_barrier();
+        compute(step, buf);
+    }
+
+    // ---- results: the lane's row, dims 32 g + 8 i + 4 h ..+3
+    l = sum_halves(l);
+    if (parts == 1) {
+        if (row < rows) {
+            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+            const int64_t at = (int64_t)(seq.q0 + qi) * a.q_heads + head * group + hh;
+#pragma unroll
+            for (int g = 0; g < N32; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint2 *>(a.out + at * D + 32 * g + 8 * i + 4 * h) =
+                        make_uint2(pack_h2(o[g][4 * i] * inv, o[g][4 * i + 1] * inv), pack_h2(o[g][4 * i + 2] * inv, o[g][4 * i + 3] * inv));
+            if (a.lse && h == 0)
+                a.lse[at] = l > 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+        }
+        return;
+    }
+    if (row < rows) {
+        float *dst = w.base + ((int64_t)(slot0 + part - part0) * w.slot_rows + 32 * wave + r32) * (D + 2);
+#pragma unroll
+        for (int g = 0; g < N32; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                store_shared(dst + 32 * g + 8 * i + 4 * h, o[g][4 * i], o[g][4 * i + 1]);
+                store_shared(dst + 32 * g + 8 * i + 4 * h + 2, o[g][4 * i + 2], o[g][4 * i + 3]);
+            }
+        if (h == 0)
+            store_shared(dst + D, l > 0.0f ? ref : -INFINITY, l);
+    }
+    __builtin_amdgcn_s_waitcnt(0);                       // this wave's stores are complete
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = arrive(counter, parts) ? 1 : 0;
+    __syncthreads();
+    if (last)
+        join_parts<D>(w, a, seq, head, row0, rows_here, slot0, parts, reinterpret_cast<float *>(&kt[0][0][0]));
+}
+
+}  // namespace
+
+void launch_kv4_prefill(const Kv4Cache &c, const Kv4AttnArgs &a, int row_limit, void *workspace, hipStream_t st)
+{
+    const Kv4Tiles t = kv4_prefill_tiles(a.T, a.B, a.group, c.heads, (int64_t)a.max_pages << c.shift);
+    Partial w;
+    w.grid = (int)t.grid;
+    w.row_limit = row_limit;
+    w.slot_rows = kRows;
+    w.slots = (int)t.slots;
+    w.over_group = over_group(a.group);
+    w.counters = static_cast<uint64_t *>(workspace);
+    w.base = reinterpret_cast<float *>(static_cast<char *>(workspace) + kv4_counter_bytes(t.slots, 1));
+    const dim3 grid((unsigned)t.grid), block(kThreads);
+    const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, c, a, w); };
+    switch (c.D * 8 + c.D / c.G) {
+    case 64 * 8 + 1: launch(kv4_prefill_kernel<64, 1>); return;
+    case 64 * 8 + 2: launch(kv4_prefill_kernel<64, 2>); return;
+    case 128 * 8 + 1: launch(kv4_prefill_kernel<128, 1>); return;
+    case 128 * 8 + 2: launch(kv4_prefill_kernel<128, 2>); return;
+    case 128 * 8 + 4: launch(kv4_prefill_kernel<128, 4>); return;
+    case 256 * 8 + 1: launch(kv4_prefill_kernel<256, 1>); return;
+    case 256 * 8 + 2: launch(kv4_prefill_kernel<256, 2>); return;
+    default: launch(kv4_prefill_kernel<256, 4>); return;
+    }
+}
+
+}  // namespace w4a8
