@@ -10,38 +10,71 @@ cache and attention over it (marshalling only, as in ops.py).
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from . import ops
 from ._lib import CacheStruct, check, lib
-from .ops import _need, _out, _p, _shaped, _st
+from .ops import _need, _shaped
+
+# A decode step calls these for microseconds of GPU work each, so the checks are
+# kept short: pointers go to ctypes as integers, the stream is torch's current
+# one as a number, and the device is only switched when it is not the current.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _rows(t, name, like=None, heads=None, head_dim=None):
-    """fp16 [T, heads, head_dim] whose heads are contiguous in a token; tokens may be strided."""
+def _stream(index):
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _call(index, fn, *args):
+    """fn(*args, stream) with device `index` current."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _stream(index))
+    if status:
+        check(status)
+
+
+def _rows(t, name, index=None, heads=None, head_dim=None):
+    """fp16 [T, heads, head_dim] whose heads are contiguous in a token; tokens may be strided.
+    Returns (T, elements from one token to the next)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != ops._DEVICE_TYPE:
-        raise ValueError(f"{name} must be a device tensor, got {t.device}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, the other operands on {like.device}")
-    if t.dtype != torch.float16:
+    if index is None:
+        if t.device.type != ops._DEVICE_TYPE:
+            raise ValueError(f"{name} must be a device tensor, got {t.device}")
+    elif t.get_device() != index:
+        raise ValueError(f"{name} must be on the device of the other operands, got {t.device}")
+    if t.dtype is not torch.float16:
         raise TypeError(f"{name} must be torch.float16, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dims [T, heads, head_dim], got shape {tuple(t.shape)}")
     T, h, d = t.shape
     if (heads is not None and h != heads) or (head_dim is not None and d != head_dim):
         raise ValueError(f"{name} must have shape [T, {heads}, {head_dim}], got {tuple(t.shape)}")
-    st = t.stride()
-    if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
-        raise ValueError(f"{name} must have contiguous heads within a token, got strides {st}")
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+        raise ValueError(f"{name} must have contiguous heads within a token, got strides {(st, sh, sd)}")
+    return T, st if T > 1 else h * d
+
+
+def _flat(t, dtype, shape, name, index):
+    """t must be a contiguous `dtype` tensor of exactly `shape` on device `index`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got shape {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the device of the other operands, got {t.device}")
     return t
-
-
-def _token_stride(t):
-    """Elements from one token to the next (a single token has none of its own)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
 
 
 class KV4Cache:
@@ -55,7 +88,7 @@ class KV4Cache:
     """
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "pages", "kv_heads", "page_size", "head_dim",
-                 "group_size", "device", "_struct", "_ref")
+                 "group_size", "device", "_index", "_struct", "_ref")
 
     def __init__(self, k, k_scale, v, v_scale):
         _need(k, torch.uint8, "k", 4)
@@ -79,7 +112,7 @@ class KV4Cache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_size = pages, heads, page
         self.head_dim, self.group_size = 2 * half, 2 * half // groups
-        self.device = k.device
+        self.device, self._index = k.device, k.get_device()
         self._struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                    pages, heads, page, self.head_dim, self.group_size)
         self._ref = ctypes.addressof(self._struct)
@@ -104,61 +137,68 @@ def _cache(c):
     return c
 
 
+@functools.lru_cache(maxsize=64)
+def _sections(sections, half):
+    """The C array of an axis' pair counts, checked."""
+    if not 1 <= len(sections) <= 3 or min(sections) < 0 or sum(sections) != half:
+        raise ValueError(f"sections must be 1 to 3 counts that sum to {half}, got {sections}")
+    return (ctypes.c_int32 * len(sections))(*sections)
+
+
 def rotary_axes(x, positions, inv_freq, sections=None, interleaved: bool = False, out=None):
     """Rotary positions: x fp16 [T, heads, head_dim] (tokens may be strided), positions int64
     [axes, T] (or [T]), inv_freq fp32 [rotary_dim / 2]; sections: how many pairs each axis
     turns (default: one axis turns all).  out (default: a new tensor) may be x."""
-    _rows(x, "x")
-    T, heads, D = x.shape
-    _need(inv_freq, torch.float32, "inv_freq", 1, x)
-    half = inv_freq.shape[0]
+    T, stride = _rows(x, "x")
+    _, heads, D = x.shape
+    index = x.get_device()
+    half = inv_freq.numel()
+    _flat(inv_freq, torch.float32, (half,), "inv_freq", index)
     if half == 0 or half % 8 or 2 * half > D:
         raise ValueError(f"inv_freq must have rotary_dim / 2 values, a multiple of 8 up to {D // 2}, "
                          f"got {half}")
-    sections = (half,) if sections is None else tuple(int(n) for n in sections)
-    axes = len(sections)
-    if not 1 <= axes <= 3 or min(sections) < 0 or sum(sections) != half:
-        raise ValueError(f"sections must be 1 to 3 counts that sum to {half}, got {sections}")
-    if positions.dim() == 1:
-        positions = positions.unsqueeze(0)
-    _shaped(positions, torch.int64, (axes, T), "positions", x)
+    counts = _sections((half,) if sections is None else tuple(sections), half)
+    axes = len(counts)
+    _flat(positions, torch.int64, (T,) if positions.dim() == 1 and axes == 1 else (axes, T), "positions", index)
     if out is None:
         out = torch.empty((T, heads, D), dtype=torch.float16, device=x.device)
+        out_stride = heads * D
+    elif _rows(out, "out", index, heads, D)[0] != T:
+        raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
     else:
-        _rows(out, "out", x, heads, D)
-        if out.shape[0] != T:
-            raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
-    with torch.cuda.device(x.device):
-        check(lib().rotary_axes(_p(x), _token_stride(x), _p(positions), _p(inv_freq), T, heads, D,
-                                2 * half, axes, (ctypes.c_int32 * axes)(*sections),
-                                int(interleaved), _p(out), _token_stride(out), _st(x)))
+        out_stride = _rows(out, "out", index, heads, D)[1]
+    _call(index, lib().rotary_axes, x.data_ptr(), stride, positions.data_ptr(), inv_freq.data_ptr(), T, heads, D,
+          2 * half, axes, counts, interleaved, out.data_ptr(), out_stride)
     return out
 
 
 def kv4_write(k, v, slots, cache):
     """Quantize T tokens' keys and values (fp16 [T, kv_heads, head_dim], tokens may be strided)
     into the cache's slots (int64 [T]; outside the cache: not written)."""
-    _cache(cache)
-    _rows(k, "k", cache, cache.kv_heads, cache.head_dim)
-    _rows(v, "v", cache, cache.kv_heads, cache.head_dim)
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError(f"v has {v.shape[0]} tokens, k has {T}: shape mismatch")
-    _shaped(slots, torch.int64, (T,), "slots", cache)
-    with torch.cuda.device(cache.device):
-        check(lib().kv4_write(_p(k), _token_stride(k), _p(v), _token_stride(v), _p(slots), T,
-                              cache._ref, _st(k)))
+    index = _cache(cache)._index
+    T, k_stride = _rows(k, "k", index, cache.kv_heads, cache.head_dim)
+    Tv, v_stride = _rows(v, "v", index, cache.kv_heads, cache.head_dim)
+    if Tv != T:
+        raise ValueError(f"v has {Tv} tokens, k has {T}: shape mismatch")
+    _flat(slots, torch.int64, (T,), "slots", index)
+    _call(index, lib().kv4_write, k.data_ptr(), k_stride, v.data_ptr(), v_stride, slots.data_ptr(), T, cache._ref)
 
 
 def kv4_read(cache, slots, k=None, v=None):
     """The keys and values of T slots (int64 [T]) as fp16 [T, kv_heads, head_dim] each."""
-    _cache(cache)
-    _need(slots, torch.int64, "slots", 1, cache)
-    shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
-    k = _out(k, shape, torch.float16, cache, "k")
-    v = _out(v, shape, torch.float16, cache, "v")
-    with torch.cuda.device(cache.device):
-        check(lib().kv4_read(cache._ref, _p(slots), shape[0], _p(k), _p(v), _st(slots)))
+    index = _cache(cache)._index
+    T = slots.numel()
+    _flat(slots, torch.int64, (T,), "slots", index)
+    shape = (T, cache.kv_heads, cache.head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.float16, device=cache.device)
+    else:
+        _flat(k, torch.float16, shape, "k", index)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.float16, device=cache.device)
+    else:
+        _flat(v, torch.float16, shape, "v", index)
+    _call(index, lib().kv4_read, cache._ref, slots.data_ptr(), T, k.data_ptr(), v.data_ptr())
     return k, v
 
 
@@ -169,8 +209,8 @@ def kv4_attention_workspace_size(q_heads: int, kv_heads: int, head_dim: int, tok
 
 
 def kv4_attention_workspace(cache, q_heads: int, tokens: int, sequences: int, max_q: int = 1):
-    """A workspace for calls of kv4_attention up to these sizes, to be kept between calls that do
-    not overlap."""
+    """A workspace for calls of kv4_attention of these sizes, to be kept between calls that do not
+    overlap."""
     _cache(cache)
     need = kv4_attention_workspace_size(q_heads, cache.kv_heads, cache.head_dim, tokens, sequences,
                                         max_q)
@@ -183,35 +223,43 @@ def kv4_attention(q, cache, page_table, kv_lens, q_starts=None, max_q: int = 1, 
     """Attention of T query rows (fp16 [T, q_heads, head_dim], tokens may be strided) over the
     cache: page_table int32 [sequences, max_pages], kv_lens int32 [sequences] (the queries' own
     tokens counted), q_starts int32 [sequences + 1] (default: one query a sequence), max_q an
-    upper bound of a sequence's queries.  scale defaults to head_dim ** -0.5.  Returns out fp16
-    [T, q_heads, head_dim], with return_lse (out, lse fp32 [T, q_heads])."""
-    _cache(cache)
-    _rows(q, "q", cache, None, None)
-    T, heads, D = q.shape
+    upper bound of a sequence's queries.  scale defaults to head_dim ** -0.5.  workspace: of
+    kv4_attention_workspace (default: a new one).  Returns out fp16 [T, q_heads, head_dim], with
+    return_lse (out, lse fp32 [T, q_heads])."""
+    index = _cache(cache)._index
+    T, stride = _rows(q, "q", index)
+    _, heads, D = q.shape
     if D != cache.head_dim or heads == 0 or heads % cache.kv_heads:
         raise ValueError(f"q must have head_dim {cache.head_dim} and a multiple of {cache.kv_heads} "
                          f"heads, got shape {tuple(q.shape)}")
-    _need(page_table, torch.int32, "page_table", 2, cache)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must have 2 dims, got shape {tuple(page_table.shape)}")
     B, max_pages = page_table.shape
-    _shaped(kv_lens, torch.int32, (B,), "kv_lens", cache)
+    _flat(page_table, torch.int32, (B, max_pages), "page_table", index)
+    _flat(kv_lens, torch.int32, (B,), "kv_lens", index)
     if q_starts is not None:
-        _shaped(q_starts, torch.int32, (B + 1,), "q_starts", cache)
+        starts = _flat(q_starts, torch.int32, (B + 1,), "q_starts", index).data_ptr()
     elif T != B:
         raise ValueError(f"without q_starts q must have one row a sequence, got shape {tuple(q.shape)} "
                          f"for {B} sequences")
-    need = lib().kv4_attention_workspace_size(heads, cache.kv_heads, D, T, B, max_q)
+    else:
+        starts = None
+    L = lib()
     if workspace is None:
+        need = L.kv4_attention_workspace_size(heads, cache.kv_heads, D, T, B, max_q)
         workspace = torch.empty((need,), dtype=torch.uint8, device=cache.device)
     else:
-        _need(workspace, torch.uint8, "workspace", 1, cache)
-        if workspace.numel() < need:
-            raise ValueError(f"workspace has {workspace.numel()} bytes, {need} needed")
-    out = _out(out, (T, heads, D), torch.float16, cache, "out")
-    if return_lse or lse is not None:
-        lse = _out(lse, (T, heads), torch.float32, cache, "lse")
-    with torch.cuda.device(cache.device):
-        check(lib().kv4_attention(_p(q), _token_stride(q), T, heads, cache._ref, _p(page_table),
-                                  max_pages, _p(kv_lens), _p(q_starts), B, max_q, int(causal),
-                                  window, D ** -0.5 if scale is None else scale, _p(out), _p(lse),
-                                  _p(workspace), workspace.numel(), _st(q)))
+        _flat(workspace, torch.uint8, (workspace.numel(),), "workspace", index)     # its size: by the library
+    shape = (T, heads, D)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float16, device=cache.device)
+    else:
+        _flat(out, torch.float16, shape, "out", index)
+    if lse is not None:
+        _flat(lse, torch.float32, (T, heads), "lse", index)
+    elif return_lse:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=cache.device)
+    _call(index, L.kv4_attention, q.data_ptr(), stride, T, heads, cache._ref, page_table.data_ptr(), max_pages,
+          kv_lens.data_ptr(), starts, B, max_q, causal, window, D ** -0.5 if scale is None else scale,
+          out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return (out, lse) if return_lse else out
