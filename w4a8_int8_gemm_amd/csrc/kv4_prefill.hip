@@ -210,7 +210,8 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         }
     };
     // codes to LDS; a hidden key's K scale is -1 and its V scale 0
-    const auto produce = [&](int buf) {
+    const auto produce = [&](auto bc) {
+        constexpr int buf = decltype(bc)::value;
         if (for_v) {
             const int r = u & 15, piece = u >> 4;
             each<N32>([&](auto gc) {
@@ -256,7 +257,17 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
     // key of lane % 16 in the runs of four that the lane's half has of 32 keys
     const int lane_key = (lane & 15) / 4 * 8 + 4 * h + (lane & 3);
 
-    const auto compute = [&](int step, int buf) {
+    // a row's pieces where the swizzle puts them; rows 32 apart have the same
+    int kpiece[D / 16], vpiece[4];
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+        kpiece[k] = swizzle<KC>(r32, 2 * k + h);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        vpiece[k] = swizzle<VC>(r32, 2 * k + h);
+
+    const auto compute = [&](int step, auto bc) {
+        constexpr int buf = decltype(bc)::value;
         const int t0 = step * kKeys;
         if (t0 >= hi_any || t0 + (kKeys - 1) < lo_any)
             return;
@@ -285,7 +296,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
 #pragma unroll
                 for (int k = g * 2 * PER; k < (g + 1) * 2 * PER; ++k)
                     acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        __builtin_bit_cast(h8, kt[buf][32 * x + r32][swizzle<KC>(32 * x + r32, 2 * k + h)]), q[k], acc, 0, 0, 0);
+                        __builtin_bit_cast(h8, kt[buf][32 * x + r32][kpiece[k]]), q[k], acc, 0, 0, 0);
                 each<16>([&](auto ec) {
                     constexpr int e = decltype(ec)::value;
                     const float f = row_lane<e>(ks[g]);
@@ -297,7 +308,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
                     constexpr int e = decltype(ec)::value;
                     const int key = t0 + 32 * x + e / 4 * 8 + 4 * h + e % 4;
                     const float there = row_lane<e>(ks[0]);          // by all lanes: no lane may be off when it is read
-                    s[x][e] = (key >= lo) & (key < hi) & (there >= 0.0f) ? s[x][e] : -INFINITY;
+                    s[x][e] = ((key >= lo) & (key < hi) & (there >= 0.0f)) ? s[x][e] : -INFINITY;
                 });
             }
         }
@@ -323,6 +334,10 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         top = m;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+            // keeps the lane moves of the scales in this block, where they fold into the products
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                asm("" : "+v"(vs[x][g]));
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -342,7 +357,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
 #pragma unroll
                     for (int g = grp * PER; g < (grp + 1) * PER; ++g)
                         o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            __builtin_bit_cast(h8, vt[buf][32 * g + r32][swizzle<VC>(32 * g + r32, 4 * x + 2 * m2 + h)]),
+                            __builtin_bit_cast(h8, vt[buf][32 * g + r32][vpiece[2 * x + m2]]),
                             __builtin_bit_cast(h8, y), o[g], 0, 0, 0);
                 });
             });
@@ -354,15 +369,20 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         fetch(s0);
         pages_of(s0 + 1);
     }
-    for (int step = s0; step < s1; ++step) {
-        const int buf = (step - s0) & 1;
-        produce(buf);
+    const auto one = [&](int step, auto bc) {
+        produce(bc);
         if (step + 1 < s1) {
             fetch(step + 1);
             pages_of(step + 2);
         }
         lds_barrier();
-        compute(step, buf);
+        compute(step, bc);
+    };
+    // in pairs: the buffers' addresses are constants of the instructions
+    for (int step = s0; step < s1; step += 2) {
+        one(step, std::integral_constant<int, 0>());
+        if (step + 1 < s1)
+            one(step + 1, std::integral_constant<int, 1>());
     }
 
     // ---- results: the lane's row, dims 32 g + 8 i + 4 h ..+3
