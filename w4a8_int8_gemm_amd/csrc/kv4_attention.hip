@@ -31,8 +31,9 @@ size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int 
     size_t bytes = decode_bytes(q_heads, kv_heads, D, T, B, max_q);
     if ((int64_t)group * (max_q < T ? max_q : T) > kv4_decode_limit(D)) {
         // any length of keys: the table's width is not known here
-        const Kv4Tiles t = kv4_prefill_tiles(T, B, group, kv_heads, int64_t(1) << 30);
-        bytes += kv4_counter_bytes(t.slots, 1) + (size_t)t.slots * 128 * (D + 2) * sizeof(float);
+        const int rows = kv4_tile_rows(T, group, kv_heads, D);
+        const Kv4Tiles t = kv4_prefill_tiles(T, B, group, kv_heads, int64_t(1) << 30, rows);
+        bytes += kv4_counter_bytes(t.slots, 1) + (size_t)t.slots * rows * (D + 2) * sizeof(float);
     }
     return bytes;
 }

@@ -29,6 +29,15 @@ namespace w4a8 {
 namespace {
 
 
+// The weights p = exp2(s - ref) times a value's scale have to fit fp16, whose
+// normal numbers span 30 binades.  ref = (largest score seen) + (exponent of
+// the largest scale seen) - kHeadroom puts every weight below 2^14 and lets
+// scores times scales 28 binades under the largest keep all their bits; any
+// reference gives the same quotient, so sum and output need no correction.
+constexpr int kHeadroom = 13;
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+
 // Pieces of 16 keys in a step: more of them share the softmax's bookkeeping,
 // where the registers hold them.
 template <int D, int RT> constexpr int kPieces = 2;
@@ -441,7 +450,7 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
             last = arrive(w.counters + item * kCounterStride, parts) ? 1 : 0;
         __syncthreads();
         if (last)
-            join_parts<D>(w, a, seq, head, 0, rows, blockIdx.x - part, parts, &os[0][0][0]);
+            join_parts<D, kThreads>(w, a, seq, head, 0, rows, blockIdx.x - part, parts, &os[0][0][0]);
     }
 }
 

@@ -151,13 +151,7 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 // The exponent floor(log2 v) of a scale's bits, -127 for 0.
 __device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >> 23) - 127; }
 
-// The weights p = exp2(s - ref) times a value's scale have to fit fp16, whose
-// normal numbers span 30 binades.  ref = (largest score seen) + (exponent of
-// the largest scale seen) - kHeadroom puts every weight below 2^14 and lets
-// scores times scales 28 binades under the largest keep all their bits; any
-// reference gives the same quotient, so sum and output need no correction.
-constexpr int kHeadroom = 13;
-constexpr int kNoScale = -100;                // exponent before any key
+constexpr int kNoScale = -100;                // exponent of the largest scale before any key
 
 // Values that other workgroups, on other chiplets with L2 caches of their
 // own, wrote or will read within one launch: loads and stores at device scope.
@@ -196,9 +190,6 @@ __device__ __forceinline__ bool arrive(uint64_t *counter, int parts)
     return true;
 }
 
-// Four waves a workgroup in both kernels.
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
-
 // Where parts of a result that several workgroups compute meet.
 struct Partial {
     float *base;                // [slots][slot_rows][D + 2]: output, reference and sum
@@ -235,7 +226,7 @@ __device__ __forceinline__ void store_row(const Partial &w, const Kv4AttnArgs &a
 // their (sequence, head) on.  A thread takes four dims of a row; where there are more threads, groups of them take every
 // so-many-th part and are joined in LDS.  Parts come from memory at some
 // microseconds' latency, so eight are in flight at a time.
-template <int D>
+template <int D, int kThreads>
 __device__ void join_parts(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int row0, int rows, int p0,
                            int parts, float *lds)
 {

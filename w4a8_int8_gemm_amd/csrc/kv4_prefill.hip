@@ -27,7 +27,9 @@ namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-constexpr int kRows = 128, kKeys = 64;
+constexpr int kKeys = 64;
+constexpr int kHeadroom = 11, kRange = 14;    // binades of a row's largest weight over its scale: when set, at most
+constexpr float kFarBelow = -1e30f;           // under every score
 
 // Piece `c` of 16 bytes in a row of N pieces, moved so that the same piece of 16
 // consecutive rows (of N / 2 pairs of rows where a row is half the banks) is
@@ -37,10 +39,12 @@ template <int N> __device__ __forceinline__ int swizzle(int row, int c)
     return N >= 16 ? c ^ (row & 15) : c ^ ((row >> 1) & 7);
 }
 
-template <int D, int NG>
-__global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
+template <int D, int NG, int WV>
+__global__ __launch_bounds__(64 * WV, D < 256 ? 8 / WV : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
 {
     constexpr int N32 = D / 32, PER = N32 / NG, KC = D / 8, VC = kKeys / 8;
+    constexpr int kRows = 32 * WV;
+    constexpr int SPLIT = WV / 4, NV = N32 / SPLIT;      // producers: threads that share a word of V; its bytes of one
     __shared__ u32x4 kt[2][kKeys][KC];                   // fp16 codes [key][dim], pieces of 8 dims
     __shared__ u32x4 vt[2][D][VC];                       // fp16 codes [dim][key], pieces of 8 keys
     __shared__ float ksc[2][NG][kKeys], vsc[2][NG][kKeys];
@@ -142,12 +146,13 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
     // ---- the producer's side of a thread
     const int32_t *table = a.table + (int64_t)b * a.max_pages;
     const int last_key = seq.n - 1;
-    const bool for_v = wave < 2;
-    const int u = threadIdx.x & 127;
-    // V: 8 keys of piece u / 16 = (half of 32 keys, 16 of it, run), word u % 16; K: keys u / 4 and 32 more, words u % 4
-    const int vkey = (u >> 5) * 16 + ((u >> 4) & 1) * 4;  // its keys: vkey + 0..3, vkey + 8 + 0..3
+    const bool for_v = wave < WV / 2;
+    const int u = threadIdx.x & (32 * WV - 1);
+    // V: 8 keys of piece u / 16 % 8 = (half of 32 keys, 16 of it, run), bytes of word u % 16; K: key u / 4 (and 32
+    // more), words u % 4
+    const int vkey = (u >> 5 & 3) * 16 + ((u >> 4) & 1) * 4, vpart = u >> 7;   // its keys: vkey + 0..3, vkey + 8 + 0..3
     const int pkey = for_v ? vkey : u >> 2;
-    uint32_t code[8 * (D > 128 ? D / 128 : 1)];
+    uint32_t code[8 * (NV > 4 ? 2 : 1)];
     float scale[2][NG];
     int page[2];                                         // of the next tile's keys
     bool there[2] = {false, false};                      // the loaded tile's
@@ -167,13 +172,15 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
             const int r = u & 15, key = step * kKeys + vkey;
             const bool ok = kv4_page_ok(page[0], c.pages);
             const int64_t at = c.row(ok ? page[0] : 0, head, key & mask);
-            const uint8_t *p = c.v + at * (D / 2) + r * N32;
+            const uint8_t *p = c.v + at * (D / 2) + r * N32 + vpart * NV;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint8_t *pj = p + (j % 4 + j / 4 * 8) * (D / 2);
-                if constexpr (N32 == 2) {
+                if constexpr (NV == 1) {
+                    code[j] = *pj;
+                } else if constexpr (NV == 2) {
                     code[j] = *reinterpret_cast<const uint16_t *>(pj);
-                } else if constexpr (N32 == 4) {
+                } else if constexpr (NV == 4) {
                     code[j] = *reinterpret_cast<const uint32_t *>(pj);
                 } else {
                     const uint2 x = *reinterpret_cast<const uint2 *>(pj);
@@ -187,7 +194,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         } else {
             const int b4 = u & 3;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < 2 / SPLIT; ++x) {
                 const int key = step * kKeys + (u >> 2) + 32 * x;
                 const bool ok = kv4_page_ok(page[x], c.pages);
                 const int64_t at = c.row(ok ? page[x] : 0, head, key & mask);
@@ -213,16 +220,16 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
     const auto produce = [&](auto bc) {
         constexpr int buf = decltype(bc)::value;
         if (for_v) {
-            const int r = u & 15, piece = u >> 4;
-            each<N32>([&](auto gc) {
-                constexpr int g = decltype(gc)::value, W = N32 > 4 ? 2 : 1, o = g / 4;
+            const int r = u & 15, piece = u >> 4 & 7;
+            each<NV>([&](auto gc) {
+                constexpr int g = decltype(gc)::value, W = NV > 4 ? 2 : 1, o = g / 4;
                 const uint32_t x0 = byte_pair<g % 4>(code[0 * W + o], code[1 * W + o]), x1 = byte_pair<g % 4>(code[2 * W + o], code[3 * W + o]);
                 const uint32_t x2 = byte_pair<g % 4>(code[4 * W + o], code[5 * W + o]), x3 = byte_pair<g % 4>(code[6 * W + o], code[7 * W + o]);
-                const int d = 32 * g + 2 * r, at = swizzle<VC>(d, piece);
+                const int d = 32 * (g + NV * vpart) + 2 * r, at = swizzle<VC>(d, piece);
                 vt[buf][d][at] = (u32x4){codes_low(x0), codes_low(x1), codes_low(x2), codes_low(x3)};
                 vt[buf][d + 1][at] = (u32x4){codes_high(x0), codes_high(x1), codes_high(x2), codes_high(x3)};
             });
-            if (r < 8) {
+            if (r < 8 && vpart == 0) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
                     vsc[buf][g][vkey + r % 4 + (r >> 2) * 8] = there[0] ? scale[0][g] : 0.0f;
@@ -230,7 +237,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         } else {
             const int b4 = u & 3;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < 2 / SPLIT; ++x) {
                 const int key = (u >> 2) + 32 * x;
 #pragma unroll
                 for (int i = 0; i < N32; ++i)
@@ -251,12 +258,16 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             o[g][e] = 0.0f;
-    float ref = 0.0f, top = -INFINITY, l = 0.0f;
+    // Weights are taken relative to `ref`, which follows the largest score only
+    // when a weight could leave fp16's range (a score above `bound`): with the
+    // values' largest scale below 2^(scale_exp + 1), weights p = 2^(score - ref)
+    // times scale stay below 2^15, and a row's largest is above 1 when set.
+    float ref = kFarBelow, bound = kFarBelow, l = 0.0f;
     int scale_exp = kNoScale;
+    uint32_t scale_cap = 0;                              // bits of 2^(scale_exp + 1)
     const float score_scale = a.scale * kLog2e;
     // key of lane % 16 in the runs of four that the lane's half has of 32 keys
     const int lane_key = (lane & 15) / 4 * 8 + 4 * h + (lane & 3);
-
     // a row's pieces where the swizzle puts them; rows 32 apart have the same
     int kpiece[D / 16], vpiece[4];
 #pragma unroll
@@ -266,102 +277,133 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
     for (int k = 0; k < 4; ++k)
         vpiece[k] = swizzle<VC>(r32, 2 * k + h);
 
-    const auto compute = [&](int step, auto bc) {
+    // Scores of 32 keys: lane's row, keys 8 (e / 4) + 4 h + e % 4 of them.
+    const auto scores = [&](float (&s)[16], const float (&ks)[NG], int x, auto bc) {
         constexpr int buf = decltype(bc)::value;
-        const int t0 = step * kKeys;
-        if (t0 >= hi_any || t0 + (kKeys - 1) < lo_any)
-            return;
-        float s[2][16];
-        float vs[2][NG];
-        uint32_t big = 0;
+        each<NG>([&](auto gc) {
+            constexpr int g = decltype(gc)::value;
+            v16f acc;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float ks[NG];
+            for (int e = 0; e < 16; ++e)
+                acc[e] = 0.0f;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                ks[g] = ksc[buf][g][32 * x + lane_key];
-                vs[x][g] = vsc[buf][g][32 * x + lane_key];
-                big = max(big, __float_as_uint(vs[x][g]));
-            }
-            const uint64_t gone = __ballot(ks[0] < 0.0f);
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                ks[g] *= score_scale;
-            each<NG>([&](auto gc) {
-                constexpr int g = decltype(gc)::value;
-                v16f acc;
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    acc[e] = 0.0f;
-#pragma unroll
-                for (int k = g * 2 * PER; k < (g + 1) * 2 * PER; ++k)
-                    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        __builtin_bit_cast(h8, kt[buf][32 * x + r32][kpiece[k]]), q[k], acc, 0, 0, 0);
-                each<16>([&](auto ec) {
-                    constexpr int e = decltype(ec)::value;
-                    const float f = row_lane<e>(ks[g]);
-                    s[x][e] = g == 0 ? acc[e] * f : fmaf(acc[e], f, s[x][e]);
-                });
+            for (int k = g * 2 * PER; k < (g + 1) * 2 * PER; ++k)
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kt[buf][32 * x + r32][kpiece[k]]), q[k],
+                                                             acc, 0, 0, 0);
+            each<16>([&](auto ec) {
+                constexpr int e = decltype(ec)::value;
+                const float f = row_lane<e>(ks[g]);
+                s[e] = g == 0 ? acc[e] * f : fmaf(acc[e], f, s[e]);
             });
-            if (t0 < lo_all || t0 + kKeys > hi_all || gone) {
-                each<16>([&](auto ec) {
-                    constexpr int e = decltype(ec)::value;
-                    const int key = t0 + 32 * x + e / 4 * 8 + 4 * h + e % 4;
-                    const float there = row_lane<e>(ks[0]);          // by all lanes: no lane may be off when it is read
-                    s[x][e] = ((key >= lo) & (key < hi) & (there >= 0.0f)) ? s[x][e] : -INFINITY;
-                });
-            }
-        }
-        big = max_rows_u32(group_max_u32<16>(big));
-        scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
-        float m = s[0][0];
+        });
+    };
+    const auto hide = [&](float (&s)[16], float ks0, int t0) {
+        each<16>([&](auto ec) {
+            constexpr int e = decltype(ec)::value;
+            const int key = t0 + e / 4 * 8 + 4 * h + e % 4;
+            const float there = row_lane<e>(ks0);        // by all lanes: no lane may be off when it is read
+            s[e] = ((key >= lo) & (key < hi) & (there >= 0.0f)) ? s[e] : -INFINITY;
+        });
+    };
+    // The largest of a lane's scores.
+    const auto largest = [&](const float (&s)[16]) {
+        float m = max3(s[0], s[1], s[2]);
 #pragma unroll
-        for (int e = 1; e < 31; e += 2)
-            m = max3(m, s[e / 16][e % 16], s[(e + 1) / 16][(e + 1) % 16]);
-        m = max3(m, s[1][15], top);
+        for (int e = 3; e < 15; e += 2)
+            m = max3(m, s[e], s[e + 1]);
+        return max3(m, s[15], s[15]);
+    };
+    const auto rescale = [&](float m) {
         m = max_halves(m);
-        const float nref = (m == -INFINITY ? 0.0f : m) + (float)(scale_exp - kHeadroom);
-        if (__ballot(nref != ref)) {
-            const float alpha = top == -INFINITY ? 0.0f : exp2_hw(ref - nref);
+        if (m > bound) {
+            const float nref = m + (float)(scale_exp - kHeadroom);
+            const float alpha = exp2_hw(ref - nref);     // 0 before the first key
             l *= alpha;
+            ref = nref;
+            bound = ref + (float)(kRange - scale_exp);
 #pragma unroll
             for (int g = 0; g < N32; ++g)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     o[g][e] *= alpha;
-            ref = nref;
         }
-        top = m;
+    };
+    const auto weights = [&](float (&s)[16]) {
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            // keeps the lane moves of the scales in this block, where they fold into the products
+        for (int e = 0; e < 16; ++e) {
+            s[e] = exp2_hw(s[e] - ref);
+            sum[e % 4] += s[e];
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    };
+    const auto output = [&](const float (&s)[16], const float (&vs)[NG], int x, auto bc) {
+        constexpr int buf = decltype(bc)::value;
+        each<2>([&](auto mc) {
+            constexpr int m2 = decltype(mc)::value;
+            each<NG>([&](auto gc) {
+                constexpr int grp = decltype(gc)::value;
+                u32x4 y;                                 // weight times the value's scale, the one rounding to fp16
+                each<4>([&](auto ic) {
+                    constexpr int e = 8 * m2 + 2 * decltype(ic)::value;
+                    y[decltype(ic)::value] = pack_h2(s[e] * row_lane<e>(vs[grp]), s[e + 1] * row_lane<e + 1>(vs[grp]));
+                });
+#pragma unroll
+                for (int g = grp * PER; g < (grp + 1) * PER; ++g)
+                    o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        __builtin_bit_cast(h8, vt[buf][32 * g + r32][vpiece[2 * x + m2]]), __builtin_bit_cast(h8, y), o[g], 0, 0, 0);
+            });
+        });
+    };
+
+    const auto compute = [&](int step, auto bc) {
+        constexpr int buf = decltype(bc)::value;
+        const int t0 = step * kKeys;
+        if (t0 >= hi_any || t0 + (kKeys - 1) < lo_any)
+            return;
+        float ks[2][NG], vs[2][NG];
+        uint32_t big = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                ks[x][g] = ksc[buf][g][32 * x + lane_key];
+                vs[x][g] = vsc[buf][g][32 * x + lane_key];
+                big = max(big, __float_as_uint(vs[x][g]));
+            }
+        if (__ballot(big >= scale_cap)) {                // rare: values larger than any before
+            big = max_rows_u32(group_max_u32<16>(big));
+            scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
+            scale_cap = (uint32_t)(scale_exp + 128) << 23;
+            bound = ref + (float)(kRange - scale_exp);
+        }
+        const bool some_hidden = t0 < lo_all || t0 + kKeys > hi_all || __ballot(fminf(ks[0][0], ks[1][0]) < 0.0f);
+        const float ks0 = ks[0][0], ks1 = ks[1][0];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+                ks[x][g] *= score_scale;
+        float s0[16], s1[16];
+        scores(s0, ks[0], 0, bc);
+        scores(s1, ks[1], 1, bc);
+        if (some_hidden) {
+            hide(s0, ks0, t0);
+            hide(s1, ks1, t0 + 32);
+        }
+        const float m = max3(largest(s0), largest(s1), -INFINITY);
+        if (__ballot(m > bound))                         // rare after the first tiles
+            rescale(m);
+        // keeps the lane moves of the scales in this block, where they fold into the products
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int g = 0; g < NG; ++g)
                 asm("" : "+v"(vs[x][g]));
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                s[x][e] = exp2_hw(s[x][e] - nref);
-                sum[e % 4] += s[x][e];
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            each<2>([&](auto mc) {
-                constexpr int m2 = decltype(mc)::value;
-                each<NG>([&](auto gc) {
-                    constexpr int grp = decltype(gc)::value;
-                    u32x4 y;                             // weight times the value's scale, the one rounding to fp16
-                    each<4>([&](auto ic) {
-                        constexpr int e = 8 * m2 + 2 * decltype(ic)::value;
-                        y[decltype(ic)::value] = pack_h2(s[x][e] * row_lane<e>(vs[x][grp]), s[x][e + 1] * row_lane<e + 1>(vs[x][grp]));
-                    });
-#pragma unroll
-                    for (int g = grp * PER; g < (grp + 1) * PER; ++g)
-                        o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            __builtin_bit_cast(h8, vt[buf][32 * g + r32][vpiece[2 * x + m2]]),
-                            __builtin_bit_cast(h8, y), o[g], 0, 0, 0);
-                });
-            });
-        }
+        weights(s0);
+        output(s0, vs[0], 0, bc);
+        weights(s1);
+        output(s1, vs[1], 1, bc);
     };
 
     if (s0 < s1) {
@@ -420,33 +462,35 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         last = arrive(counter, parts) ? 1 : 0;
     __syncthreads();
     if (last)
-        join_parts<D>(w, a, seq, head, row0, rows_here, slot0, parts, reinterpret_cast<float *>(&kt[0][0][0]));
+        join_parts<D, 64 * WV>(w, a, seq, head, row0, rows_here, slot0, parts, reinterpret_cast<float *>(&kt[0][0][0]));
 }
 
 }  // namespace
 
 void launch_kv4_prefill(const Kv4Cache &c, const Kv4AttnArgs &a, int row_limit, void *workspace, hipStream_t st)
 {
-    const Kv4Tiles t = kv4_prefill_tiles(a.T, a.B, a.group, c.heads, (int64_t)a.max_pages << c.shift);
+    const int rows = kv4_tile_rows(a.T, a.group, c.heads, c.D);
+    const Kv4Tiles t = kv4_prefill_tiles(a.T, a.B, a.group, c.heads, (int64_t)a.max_pages << c.shift, rows);
     Partial w;
     w.grid = (int)t.grid;
     w.row_limit = row_limit;
-    w.slot_rows = kRows;
+    w.slot_rows = rows;
     w.slots = (int)t.slots;
     w.over_group = over_group(a.group);
     w.counters = static_cast<uint64_t *>(workspace);
     w.base = reinterpret_cast<float *>(static_cast<char *>(workspace) + kv4_counter_bytes(t.slots, 1));
-    const dim3 grid((unsigned)t.grid), block(kThreads);
+    const dim3 grid((unsigned)t.grid), block(2 * rows);
     const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, c, a, w); };
+    const bool wide = rows == 256;
     switch (c.D * 8 + c.D / c.G) {
-    case 64 * 8 + 1: launch(kv4_prefill_kernel<64, 1>); return;
-    case 64 * 8 + 2: launch(kv4_prefill_kernel<64, 2>); return;
-    case 128 * 8 + 1: launch(kv4_prefill_kernel<128, 1>); return;
-    case 128 * 8 + 2: launch(kv4_prefill_kernel<128, 2>); return;
-    case 128 * 8 + 4: launch(kv4_prefill_kernel<128, 4>); return;
-    case 256 * 8 + 1: launch(kv4_prefill_kernel<256, 1>); return;
-    case 256 * 8 + 2: launch(kv4_prefill_kernel<256, 2>); return;
-    default: launch(kv4_prefill_kernel<256, 4>); return;
+    case 64 * 8 + 1: launch(wide ? kv4_prefill_kernel<64, 1, 8> : kv4_prefill_kernel<64, 1, 4>); return;
+    case 64 * 8 + 2: launch(wide ? kv4_prefill_kernel<64, 2, 8> : kv4_prefill_kernel<64, 2, 4>); return;
+    case 128 * 8 + 1: launch(wide ? kv4_prefill_kernel<128, 1, 8> : kv4_prefill_kernel<128, 1, 4>); return;
+    case 128 * 8 + 2: launch(wide ? kv4_prefill_kernel<128, 2, 8> : kv4_prefill_kernel<128, 2, 4>); return;
+    case 128 * 8 + 4: launch(wide ? kv4_prefill_kernel<128, 4, 8> : kv4_prefill_kernel<128, 4, 4>); return;
+    case 256 * 8 + 1: launch(kv4_prefill_kernel<256, 1, 4>); return;
+    case 256 * 8 + 2: launch(kv4_prefill_kernel<256, 2, 4>); return;
+    default: launch(kv4_prefill_kernel<256, 4, 4>); return;
     }
 }
 
