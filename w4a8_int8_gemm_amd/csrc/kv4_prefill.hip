@@ -13,8 +13,7 @@
 // while the next tile's codes are on their way.  S^T = K Q^T on 32x32x16
 // matrix instructions leaves a lane with one query row and runs of four keys,
 // which is the operand of O^T = V^T P^T if V^T's keys lie in that order: they
-// do, eight keys of two such runs in one 16-byte piece.  Rows of both tiles
-// are swizzled so that 16 lanes' pieces cover all banks.
+// do, eight keys of two such runs in one 16-byte piece.
 //
 // Where the rows alone do not fill the chip a (sequence, head, rows) tile's
 // keys are cut into parts of equal width, joined as in the kernel for few rows.
@@ -28,25 +27,18 @@ namespace {
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kKeys = 64;
-constexpr int kHeadroom = 11, kRange = 14;    // binades of a row's largest weight over its scale: when set, at most
+constexpr int kHeadroom = 12, kRange = 14;    // binades of a row's largest weight over its scale: when set, at most
 constexpr float kFarBelow = -1e30f;           // under every score
 
-// Piece `c` of 16 bytes in a row of N pieces, moved so that the same piece of 16
-// consecutive rows (of N / 2 pairs of rows where a row is half the banks) is
-// on different banks.
-template <int N> __device__ __forceinline__ int swizzle(int row, int c)
-{
-    return N >= 16 ? c ^ (row & 15) : c ^ ((row >> 1) & 7);
-}
-
 template <int D, int NG, int WV>
-__global__ __launch_bounds__(64 * WV, D < 256 ? 8 / WV : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
+__global__ __launch_bounds__(64 * WV, D < 256 ? 2 : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
 {
     constexpr int N32 = D / 32, PER = N32 / NG, KC = D / 8, VC = kKeys / 8;
     constexpr int kRows = 32 * WV;
     constexpr int SPLIT = WV / 4, NV = N32 / SPLIT;      // producers: threads that share a word of V; its bytes of one
-    __shared__ u32x4 kt[2][kKeys][KC];                   // fp16 codes [key][dim], pieces of 8 dims
-    __shared__ u32x4 vt[2][D][VC];                       // fp16 codes [dim][key], pieces of 8 keys
+    // a piece more in a row than it holds: 16 rows' pieces are on different banks
+    __shared__ u32x4 kt[2][kKeys][KC + 1];               // fp16 codes [key][dim], pieces of 8 dims
+    __shared__ u32x4 vt[2][D][VC + 1];                   // fp16 codes [dim][key], pieces of 8 keys
     __shared__ float ksc[2][NG][kKeys], vsc[2][NG][kKeys];
     __shared__ int last;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -225,9 +217,9 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 8 / WV : 1) void kv4_prefill_ker
                 constexpr int g = decltype(gc)::value, W = NV > 4 ? 2 : 1, o = g / 4;
                 const uint32_t x0 = byte_pair<g % 4>(code[0 * W + o], code[1 * W + o]), x1 = byte_pair<g % 4>(code[2 * W + o], code[3 * W + o]);
                 const uint32_t x2 = byte_pair<g % 4>(code[4 * W + o], code[5 * W + o]), x3 = byte_pair<g % 4>(code[6 * W + o], code[7 * W + o]);
-                const int d = 32 * (g + NV * vpart) + 2 * r, at = swizzle<VC>(d, piece);
-                vt[buf][d][at] = (u32x4){codes_low(x0), codes_low(x1), codes_low(x2), codes_low(x3)};
-                vt[buf][d + 1][at] = (u32x4){codes_high(x0), codes_high(x1), codes_high(x2), codes_high(x3)};
+                const int d = 32 * (g + NV * vpart) + 2 * r;
+                vt[buf][d][piece] = (u32x4){codes_low(x0), codes_low(x1), codes_low(x2), codes_low(x3)};
+                vt[buf][d + 1][piece] = (u32x4){codes_high(x0), codes_high(x1), codes_high(x2), codes_high(x3)};
             });
             if (r < 8 && vpart == 0) {
 #pragma unroll
@@ -241,7 +233,7 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 8 / WV : 1) void kv4_prefill_ker
                 const int key = (u >> 2) + 32 * x;
 #pragma unroll
                 for (int i = 0; i < N32; ++i)
-                    kt[buf][key][swizzle<KC>(key, 4 * i + b4)] = __builtin_bit_cast(u32x4, codes8(code[N32 * x + i]));
+                    kt[buf][key][4 * i + b4] = __builtin_bit_cast(u32x4, codes8(code[N32 * x + i]));
                 if (b4 == 0) {
 #pragma unroll
                     for (int g = 0; g < NG; ++g)
@@ -268,33 +260,29 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 8 / WV : 1) void kv4_prefill_ker
     const float score_scale = a.scale * kLog2e;
     // key of lane % 16 in the runs of four that the lane's half has of 32 keys
     const int lane_key = (lane & 15) / 4 * 8 + 4 * h + (lane & 3);
-    // a row's pieces where the swizzle puts them; rows 32 apart have the same
-    int kpiece[D / 16], vpiece[4];
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k)
-        kpiece[k] = swizzle<KC>(r32, 2 * k + h);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        vpiece[k] = swizzle<VC>(r32, 2 * k + h);
-
     // Scores of 32 keys: lane's row, keys 8 (e / 4) + 4 h + e % 4 of them.
-    const auto scores = [&](float (&s)[16], const float (&ks)[NG], int x, auto bc) {
-        constexpr int buf = decltype(bc)::value;
+    const auto products = [&](v16f &acc, auto xc, auto gc, auto bc) {
+        constexpr int x = decltype(xc)::value, g = decltype(gc)::value, buf = decltype(bc)::value;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            acc[e] = 0.0f;
+#pragma unroll
+        for (int k = g * 2 * PER; k < (g + 1) * 2 * PER; ++k)
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kt[buf][32 * x + r32][2 * k + h]), q[k], acc,
+                                                         0, 0, 0);
+    };
+    const auto scale_scores = [&](float (&s)[16], const v16f &acc, float ks, auto gc) {
+        each<16>([&](auto ec) {
+            constexpr int e = decltype(ec)::value;
+            const float f = row_lane<e>(ks);
+            s[e] = decltype(gc)::value == 0 ? acc[e] * f : fmaf(acc[e], f, s[e]);
+        });
+    };
+    const auto scores = [&](float (&s)[16], const float (&ks)[NG], auto xc, auto bc) {
         each<NG>([&](auto gc) {
-            constexpr int g = decltype(gc)::value;
             v16f acc;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                acc[e] = 0.0f;
-#pragma unroll
-            for (int k = g * 2 * PER; k < (g + 1) * 2 * PER; ++k)
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, kt[buf][32 * x + r32][kpiece[k]]), q[k],
-                                                             acc, 0, 0, 0);
-            each<16>([&](auto ec) {
-                constexpr int e = decltype(ec)::value;
-                const float f = row_lane<e>(ks[g]);
-                s[e] = g == 0 ? acc[e] * f : fmaf(acc[e], f, s[e]);
-            });
+            products(acc, xc, gc, bc);
+            scale_scores(s, acc, ks[decltype(gc)::value], gc);
         });
     };
     const auto hide = [&](float (&s)[16], float ks0, int t0) {
@@ -313,10 +301,12 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 8 / WV : 1) void kv4_prefill_ker
             m = max3(m, s[e], s[e + 1]);
         return max3(m, s[15], s[15]);
     };
-    const auto rescale = [&](float m) {
+    // References are whole, so that a factor is a power of two and the pending
+    // weights w (of `pending` operands) keep their bits.
+    const auto rescale = [&](float m, h8 *w, int pending) {
         m = max_halves(m);
         if (m > bound) {
-            const float nref = m + (float)(scale_exp - kHeadroom);
+            const float nref = ceilf(m) + (float)(scale_exp - kHeadroom);
             const float alpha = exp2_hw(ref - nref);     // 0 before the first key
             l *= alpha;
             ref = nref;
@@ -326,6 +316,11 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 8 / WV : 1) void kv4_prefill_ker
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     o[g][e] *= alpha;
+#pragma unroll
+            for (int i = 0; i < pending; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    w[i][e] = (_Float16)((float)w[i][e] * alpha);
         }
     };
     const auto weights = [&](float (&s)[16]) {
@@ -337,25 +332,30 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 8 / WV : 1) void kv4_prefill_ker
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
-    const auto output = [&](const float (&s)[16], const float (&vs)[NG], int x, auto bc) {
-        constexpr int buf = decltype(bc)::value;
+    // Weight times the value's scale, the one rounding to fp16: the operands of 32 keys.
+    const auto operands = [&](h8 (&w)[2][NG], const float (&s)[16], const float (&vs)[NG]) {
         each<2>([&](auto mc) {
             constexpr int m2 = decltype(mc)::value;
             each<NG>([&](auto gc) {
                 constexpr int grp = decltype(gc)::value;
-                u32x4 y;                                 // weight times the value's scale, the one rounding to fp16
+                u32x4 y;
                 each<4>([&](auto ic) {
                     constexpr int e = 8 * m2 + 2 * decltype(ic)::value;
                     y[decltype(ic)::value] = pack_h2(s[e] * row_lane<e>(vs[grp]), s[e + 1] * row_lane<e + 1>(vs[grp]));
                 });
-#pragma unroll
-                for (int g = grp * PER; g < (grp + 1) * PER; ++g)
-                    o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        __builtin_bit_cast(h8, vt[buf][32 * g + r32][vpiece[2 * x + m2]]), __builtin_bit_cast(h8, y), o[g], 0, 0, 0);
+                w[m2][grp] = __builtin_bit_cast(h8, y);
             });
         });
     };
-
+    const auto output = [&](const h8 (&w)[2][NG], auto xc, auto bc) {
+        constexpr int x = decltype(xc)::value, buf = decltype(bc)::value;
+#pragma unroll
+        for (int m2 = 0; m2 < 2; ++m2)
+#pragma unroll
+            for (int g = 0; g < N32; ++g)
+                o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                    __builtin_bit_cast(h8, vt[buf][32 * g + r32][2 * (2 * x + m2) + h]), w[m2][g / PER], o[g], 0, 0, 0);
+    };
     const auto compute = [&](int step, auto bc) {
         constexpr int buf = decltype(bc)::value;
         const int t0 = step * kKeys;
@@ -384,26 +384,35 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 8 / WV : 1) void kv4_prefill_ker
 #pragma unroll
             for (int g = 0; g < NG; ++g)
                 ks[x][g] *= score_scale;
+        const std::integral_constant<int, 0> first_half;
+        const std::integral_constant<int, 1> second_half;
         float s0[16], s1[16];
-        scores(s0, ks[0], 0, bc);
-        scores(s1, ks[1], 1, bc);
-        if (some_hidden) {
+        h8 w0[2][NG], w1[2][NG];
+        scores(s0, ks[0], first_half, bc);
+        if (some_hidden)
             hide(s0, ks0, t0);
-            hide(s1, ks1, t0 + 32);
-        }
-        const float m = max3(largest(s0), largest(s1), -INFINITY);
-        if (__ballot(m > bound))                         // rare after the first tiles
-            rescale(m);
+        const float m0 = largest(s0);
+        if (__ballot(m0 > bound))                        // rare after the first tiles
+            rescale(m0, nullptr, 0);
         // keeps the lane moves of the scales in this block, where they fold into the products
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-                asm("" : "+v"(vs[x][g]));
+        for (int g = 0; g < NG; ++g)
+            asm("" : "+v"(vs[0][g]), "+v"(ks[1][g]));
+        scores(s1, ks[1], second_half, bc);
         weights(s0);
-        output(s0, vs[0], 0, bc);
+        operands(w0, s0, vs[0]);
+        if (some_hidden)
+            hide(s1, ks1, t0 + 32);
+        const float m1 = largest(s1);
+        if (__ballot(m1 > bound))
+            rescale(m1, &w0[0][0], 2 * NG);
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            asm("" : "+v"(vs[1][g]));
+        output(w0, first_half, bc);
         weights(s1);
-        output(s1, vs[1], 1, bc);
+        operands(w1, s1, vs[1]);
+        output(w1, second_half, bc);
     };
 
     if (s0 < s1) {
