@@ -454,10 +454,10 @@ uint64_t next_tag()
     return (tag.fetch_add(1, std::memory_order_relaxed) | (uint64_t(1) << 47)) << 16;
 }
 
-// T tokens of a cache: one lane takes 8 elements, 2^31 workgroups of 256 at most.
+// T tokens of a cache: four lanes a row, numbered in 32 bits.
 w4a8_status_t check_tokens(const char *fn, int64_t T, const kv4_cache_t *c)
 {
-    if (T < 0 || T > kMaxDim || T * c->kv_heads > kMaxDim)
+    if (T < 0 || T > kMaxDim || T * c->kv_heads > (1 << 29))
         return fail(W4A8_ERR_INVALID_ARG, "%s: T=%lld out of range", fn, (long long)T);
     return W4A8_OK;
 }

@@ -31,9 +31,8 @@ size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int 
     size_t bytes = decode_bytes(q_heads, kv_heads, D, T, B, max_q);
     if ((int64_t)group * (max_q < T ? max_q : T) > kv4_decode_limit(D)) {
         // any length of keys: the table's width is not known here
-        const int rows = kv4_tile_rows(T, group, kv_heads, D);
-        const Kv4Tiles t = kv4_prefill_tiles(T, B, group, kv_heads, int64_t(1) << 30, rows);
-        bytes += kv4_counter_bytes(t.slots, 1) + (size_t)t.slots * rows * (D + 2) * sizeof(float);
+        const Kv4Tiles t = kv4_prefill_tiles(T, B, group, kv_heads, int64_t(1) << 30);
+        bytes += kv4_counter_bytes(t.slots, 1) + (size_t)t.slots * kTileRows * (D + 2) * sizeof(float);
     }
     return bytes;
 }
@@ -41,8 +40,10 @@ size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int 
 void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st)
 {
     const int limit = kv4_decode_limit(c.D);
-    const bool few = a.group <= limit, many = (int64_t)a.group * a.max_q > limit;
-    // every sequence has more rows than the kernel for few takes: one query is too many for it
+    const bool many = (int64_t)a.group * a.max_q > limit;
+    // Where all sequences have max_q queries, or one query is too many rows for
+    // the kernel for few, the other kernel takes them all.
+    const bool few = a.group <= limit && !(many && a.T == (int64_t)a.B * a.max_q);
     if (few)
         launch_kv4_decode(c, a, decode_rows(c.D, a.group, a.max_q), st);
     if (many)

@@ -3,23 +3,18 @@
 //
 // Both are bound by HBM: the writer reads 2 bytes and writes 1/2 (+ 4 / G) per
 // element, the reader the other way round.
+//
+// Four neighbouring lanes have a (token, head) row of K or V, lane b the
+// elements 32 g + 8 b ..+7 of every 32: 16 bytes of fp16 for each g, and in
+// the cache, whose rows are stored transposed, D / 8 bytes in one run (K's
+// words b n .. b n + n - 1; V's bytes 4 b n .. 4 b n + 4 n - 1, after a
+// transposition of 4 x 4 bytes in registers).  A scale's maximum is taken over
+// a lane's own elements and the four lanes.
 #include "kv4.hpp"
 
 namespace w4a8 {
 
 namespace {
-
-// Maximum over groups of W consecutive lanes (4, 8, 16 or 32).
-template <int W>
-__device__ __forceinline__ uint32_t scale_group_max(uint32_t v)
-{
-    if constexpr (W == 32) {
-        v = group_max_u32<16>(v);
-        return max(v, (uint32_t)__shfl_xor((int)v, 16));
-    } else {
-        return group_max_u32<W>(v);
-    }
-}
 
 // Eight codes (bytes, k = 0..7) to eight nibbles, element 0 lowest.
 __device__ __forceinline__ uint32_t pack_nibbles(uint2 c)
@@ -29,90 +24,180 @@ __device__ __forceinline__ uint32_t pack_nibbles(uint2 c)
     return (x & 0xffu) | ((x >> 8) & 0xff00u) | ((y & 0xffu) << 16) | ((y << 8) & 0xff000000u);
 }
 
-// One lane per 8 elements of a (token, head) row; G / 8 neighbouring lanes share a scale.
-template <int G>
-__global__ __launch_bounds__(256) void kv4_write_kernel(const uint16_t *__restrict__ k,
-                                                        int64_t k_stride,
-                                                        const uint16_t *__restrict__ v,
-                                                        int64_t v_stride,
-                                                        const int64_t *__restrict__ slots,
-                                                        int64_t T, Kv4Cache c)
+// Byte i of word j becomes byte j of word i.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4])
 {
-    const int per = c.D / 8, n = c.D / 32;
-    const int64_t work = T * c.heads * per;
-    const int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const bool inside = w < work;
-    const int64_t wc = inside ? w : work - 1;
-    const int chunk = (int)(wc % per);
-    const int64_t th = wc / per;
-    const int head = (int)(th % c.heads);
-    const int64_t t = th / c.heads;
-    const int64_t slot = slots[t];
-    const bool write = inside && slot >= 0 && slot < (c.pages << c.shift);
-    const int64_t row = c.row(slot >> c.shift, head, (int)(slot & ((1 << c.shift) - 1)));
+    const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+    const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+    w[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+    w[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+    w[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+    w[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+// A lane's natural words (word g: elements 32 g + 8 b ..+7) of a V row to its
+// stored ones, whose bytes run over g first; and back.
+template <int N> __device__ __forceinline__ void v_stored(uint32_t (&w)[N])
+{
+    if constexpr (N == 2) {
+        const uint32_t a = w[0], b = w[1];
+        w[0] = __builtin_amdgcn_perm(b, a, 0x05010400u);
+        w[1] = __builtin_amdgcn_perm(b, a, 0x07030602u);
+    } else if constexpr (N == 4) {
+        transpose4(w);
+    } else {
+        uint32_t a[4] = {w[0], w[1], w[2], w[3]}, b[4] = {w[4], w[5], w[6], w[7]};
+        transpose4(a);
+        transpose4(b);
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        const uint16_t *src = (kv ? v + t * v_stride : k + t * k_stride) + head * c.D + chunk * 8;
-        const uint4 x = load_nt(reinterpret_cast<const uint4 *>(src));
-        const uint32_t m = scale_group_max<G / 8>(absmax_bits8(x));
-        const float s = quant_scale(h2f((uint16_t)m), 7.0f);
-        if (!write)
-            continue;
-        if (chunk % (G / 8) == 0)
-            (kv ? c.vs : c.ks)[row * (c.D / G) + chunk / (G / 8)] = s;
-        const uint32_t word = pack_nibbles(quant_chunk8(x, s, 1.0f / s, 7.0f));
-        const int g = chunk / 4, b = chunk % 4;
-        if (kv == 0) {
-            *reinterpret_cast<uint32_t *>(c.k + row * (c.D / 2) + (b * n + g) * 4) = word;
-        } else {
-            uint8_t *dst = c.v + row * (c.D / 2) + g;
+        for (int e = 0; e < 4; ++e)
+            w[2 * e] = a[e], w[2 * e + 1] = b[e];
+    }
+}
+template <int N> __device__ __forceinline__ void v_natural(uint32_t (&w)[N])
+{
+    if constexpr (N == 2) {
+        const uint32_t a = w[0], b = w[1];
+        w[0] = __builtin_amdgcn_perm(b, a, 0x06040200u);
+        w[1] = __builtin_amdgcn_perm(b, a, 0x07050301u);
+    } else if constexpr (N == 4) {
+        transpose4(w);
+    } else {
+        uint32_t a[4] = {w[0], w[2], w[4], w[6]}, b[4] = {w[1], w[3], w[5], w[7]};
+        transpose4(a);
+        transpose4(b);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                dst[(4 * b + e) * n] = (uint8_t)(word >> (8 * e));
+        for (int g = 0; g < 4; ++g)
+            w[g] = a[g], w[4 + g] = b[g];
+    }
+}
+
+template <int N> __device__ __forceinline__ void store_words(uint8_t *p, const uint32_t (&w)[N])
+{
+    if constexpr (N == 2) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+}
+template <int N> __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
+{
+    if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const uint4 x = reinterpret_cast<const uint4 *>(p)[i];
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
         }
     }
 }
 
-// One lane per 8 elements of a (token, head) row.
-__global__ __launch_bounds__(256) void kv4_read_kernel(Kv4Cache c, const int64_t *__restrict__ slots,
-                                                       int64_t T, uint16_t *__restrict__ k,
-                                                       uint16_t *__restrict__ v)
+// grid.y: K, V
+template <int D, int NG>
+__global__ __launch_bounds__(256) void kv4_write_kernel(const uint16_t *__restrict__ k, int64_t k_stride,
+                                                        const uint16_t *__restrict__ v, int64_t v_stride,
+                                                        const int64_t *__restrict__ slots, int64_t T, Kv4Cache c)
 {
-    const int per = c.D / 8, n = c.D / 32;
-    const int64_t w = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (w >= T * c.heads * per)
+    constexpr int N = D / 32, PER = N / NG;
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x, row_of = i >> 2, b = i & 3;
+    const int64_t t = row_of / (uint32_t)c.heads;
+    const int head = row_of % (uint32_t)c.heads;
+    if (t >= T)                                          // whole groups of four lanes
         return;
-    const int chunk = (int)(w % per);
-    const int64_t th = w / per;
-    const int head = (int)(th % c.heads);
-    const int64_t slot = slots[th / c.heads];
+    const bool is_v = blockIdx.y != 0;
+    const uint16_t *src = (is_v ? v + t * v_stride : k + t * k_stride) + head * D + 8 * b;
+    uint4 x[N];
+#pragma unroll
+    for (int g = 0; g < N; ++g)
+        x[g] = load_nt(reinterpret_cast<const uint4 *>(src + 32 * g));
+    const int64_t slot = slots[t];
+    if (slot < 0 || slot >= (c.pages << c.shift))
+        return;
+    float s[NG];
+    uint32_t w[N];
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int g = q * PER; g < (q + 1) * PER; ++g)
+            m = max(m, absmax_bits8(x[g]));
+        s[q] = quant_scale(h2f((uint16_t)group_max_u32<4>(m)), 7.0f);
+        const float r = 1.0f / s[q];
+#pragma unroll
+        for (int g = q * PER; g < (q + 1) * PER; ++g)
+            w[g] = pack_nibbles(quant_chunk8(x[g], s[q], r, 7.0f));
+    }
+    if (is_v)
+        v_stored(w);
+    const int64_t row = c.row(slot >> c.shift, head, (int)(slot & ((1 << c.shift) - 1)));
+    store_words(((is_v ? c.v : c.k) + row * (D / 2)) + b * (D / 8), w);
+    float *sp = (is_v ? c.vs : c.ks) + row * NG;
+#pragma unroll
+    for (int q = 0; q < NG; ++q)
+        if (b == q)
+            sp[q] = s[q];
+}
+
+// grid.y: K, V
+template <int D, int NG>
+__global__ __launch_bounds__(256) void kv4_read_kernel(Kv4Cache c, const int64_t *__restrict__ slots, int64_t T,
+                                                       uint16_t *__restrict__ k, uint16_t *__restrict__ v)
+{
+    constexpr int N = D / 32, PER = N / NG;
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x, row_of = i >> 2, b = i & 3;
+    const int64_t t = row_of / (uint32_t)c.heads;
+    const int head = row_of % (uint32_t)c.heads;
+    if (t >= T)
+        return;
+    const bool is_v = blockIdx.y != 0;
+    const int64_t slot = slots[t];
     const bool there = slot >= 0 && slot < (c.pages << c.shift);
-    const int64_t row =
-        there ? c.row(slot >> c.shift, head, (int)(slot & ((1 << c.shift) - 1))) : 0;
-    const int g = chunk / 4, b = chunk % 4;
+    uint32_t w[N];
+    float s[NG];
+    if (there) {
+        const int64_t row = c.row(slot >> c.shift, head, (int)(slot & ((1 << c.shift) - 1)));
+        load_words(w, (is_v ? c.v : c.k) + row * (D / 2) + b * (D / 8));
+        const float *sp = (is_v ? c.vs : c.ks) + row * NG;
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        uint4 y = make_uint4(0u, 0u, 0u, 0u);
-        if (there) {
-            const float s = (kv ? c.vs : c.ks)[row * (c.D / c.G) + chunk * 8 / c.G];
-            uint32_t word;
-            if (kv == 0) {
-                word = *reinterpret_cast<const uint32_t *>(c.k + row * (c.D / 2) + (b * n + g) * 4);
-            } else {
-                const uint8_t *src = c.v + row * (c.D / 2) + g;
-                word = 0;
+        for (int q = 0; q < NG; ++q)
+            s[q] = sp[q];
+    } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    word |= (uint32_t)src[(4 * b + e) * n] << (8 * e);
-            }
-            float f[8];
+        for (int g = 0; g < N; ++g)
+            w[g] = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                f[e] = (float)((int32_t)(word << (28 - 4 * e)) >> 28) * s;
-            y = make_uint4(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]), pack_h2(f[4], f[5]),
-                           pack_h2(f[6], f[7]));
-        }
-        *reinterpret_cast<uint4 *>((kv ? v : k) + th * c.D + chunk * 8) = y;
+        for (int q = 0; q < NG; ++q)
+            s[q] = 0.0f;
+    }
+    if (is_v)
+        v_natural(w);
+    uint16_t *dst = (is_v ? v : k) + (int64_t)row_of * D + 8 * b;
+#pragma unroll
+    for (int g = 0; g < N; ++g) {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = (float)((int32_t)(w[g] << (28 - 4 * e)) >> 28) * s[g / PER];
+        *reinterpret_cast<uint4 *>(dst + 32 * g) =
+            make_uint4(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]), pack_h2(f[4], f[5]), pack_h2(f[6], f[7]));
+    }
+}
+
+template <typename F> void each_geometry(const Kv4Cache &c, F &&f)
+{
+    switch (c.D * 8 + c.D / c.G) {
+    case 64 * 8 + 1: f(std::integral_constant<int, 64>(), std::integral_constant<int, 1>()); return;
+    case 64 * 8 + 2: f(std::integral_constant<int, 64>(), std::integral_constant<int, 2>()); return;
+    case 128 * 8 + 1: f(std::integral_constant<int, 128>(), std::integral_constant<int, 1>()); return;
+    case 128 * 8 + 2: f(std::integral_constant<int, 128>(), std::integral_constant<int, 2>()); return;
+    case 128 * 8 + 4: f(std::integral_constant<int, 128>(), std::integral_constant<int, 4>()); return;
+    case 256 * 8 + 1: f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>()); return;
+    case 256 * 8 + 2: f(std::integral_constant<int, 256>(), std::integral_constant<int, 2>()); return;
+    default: f(std::integral_constant<int, 256>(), std::integral_constant<int, 4>()); return;
     }
 }
 
@@ -121,24 +206,20 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4Cache c, const int64_t
 void launch_kv4_write(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
                       const int64_t *slots, int64_t T, const Kv4Cache &c, hipStream_t st)
 {
-    const unsigned blocks = (unsigned)((T * c.heads * (c.D / 8) + 255) / 256);
-    const auto launch = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(blocks), dim3(256), 0, st, k, k_stride, v, v_stride, slots,
-                           T, c);
-    };
-    switch (c.G) {
-    case 32: launch(kv4_write_kernel<32>); return;
-    case 64: launch(kv4_write_kernel<64>); return;
-    case 128: launch(kv4_write_kernel<128>); return;
-    default: launch(kv4_write_kernel<256>); return;
-    }
+    const dim3 grid((unsigned)((T * c.heads * 4 + 255) / 256), 2);
+    each_geometry(c, [&](auto d, auto ng) {
+        hipLaunchKernelGGL((kv4_write_kernel<decltype(d)::value, decltype(ng)::value>), grid, dim3(256), 0, st, k, k_stride,
+                           v, v_stride, slots, T, c);
+    });
 }
 
-void launch_kv4_read(const Kv4Cache &c, const int64_t *slots, int64_t T, uint16_t *k, uint16_t *v,
-                     hipStream_t st)
+void launch_kv4_read(const Kv4Cache &c, const int64_t *slots, int64_t T, uint16_t *k, uint16_t *v, hipStream_t st)
 {
-    const unsigned blocks = (unsigned)((T * c.heads * (c.D / 8) + 255) / 256);
-    hipLaunchKernelGGL(kv4_read_kernel, dim3(blocks), dim3(256), 0, st, c, slots, T, k, v);
+    const dim3 grid((unsigned)((T * c.heads * 4 + 255) / 256), 2);
+    each_geometry(c, [&](auto d, auto ng) {
+        hipLaunchKernelGGL((kv4_read_kernel<decltype(d)::value, decltype(ng)::value>), grid, dim3(256), 0, st, c, slots, T, k,
+                           v);
+    });
 }
 
 }  // namespace w4a8

@@ -86,29 +86,28 @@ KV4_HD int64_t kv4_decode_grid(int64_t B, int heads, int64_t most)
     return pairs * (each - 1) < kPartsMore ? pairs * each : pairs + kPartsMore;
 }
 
-// The same for tiles of rows: an item is a (sequence, head) pair's tile of rows, a sequence's items are cut alike.  Parts of items that are cut number
-// at most 2 kTilesMore (ceil(x) < 2 x for x > 1).
-constexpr int kTilesMore = 512;
+// The same for tiles of kTileRows rows: an item is a (sequence, head) pair's
+// tile, a sequence's items are cut alike.  A part is at most an even share of
+// a compute unit (joining large parts costs more than an uneven end), and not
+// under kLeastTileKeys keys.  Parts of items that are cut number at most
+// 2 kTileShares (ceil(x) < 2 x for x > 1).
+constexpr int kTileRows = 128, kTileShares = 256, kLeastTileKeys = 512;
 KV4_HD int kv4_tile_limit(int64_t total, int keys)
 {
-    const int64_t l = (total + kTilesMore - 1) / kTilesMore, least = kLeastKeys / keys;
+    const int64_t l = (total + kTileShares - 1) / kTileShares, least = kLeastTileKeys / keys;
     return l < least ? (int)least : l > 0x3fffffff ? 0x3fffffff : (int)l;
 }
 // Workgroups for all parts, and slots for the parts of items that are cut, of
 // T rows in B sequences, `group` query heads a kv head, up to `most` keys.
-KV4_HD int kv4_tile_rows(int64_t T, int group, int heads, int D)
-{
-    return D < 256 && T * group * heads >= 256 * 256 ? 256 : 128;
-}
 struct Kv4Tiles {
     int64_t grid, slots;
 };
-KV4_HD Kv4Tiles kv4_prefill_tiles(int64_t T, int64_t B, int group, int heads, int64_t most, int rows)
+KV4_HD Kv4Tiles kv4_prefill_tiles(int64_t T, int64_t B, int group, int heads, int64_t most)
 {
-    const int64_t items = (T * group / rows + (B < T ? B : T)) * heads;
-    const int64_t each = (most + 63) / 64 / (kLeastKeys / 64) + 1;   // parts of one item, at most
+    const int64_t items = (T * group / kTileRows + (B < T ? B : T)) * heads;
+    const int64_t each = (most + 63) / 64 / (kLeastTileKeys / 64) + 1;   // parts of one item, at most
     Kv4Tiles t;
-    t.slots = each < 2 ? 0 : items * each < 2 * kTilesMore ? items * each : 2 * kTilesMore;
+    t.slots = each < 2 ? 0 : items * each < 2 * kTileShares ? items * each : 2 * kTileShares;
     t.grid = items + t.slots;
     return t;
 }

@@ -26,16 +26,14 @@ namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-constexpr int kKeys = 64;
+constexpr int kRows = kTileRows, kKeys = 64, kThreads = 2 * kRows;
 constexpr int kHeadroom = 12, kRange = 14;    // binades of a row's largest weight over its scale: when set, at most
 constexpr float kFarBelow = -1e30f;           // under every score
 
-template <int D, int NG, int WV>
-__global__ __launch_bounds__(64 * WV, D < 256 ? 2 : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
+template <int D, int NG>
+__global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
 {
     constexpr int N32 = D / 32, PER = N32 / NG, KC = D / 8, VC = kKeys / 8;
-    constexpr int kRows = 32 * WV;
-    constexpr int SPLIT = WV / 4, NV = N32 / SPLIT;      // producers: threads that share a word of V; its bytes of one
     // a piece more in a row than it holds: 16 rows' pieces are on different banks
     __shared__ u32x4 kt[2][kKeys][KC + 1];               // fp16 codes [key][dim], pieces of 8 dims
     __shared__ u32x4 vt[2][D][VC + 1];                   // fp16 codes [dim][key], pieces of 8 keys
@@ -138,13 +136,12 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 2 : 1) void kv4_prefill_kernel(K
     // ---- the producer's side of a thread
     const int32_t *table = a.table + (int64_t)b * a.max_pages;
     const int last_key = seq.n - 1;
-    const bool for_v = wave < WV / 2;
-    const int u = threadIdx.x & (32 * WV - 1);
-    // V: 8 keys of piece u / 16 % 8 = (half of 32 keys, 16 of it, run), bytes of word u % 16; K: key u / 4 (and 32
-    // more), words u % 4
-    const int vkey = (u >> 5 & 3) * 16 + ((u >> 4) & 1) * 4, vpart = u >> 7;   // its keys: vkey + 0..3, vkey + 8 + 0..3
+    const bool for_v = wave < 2;
+    const int u = threadIdx.x & 127;
+    // V: 8 keys of piece u / 16 = (half of 32 keys, 16 of it, run), word u % 16; K: keys u / 4 and 32 more, words u % 4
+    const int vkey = (u >> 5) * 16 + ((u >> 4) & 1) * 4;  // its keys: vkey + 0..3, vkey + 8 + 0..3
     const int pkey = for_v ? vkey : u >> 2;
-    uint32_t code[8 * (NV > 4 ? 2 : 1)];
+    uint32_t code[8 * (N32 > 4 ? 2 : 1)];
     float scale[2][NG];
     int page[2];                                         // of the next tile's keys
     bool there[2] = {false, false};                      // the loaded tile's
@@ -164,15 +161,13 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 2 : 1) void kv4_prefill_kernel(K
             const int r = u & 15, key = step * kKeys + vkey;
             const bool ok = kv4_page_ok(page[0], c.pages);
             const int64_t at = c.row(ok ? page[0] : 0, head, key & mask);
-            const uint8_t *p = c.v + at * (D / 2) + r * N32 + vpart * NV;
+            const uint8_t *p = c.v + at * (D / 2) + r * N32;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint8_t *pj = p + (j % 4 + j / 4 * 8) * (D / 2);
-                if constexpr (NV == 1) {
-                    code[j] = *pj;
-                } else if constexpr (NV == 2) {
+                if constexpr (N32 == 2) {
                     code[j] = *reinterpret_cast<const uint16_t *>(pj);
-                } else if constexpr (NV == 4) {
+                } else if constexpr (N32 == 4) {
                     code[j] = *reinterpret_cast<const uint32_t *>(pj);
                 } else {
                     const uint2 x = *reinterpret_cast<const uint2 *>(pj);
@@ -186,7 +181,7 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 2 : 1) void kv4_prefill_kernel(K
         } else {
             const int b4 = u & 3;
 #pragma unroll
-            for (int x = 0; x < 2 / SPLIT; ++x) {
+            for (int x = 0; x < 2; ++x) {
                 const int key = step * kKeys + (u >> 2) + 32 * x;
                 const bool ok = kv4_page_ok(page[x], c.pages);
                 const int64_t at = c.row(ok ? page[x] : 0, head, key & mask);
@@ -212,16 +207,16 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 2 : 1) void kv4_prefill_kernel(K
     const auto produce = [&](auto bc) {
         constexpr int buf = decltype(bc)::value;
         if (for_v) {
-            const int r = u & 15, piece = u >> 4 & 7;
-            each<NV>([&](auto gc) {
-                constexpr int g = decltype(gc)::value, W = NV > 4 ? 2 : 1, o = g / 4;
+            const int r = u & 15, piece = u >> 4;
+            each<N32>([&](auto gc) {
+                constexpr int g = decltype(gc)::value, W = N32 > 4 ? 2 : 1, o = g / 4;
                 const uint32_t x0 = byte_pair<g % 4>(code[0 * W + o], code[1 * W + o]), x1 = byte_pair<g % 4>(code[2 * W + o], code[3 * W + o]);
                 const uint32_t x2 = byte_pair<g % 4>(code[4 * W + o], code[5 * W + o]), x3 = byte_pair<g % 4>(code[6 * W + o], code[7 * W + o]);
-                const int d = 32 * (g + NV * vpart) + 2 * r;
+                const int d = 32 * g + 2 * r;
                 vt[buf][d][piece] = (u32x4){codes_low(x0), codes_low(x1), codes_low(x2), codes_low(x3)};
                 vt[buf][d + 1][piece] = (u32x4){codes_high(x0), codes_high(x1), codes_high(x2), codes_high(x3)};
             });
-            if (r < 8 && vpart == 0) {
+            if (r < 8) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
                     vsc[buf][g][vkey + r % 4 + (r >> 2) * 8] = there[0] ? scale[0][g] : 0.0f;
@@ -229,7 +224,7 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 2 : 1) void kv4_prefill_kernel(K
         } else {
             const int b4 = u & 3;
 #pragma unroll
-            for (int x = 0; x < 2 / SPLIT; ++x) {
+            for (int x = 0; x < 2; ++x) {
                 const int key = (u >> 2) + 32 * x;
 #pragma unroll
                 for (int i = 0; i < N32; ++i)
@@ -471,35 +466,33 @@ __global__ __launch_bounds__(64 * WV, D < 256 ? 2 : 1) void kv4_prefill_kernel(K
         last = arrive(counter, parts) ? 1 : 0;
     __syncthreads();
     if (last)
-        join_parts<D, 64 * WV>(w, a, seq, head, row0, rows_here, slot0, parts, reinterpret_cast<float *>(&kt[0][0][0]));
+        join_parts<D, kThreads>(w, a, seq, head, row0, rows_here, slot0, parts, reinterpret_cast<float *>(&kt[0][0][0]));
 }
 
 }  // namespace
 
 void launch_kv4_prefill(const Kv4Cache &c, const Kv4AttnArgs &a, int row_limit, void *workspace, hipStream_t st)
 {
-    const int rows = kv4_tile_rows(a.T, a.group, c.heads, c.D);
-    const Kv4Tiles t = kv4_prefill_tiles(a.T, a.B, a.group, c.heads, (int64_t)a.max_pages << c.shift, rows);
+    const Kv4Tiles t = kv4_prefill_tiles(a.T, a.B, a.group, c.heads, (int64_t)a.max_pages << c.shift);
     Partial w;
     w.grid = (int)t.grid;
     w.row_limit = row_limit;
-    w.slot_rows = rows;
+    w.slot_rows = kRows;
     w.slots = (int)t.slots;
     w.over_group = over_group(a.group);
     w.counters = static_cast<uint64_t *>(workspace);
     w.base = reinterpret_cast<float *>(static_cast<char *>(workspace) + kv4_counter_bytes(t.slots, 1));
-    const dim3 grid((unsigned)t.grid), block(2 * rows);
+    const dim3 grid((unsigned)t.grid), block(kThreads);
     const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, st, c, a, w); };
-    const bool wide = rows == 256;
     switch (c.D * 8 + c.D / c.G) {
-    case 64 * 8 + 1: launch(wide ? kv4_prefill_kernel<64, 1, 8> : kv4_prefill_kernel<64, 1, 4>); return;
-    case 64 * 8 + 2: launch(wide ? kv4_prefill_kernel<64, 2, 8> : kv4_prefill_kernel<64, 2, 4>); return;
-    case 128 * 8 + 1: launch(wide ? kv4_prefill_kernel<128, 1, 8> : kv4_prefill_kernel<128, 1, 4>); return;
-    case 128 * 8 + 2: launch(wide ? kv4_prefill_kernel<128, 2, 8> : kv4_prefill_kernel<128, 2, 4>); return;
-    case 128 * 8 + 4: launch(wide ? kv4_prefill_kernel<128, 4, 8> : kv4_prefill_kernel<128, 4, 4>); return;
-    case 256 * 8 + 1: launch(kv4_prefill_kernel<256, 1, 4>); return;
-    case 256 * 8 + 2: launch(kv4_prefill_kernel<256, 2, 4>); return;
-    default: launch(kv4_prefill_kernel<256, 4, 4>); return;
+    case 64 * 8 + 1: launch(kv4_prefill_kernel<64, 1>); return;
+    case 64 * 8 + 2: launch(kv4_prefill_kernel<64, 2>); return;
+    case 128 * 8 + 1: launch(kv4_prefill_kernel<128, 1>); return;
+    case 128 * 8 + 2: launch(kv4_prefill_kernel<128, 2>); return;
+    case 128 * 8 + 4: launch(kv4_prefill_kernel<128, 4>); return;
+    case 256 * 8 + 1: launch(kv4_prefill_kernel<256, 1>); return;
+    case 256 * 8 + 2: launch(kv4_prefill_kernel<256, 2>); return;
+    default: launch(kv4_prefill_kernel<256, 4>); return;
     }
 }
 
