@@ -6,7 +6,7 @@
 // What bounds it: HBM.  A key and value of one head take D + 8 D / G bytes
 // and 4 D operations per query row.
 //
-// One wavefront takes steps of 64 keys (32 where the registers hold no more).  S^T =
+// One wavefront takes steps of 32 keys.  S^T =
 // K Q^T on 16x16x32 matrix instructions with the codes as fp16 (exact) and the
 // keys' scales applied to the fp32 scores; the result leaves a lane with one
 // query row and four consecutive keys of each 16, which is, for two pieces of
@@ -29,18 +29,7 @@ namespace w4a8 {
 namespace {
 
 
-// The weights p = exp2(s - ref) times a value's scale have to fit fp16, whose
-// normal numbers span 30 binades.  ref = (largest score seen) + (exponent of
-// the largest scale seen) - kHeadroom puts every weight below 2^14 and lets
-// scores times scales 28 binades under the largest keep all their bits; any
-// reference gives the same quotient, so sum and output need no correction.
-constexpr int kHeadroom = 13;
-
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-
-// Pieces of 16 keys in a step: more of them share the softmax's bookkeeping,
-// where the registers hold them.
-template <int D, int RT> constexpr int kPieces = 2;
 
 // What a lane loads for a step of P pieces of 16 keys.  Of the scales, which
 // the 16 lanes of a row share, a lane takes one key's of every second piece:
@@ -121,7 +110,7 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
                                                                                                  Partial w)
 {
     constexpr int N32 = D / 32, PER = N32 / NG;          // steps of 32 dims, of one group
-    constexpr int P = kPieces<D, RT>, KEYS = 16 * P;     // pieces and keys of a step
+    constexpr int P = 2, KEYS = 16 * P;                  // pieces of 16 keys and keys of a step
     constexpr int LD = D + 4;                            // LDS row: 16 rows of float4 without bank conflicts
     __shared__ float os[kWaves][16][LD];
     __shared__ float refs[kWaves][16 * RT], ls[kWaves][16 * RT];
@@ -207,7 +196,7 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
     // ---- queries: row lane % 16 of each 16, visible keys [lo, hi)
     h8 q[RT][N32];
     int lo[RT], hi[RT];
-    float ref[RT], top[RT], l[RT];
+    float ref[RT], bound[RT], l[RT];
     v4f o[RT][2 * N32];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
@@ -220,8 +209,7 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
             q[t][k] = order8(*reinterpret_cast<const uint4 *>(qp + 32 * k));
         lo[t] = kv4_lo(seq.n, seq.m, i, a.window);
         hi[t] = kv4_hi(seq.n, seq.m, i, a.causal);
-        ref[t] = 0.0f;
-        top[t] = -INFINITY;
+        ref[t] = bound[t] = kFarBelow;
         l[t] = 0.0f;
 #pragma unroll
         for (int k = 0; k < 2 * N32; ++k)
@@ -229,6 +217,7 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
     }
     const int lo_most = kv4_lo(seq.n, seq.m, seq.m - 1, a.window), hi_least = kv4_hi(seq.n, seq.m, 0, a.causal);
     int scale_exp = kNoScale;
+    uint32_t scale_cap = 0;                              // bits of 2^(scale_exp + 1)
     const float score_scale = a.scale * kLog2e;
 
     const auto compute = [&](const Step<P, N32, NG> &cur, int step) {
@@ -290,49 +279,48 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
                     sc[h][g] = there ? sc[h][g] : 0.0f;
             }
         }
-        // the largest value scale so far
-        uint32_t big = 0;
+        uint32_t big = 0;                                // of the value scales
 #pragma unroll
         for (int h = 0; h < P / 2; ++h)
 #pragma unroll
             for (int g = 0; g < NG; ++g)
                 big = max(big, __float_as_uint(sc[h][g]));
-        big = max_rows_u32(group_max_u32<16>((r & 4) ? big : 0u));
-        scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
-        const float shift = (float)(scale_exp - kHeadroom);
+        big = (r & 4) ? big : 0u;
+        if (__ballot(big >= scale_cap)) {                // rare: values larger than any before
+            big = max_rows_u32(group_max_u32<16>(big));
+            scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
+            scale_cap = cap_of(scale_exp);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                bound[t] = ref[t] + (float)(kRange - scale_exp);
+        }
         h8 wt[RT][P / 2][NG];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             float m = max3(s[t][0][0], s[t][0][1], s[t][0][2]);
             m = max3(m, s[t][0][3], s[t][1][0]);
             m = max3(m, s[t][1][1], s[t][1][2]);
-            if constexpr (P == 2) {
-                m = max3(m, s[t][1][3], s[t][1][3]);
-            } else {
-                m = max3(m, s[t][1][3], s[t][2][0]);
-                m = max3(m, s[t][2][1], s[t][2][2]);
-                m = max3(m, s[t][2][3], s[t][3][0]);
-                m = max3(m, s[t][3][1], s[t][3][2]);
-                m = max3(m, s[t][3][3], s[t][3][3]);
-            }
-            m = max_rows(m, top[t]);
-            const float nref = (m == -INFINITY ? 0.0f : m) + shift;
-            if (__ballot(nref != ref[t])) {              // rare after the first steps
-                const float alpha = top[t] == -INFINITY ? 0.0f : exp2_hw(ref[t] - nref);
-                l[t] *= alpha;
+            m = max3(m, s[t][1][3], s[t][1][3]);
+            if (__ballot(m > bound[t])) {                // rare after the first steps
+                m = max_rows(m, m);
+                if (m > bound[t]) {
+                    const float nref = m + (float)(scale_exp - kHeadroom);
+                    const float alpha = exp2_hw(ref[t] - nref);   // 0 before the first key
+                    l[t] *= alpha;
+                    ref[t] = nref;
+                    bound[t] = nref + (float)(kRange - scale_exp);
 #pragma unroll
-                for (int k = 0; k < 2 * N32; ++k)
+                    for (int k = 0; k < 2 * N32; ++k)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[t][k][e] *= alpha;
-                ref[t] = nref;
+                        for (int e = 0; e < 4; ++e)
+                            o[t][k][e] *= alpha;
+                }
             }
-            top[t] = m;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    s[t][p][j] = exp2_hw(s[t][p][j] - nref);
+                    s[t][p][j] = exp2_hw(s[t][p][j] - ref[t]);
                 l[t] += (s[t][p][0] + s[t][p][1]) + (s[t][p][2] + s[t][p][3]);
             }
             // weight times the value's scale, the one rounding to fp16

@@ -151,7 +151,20 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 // The exponent floor(log2 v) of a scale's bits, -127 for 0.
 __device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >> 23) - 127; }
 
+// Weights p = 2^(score - ref) are multiplied with their value's scale and
+// rounded to fp16.  The reference is not the running maximum but follows it
+// where a weight could leave fp16's range: for scales below 2^(e + 1) a score
+// above `bound` = ref + kRange - e.  Then ref = (the row's largest score) + e -
+// kHeadroom, so that its weight times the largest scale is about 2^kHeadroom:
+// products stay below 2^(kRange + 1), and those 26 binades under the largest
+// keep all their bits (a row's heaviest key may have a code of 0 in some
+// element, whose result then comes from light keys alone; 7 binades of
+// headroom were too few there).  Sum and output have the same reference, and
+// any gives the same quotient.
+constexpr int kHeadroom = 12, kRange = 14;
+constexpr float kFarBelow = -1e30f;           // reference before any key: under every score
 constexpr int kNoScale = -100;                // exponent of the largest scale before any key
+__device__ __forceinline__ uint32_t cap_of(int e) { return (uint32_t)(e + 128) << 23; }   // bits of 2^(e + 1)
 
 // Values that other workgroups, on other chiplets with L2 caches of their
 // own, wrote or will read within one launch: loads and stores at device scope.

@@ -27,8 +27,6 @@ namespace {
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kRows = kTileRows, kKeys = 64, kThreads = 2 * kRows;
-constexpr int kHeadroom = 12, kRange = 14;    // binades of a row's largest weight over its scale: when set, at most
-constexpr float kFarBelow = -1e30f;           // under every score
 
 template <int D, int NG>
 __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
@@ -245,10 +243,6 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             o[g][e] = 0.0f;
-    // Weights are taken relative to `ref`, which follows the largest score only
-    // when a weight could leave fp16's range (a score above `bound`): with the
-    // values' largest scale below 2^(scale_exp + 1), weights p = 2^(score - ref)
-    // times scale stay below 2^15, and a row's largest is above 1 when set.
     float ref = kFarBelow, bound = kFarBelow, l = 0.0f;
     int scale_exp = kNoScale;
     uint32_t scale_cap = 0;                              // bits of 2^(scale_exp + 1)
@@ -369,7 +363,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         if (__ballot(big >= scale_cap)) {                // rare: values larger than any before
             big = max_rows_u32(group_max_u32<16>(big));
             scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
-            scale_cap = (uint32_t)(scale_exp + 128) << 23;
+            scale_cap = cap_of(scale_exp);
             bound = ref + (float)(kRange - scale_exp);
         }
         const bool some_hidden = t0 < lo_all || t0 + kKeys > hi_all || __ballot(fminf(ks[0][0], ks[1][0]) < 0.0f);
