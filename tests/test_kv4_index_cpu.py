@@ -18,7 +18,9 @@ def L(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", os.path.join(HERE, "native", "kv4_index_shim.cpp"),
                     "-o", so], check=True)
     lib = ctypes.CDLL(so)
-    lib.part_limit.argtypes = [ctypes.c_int64, ctypes.c_int]
+    lib.part_limit.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int]
+    lib.tile_limit.argtypes = [ctypes.c_int64, ctypes.c_int]
+    lib.tiles.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p]
     lib.decode_grid.restype = ctypes.c_int64
     lib.decode_grid.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int64]
     lib.page_ok.argtypes = [ctypes.c_int, ctypes.c_int64]
@@ -81,10 +83,10 @@ def test_parts_cover_the_steps_and_fit_the_grid(L):
         keys = r.choice([32, 64])
         B, heads, most = r.randint(1, 70), r.randint(1, 40), 16 * r.choice([0, 1, 2, 60, 65, 5000, 1 << 20])
         counts = [max(1, -(-r.choice([most, r.randint(0, most)]) // keys)) if r.random() < 0.8 else 0 for _ in range(B)]
-        limit = L.part_limit(heads * sum(counts), keys)
+        limit = L.part_limit(heads * sum(counts), max(counts), keys)
         parts = [-(-n // limit) for n in counts]
         assert heads * sum(parts) <= L.decode_grid(B, heads, most)
-        assert max(parts) <= L.parts_more() + 1 < 65536            # arrivals are counted in 16 bits
+        assert max(parts) <= 64                                    # arrivals are counted in 16 bits
         for n, k in zip(counts, parts):
             if n:
                 cuts = [L.split(n, k, i) for i in range(k + 1)]
@@ -93,8 +95,29 @@ def test_parts_cover_the_steps_and_fit_the_grid(L):
 
 
 def test_parts_at_the_ends(L):
-    assert L.part_limit(0, 32) == 32 and L.part_limit(0, 64) == 16 and L.part_limit(1 << 60, 64) == 0x3fffffff
+    assert L.part_limit(0, 0, 32) == 32 and L.part_limit(0, 0, 64) == 16 and L.part_limit(1 << 60, 5, 64) == 0x3fffffff
     assert L.split(1 << 25, 1025, 1025) == 1 << 25
+
+
+def test_tiles_fit_the_grid_and_the_slots(L):
+    """The kernel for many rows: workgroups for every part, and a slot for every part of a cut item."""
+    r = random.Random(2)
+    out = (ctypes.c_int64 * 3)()
+    for _ in range(600):
+        B, heads, group, most = r.randint(1, 70), r.randint(1, 9), r.randint(1, 9), 16 * r.choice([1, 20, 300, 70000])
+        m = [r.randint(0, 700) for _ in range(B)]
+        T = sum(m)
+        if not T:
+            continue
+        L.tiles(T, B, group, heads, most, out)
+        grid, slots, rows = out
+        tiles = [-(-q * group // rows) for q in m]
+        steps = [max(1, -(-r.choice([most, r.randint(0, most)]) // 64)) if q else 0 for q in m]
+        limit = L.tile_limit(heads * sum(t * s for t, s in zip(tiles, steps)), 64)
+        cuts = [-(-s // limit) for s in steps]
+        assert heads * sum(t * k for t, k in zip(tiles, cuts)) <= grid
+        assert heads * sum(t * k for t, k in zip(tiles, cuts) if k > 1) <= slots
+        assert max(cuts) < 65536
 
 
 def test_pages(L):

@@ -131,11 +131,13 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
         }
     };
     int64_t steps = 0;                                   // of all sequences
+    int longest = 0;                                     // of one
     for (int base = 0; base < B; base += 64) {
         lookup(base);
         steps += group_sum_u32<64>((uint32_t)nl);
+        longest = max(longest, (int)group_max_u32<64>((uint32_t)nl));
     }
-    const int limit = kv4_part_limit(steps * c.heads, KEYS);
+    const int limit = kv4_part_limit(steps * c.heads, longest, KEYS);
     int b = -1, count = 0, parts = 0, id = blockIdx.x;   // id: within the sequences from b on
     Kv4Seq seq = {0, 0, 0};
     for (int base = 0; base < B; base += 64) {

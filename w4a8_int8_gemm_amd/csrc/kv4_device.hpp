@@ -258,18 +258,19 @@ __device__ void join_parts(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq 
                 float2 rl[kAhead], u[kAhead], v[kAhead];
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
-                    const int pp = min(p + i * groups, p1);
-                    const float *src = w.base + ((int64_t)pp * w.slot_rows + row) * (D + 2);
-                    rl[i] = load_shared(src + D);
-                    u[i] = load_shared(src + d);
-                    v[i] = load_shared(src + d + 2);
+                    rl[i] = u[i] = v[i] = make_float2(0.0f, 0.0f);
+                    const int pp = p + i * groups;
+                    if (pp <= p1) {                      // each load goes to memory: none for nothing
+                        const float *src = w.base + ((int64_t)pp * w.slot_rows + row) * (D + 2);
+                        rl[i] = load_shared(src + D);
+                        u[i] = load_shared(src + d);
+                        v[i] = load_shared(src + d + 2);
+                    }
                 }
                 float top = R;
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    rl[i].y = p + i * groups <= p1 ? rl[i].y : 0.0f;
+                for (int i = 0; i < kAhead; ++i)
                     top = fmaxf(top, rl[i].y > 0.0f ? rl[i].x : -INFINITY);
-                }
                 const float keep = R == -INFINITY ? 0.0f : exp2_hw(R - top);
                 L *= keep;
                 sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;

@@ -69,14 +69,17 @@ KV4_HD Kv4Steps kv4_steps(const Kv4Seq &s, bool causal, int window, int keys)
 
 // A (sequence, head) of `count` steps is cut into ceil(count / limit) even
 // parts.  With the limit below there are at most kPartsMore more of them in
-// all than (sequence, head) pairs, for `total` steps of all pairs: two
-// workgroups a compute unit where one sequence has them all, and no part of
-// under kLeastKeys keys is made.
-constexpr int kPartsMore = 512, kLeastKeys = 1024;
-KV4_HD int kv4_part_limit(int64_t total, int keys)
+// all than (sequence, head) pairs, for `total` steps of all pairs: three
+// workgroups a compute unit.  No part of under kLeastKeys keys is made, and
+// no more than kPartsOfOne of the longest pair (`longest` steps), whose parts
+// one workgroup joins.
+constexpr int kPartsMore = 768, kLeastKeys = 1024, kPartsOfOne = 64;
+KV4_HD int kv4_part_limit(int64_t total, int longest, int keys)
 {
-    const int64_t l = (total + kPartsMore - 1) / kPartsMore, least = kLeastKeys / keys;
-    return l < least ? (int)least : l > 0x3fffffff ? 0x3fffffff : (int)l;
+    const int64_t l = (total + kPartsMore - 1) / kPartsMore;
+    const int least = kLeastKeys / keys, most = (longest + kPartsOfOne - 1) / kPartsOfOne;
+    const int limit = l > 0x3fffffff ? 0x3fffffff : (int)l;
+    return limit > least ? (limit > most ? limit : most) : (least > most ? least : most);
 }
 KV4_HD int kv4_split(int count, int parts, int i) { return (int)((int64_t)count * i / parts); }
 // Workgroups for all parts of any lengths up to `most` keys a sequence.
