@@ -56,8 +56,10 @@ void launch_kv4_read(const Kv4Cache &c, const int64_t *slots, int64_t T, uint16_
 size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int B, int max_q);
 void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st);
 
-// Sequences of at most this many query rows a kv head (queries x query heads).
-inline int kv4_decode_limit(int D) { return D < 256 ? 64 : 32; }
+// Sequences of at most this many query rows a kv head (queries x query heads):
+// two blocks of 16.  Four blocks were no faster than the other kernel's tile of
+// 128 (11 sequences of up to 13 queries x 8 heads: 25 us with four, 15.5 without).
+constexpr int kDecodeRows = 32;
 // A counter for each (sequence, head), on lines of their own: arrivals on one line queue up.
 constexpr int kCounterStride = 16;
 inline size_t kv4_counter_bytes(int64_t B, int heads) { return ((size_t)B * heads * kCounterStride * 8 + 255) & ~size_t(255); }

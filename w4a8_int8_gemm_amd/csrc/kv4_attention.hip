@@ -8,17 +8,16 @@ namespace {
 
 // Rows a kv head that the kernel for few rows is launched for: what a sequence
 // can have, or that kernel's limit.
-int decode_rows(int D, int group, int64_t max_q)
+int decode_rows(int group, int64_t max_q)
 {
-    const int limit = kv4_decode_limit(D);
-    return group * max_q < limit ? (int)(group * max_q) : limit;
+    return group * max_q < kDecodeRows ? (int)(group * max_q) : kDecodeRows;
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 size_t decode_bytes(int q_heads, int kv_heads, int D, int64_t T, int B, int max_q)
 {
-    const int rows = decode_rows(D, q_heads / kv_heads, max_q < T ? max_q : T);
+    const int rows = decode_rows(q_heads / kv_heads, max_q < T ? max_q : T);
     return kv4_counter_bytes(B, kv_heads) +
            align256((size_t)(B * (int64_t)kv_heads + kPartsMore) * rows * (D + 2) * sizeof(float));
 }
@@ -29,7 +28,7 @@ size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int 
 {
     const int group = q_heads / kv_heads;
     size_t bytes = decode_bytes(q_heads, kv_heads, D, T, B, max_q);
-    if ((int64_t)group * (max_q < T ? max_q : T) > kv4_decode_limit(D)) {
+    if ((int64_t)group * (max_q < T ? max_q : T) > kDecodeRows) {
         // any length of keys: the table's width is not known here
         const Kv4Tiles t = kv4_prefill_tiles(T, B, group, kv_heads, int64_t(1) << 30);
         bytes += kv4_counter_bytes(t.slots, 1) + (size_t)t.slots * kTileRows * (D + 2) * sizeof(float);
@@ -39,15 +38,14 @@ size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int 
 
 void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st)
 {
-    const int limit = kv4_decode_limit(c.D);
-    const bool many = (int64_t)a.group * a.max_q > limit;
+    const bool many = (int64_t)a.group * a.max_q > kDecodeRows;
     // Where all sequences have max_q queries, or one query is too many rows for
     // the kernel for few, the other kernel takes them all.
-    const bool few = a.group <= limit && !(many && a.T == (int64_t)a.B * a.max_q);
+    const bool few = a.group <= kDecodeRows && !(many && a.T == (int64_t)a.B * a.max_q);
     if (few)
-        launch_kv4_decode(c, a, decode_rows(c.D, a.group, a.max_q), st);
+        launch_kv4_decode(c, a, decode_rows(a.group, a.max_q), st);
     if (many)
-        launch_kv4_prefill(c, a, few ? limit : 0,
+        launch_kv4_prefill(c, a, few ? kDecodeRows : 0,
                            static_cast<char *>(a.workspace) +
                                decode_bytes(a.group * c.heads, c.heads, c.D, a.T, a.B, a.max_q), st);
 }

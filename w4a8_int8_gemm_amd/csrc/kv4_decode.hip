@@ -1,7 +1,6 @@
 // Attention of few query rows over the 4-bit cache (include/w4a8.h:
-// kv4_attention): up to 64 rows (queries x query heads of a kv head; 32 where
-// head_dim is 256, whose outputs fill the registers) a sequence and kv head,
-// so that the cache is read once.
+// kv4_attention): up to 32 rows (queries x query heads of a kv head) a sequence
+// and kv head, so that the cache is read once.
 //
 // What bounds it: HBM.  A key and value of one head take D + 8 D / G bytes
 // and 4 D operations per query row.
@@ -105,8 +104,93 @@ __device__ __forceinline__ void load_step(Step<P, D / 32, NG> &s, const Kv4Cache
     }
 }
 
+// A row's output and log of the softmax sum from its joined part.
+template <int D>
+__device__ __forceinline__ void store_row(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int row,
+                                          int d, float4 sum, float ref, float l)
+{
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int i = query_of(row, w.over_group, a.group);
+    const int64_t at = (int64_t)(seq.q0 + i) * a.q_heads + head * a.group + (row - i * a.group);
+    *reinterpret_cast<uint2 *>(a.out + at * D + d) =
+        make_uint2(pack_h2(sum.x * inv, sum.y * inv), pack_h2(sum.z * inv, sum.w * inv));
+    if (a.lse && d == 0)
+        a.lse[at] = l > 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+}
+
+// Joins the parts in `parts` slots from slot p0 on: `rows` rows of their
+// (sequence, head).  A thread takes four dims of a row; where there are more threads, groups of them take every
+// so-many-th part and are joined in LDS.  Parts come from memory at some
+// microseconds' latency, so eight are in flight at a time.
+template <int D>
+__device__ void join_parts(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int rows, int p0,
+                           int parts, float *lds)
+{
+    const int p1 = p0 + parts - 1;
+    constexpr int kAhead = 8;
+    const int items = rows * (D / 4);
+    const int groups = items < kThreads ? kThreads / items : 1;
+    const int grp = items < kThreads ? threadIdx.x / items : 0;
+    for (int x0 = 0; x0 < items; x0 += kThreads) {
+        const int x = x0 + (items < kThreads ? threadIdx.x - grp * items : threadIdx.x);
+        const int row = x / (D / 4), d = x % (D / 4) * 4;
+        float R = -INFINITY, L = 0.0f;
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (x < items && grp < groups) {
+            for (int p = p0 + grp; p <= p1; p += groups * kAhead) {
+                float2 rl[kAhead], u[kAhead], v[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    rl[i] = u[i] = v[i] = make_float2(0.0f, 0.0f);
+                    const int pp = p + i * groups;
+                    if (pp <= p1) {                      // each load goes to memory: none for nothing
+                        const float *src = w.base + ((int64_t)pp * w.slot_rows + row) * (D + 2);
+                        rl[i] = load_shared(src + D);
+                        u[i] = load_shared(src + d);
+                        v[i] = load_shared(src + d + 2);
+                    }
+                }
+                float top = R;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i)
+                    top = fmaxf(top, rl[i].y > 0.0f ? rl[i].x : -INFINITY);
+                const float keep = R == -INFINITY ? 0.0f : exp2_hw(R - top);
+                L *= keep;
+                sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const float f = rl[i].y > 0.0f ? exp2_hw(rl[i].x - top) : 0.0f;
+                    L = fmaf(rl[i].y, f, L);
+                    sum.x = fmaf(u[i].x, f, sum.x), sum.y = fmaf(u[i].y, f, sum.y);
+                    sum.z = fmaf(v[i].x, f, sum.z), sum.w = fmaf(v[i].y, f, sum.w);
+                }
+                R = top;
+            }
+        }
+        if (groups > 1) {
+            float *mine = lds + threadIdx.x * 6;
+            mine[0] = R, mine[1] = L, mine[2] = sum.x, mine[3] = sum.y, mine[4] = sum.z, mine[5] = sum.w;
+            __syncthreads();
+            if (grp == 0 && x < items) {
+                for (int g = 1; g < groups; ++g) {
+                    const float *o = lds + (g * items + x) * 6;
+                    const float top = fmaxf(R, o[0]);
+                    const float f0 = R == -INFINITY ? 0.0f : exp2_hw(R - top);
+                    const float f1 = o[0] == -INFINITY ? 0.0f : exp2_hw(o[0] - top);
+                    R = top;
+                    L = L * f0 + o[1] * f1;
+                    sum.x = sum.x * f0 + o[2] * f1, sum.y = sum.y * f0 + o[3] * f1;
+                    sum.z = sum.z * f0 + o[4] * f1, sum.w = sum.w * f0 + o[5] * f1;
+                }
+            }
+        }
+        if (grp == 0 && x < items)
+            store_row<D>(w, a, seq, head, row, d, sum, R, L);
+    }
+}
+
 template <int D, int NG, int RT>
-__global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv4_decode_kernel(Kv4Cache c, Kv4AttnArgs a,
+__global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_kernel(Kv4Cache c, Kv4AttnArgs a,
                                                                                                  Partial w)
 {
     constexpr int N32 = D / 32, PER = N32 / NG;          // steps of 32 dims, of one group
@@ -440,7 +524,7 @@ __global__ __launch_bounds__(kThreads, RT == 4 || RT * D == 512 ? 1 : 2) void kv
             last = arrive(w.counters + item * kCounterStride, parts) ? 1 : 0;
         __syncthreads();
         if (last)
-            join_parts<D, kThreads>(w, a, seq, head, 0, rows, blockIdx.x - part, parts, &os[0][0][0]);
+            join_parts<D>(w, a, seq, head, rows, blockIdx.x - part, parts, &os[0][0][0]);
     }
 }
 
@@ -450,10 +534,8 @@ void launch(const Kv4Cache &c, const Kv4AttnArgs &a, const Partial &w, int rows,
     const dim3 grid((unsigned)w.grid), block(kThreads);
     if (rows <= 16)
         hipLaunchKernelGGL((kv4_decode_kernel<D, NG, 1>), grid, block, 0, st, c, a, w);
-    else if (rows <= 32)
+    else
         hipLaunchKernelGGL((kv4_decode_kernel<D, NG, 2>), grid, block, 0, st, c, a, w);
-    else if constexpr (D < 256)
-        hipLaunchKernelGGL((kv4_decode_kernel<D, NG, 4>), grid, block, 0, st, c, a, w);
 }
 
 }  // namespace

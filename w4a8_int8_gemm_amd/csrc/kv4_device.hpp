@@ -205,7 +205,7 @@ __device__ __forceinline__ bool arrive(uint64_t *counter, int parts)
 
 // Where parts of a result that several workgroups compute meet.
 struct Partial {
-    float *base;                // [slots][slot_rows][D + 2]: output, reference and sum
+    float *base;                // [slots][slot_rows * (D + 2)]: output, reference and sum
     int slots, slot_rows;
     uint64_t *counters;         // [items][kCounterStride]
     int grid;
@@ -219,91 +219,6 @@ inline uint32_t over_group(int group) { return (uint32_t)(((uint64_t(1) << 32) +
 __device__ __forceinline__ int query_of(uint32_t row, uint32_t over, int group)
 {
     return group == 1 ? (int)row : row < 65536u ? (int)__umulhi(row, over) : (int)(row / (uint32_t)group);
-}
-
-// A row's output and log of the softmax sum from its joined part.
-template <int D>
-__device__ __forceinline__ void store_row(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int row,
-                                          int d, float4 sum, float ref, float l)
-{
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int i = query_of(row, w.over_group, a.group);
-    const int64_t at = (int64_t)(seq.q0 + i) * a.q_heads + head * a.group + (row - i * a.group);
-    *reinterpret_cast<uint2 *>(a.out + at * D + d) =
-        make_uint2(pack_h2(sum.x * inv, sum.y * inv), pack_h2(sum.z * inv, sum.w * inv));
-    if (a.lse && d == 0)
-        a.lse[at] = l > 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-}
-
-// Joins the parts in `parts` slots from slot p0 on: `rows` rows from row0 of
-// their (sequence, head) on.  A thread takes four dims of a row; where there are more threads, groups of them take every
-// so-many-th part and are joined in LDS.  Parts come from memory at some
-// microseconds' latency, so eight are in flight at a time.
-template <int D, int kThreads>
-__device__ void join_parts(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int row0, int rows, int p0,
-                           int parts, float *lds)
-{
-    const int p1 = p0 + parts - 1;
-    constexpr int kAhead = 8;
-    const int items = rows * (D / 4);
-    const int groups = items < kThreads ? kThreads / items : 1;
-    const int grp = items < kThreads ? threadIdx.x / items : 0;
-    for (int x0 = 0; x0 < items; x0 += kThreads) {
-        const int x = x0 + (items < kThreads ? threadIdx.x - grp * items : threadIdx.x);
-        const int row = x / (D / 4), d = x % (D / 4) * 4;
-        float R = -INFINITY, L = 0.0f;
-        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (x < items && grp < groups) {
-            for (int p = p0 + grp; p <= p1; p += groups * kAhead) {
-                float2 rl[kAhead], u[kAhead], v[kAhead];
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    rl[i] = u[i] = v[i] = make_float2(0.0f, 0.0f);
-                    const int pp = p + i * groups;
-                    if (pp <= p1) {                      // each load goes to memory: none for nothing
-                        const float *src = w.base + ((int64_t)pp * w.slot_rows + row) * (D + 2);
-                        rl[i] = load_shared(src + D);
-                        u[i] = load_shared(src + d);
-                        v[i] = load_shared(src + d + 2);
-                    }
-                }
-                float top = R;
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i)
-                    top = fmaxf(top, rl[i].y > 0.0f ? rl[i].x : -INFINITY);
-                const float keep = R == -INFINITY ? 0.0f : exp2_hw(R - top);
-                L *= keep;
-                sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
-                    const float f = rl[i].y > 0.0f ? exp2_hw(rl[i].x - top) : 0.0f;
-                    L = fmaf(rl[i].y, f, L);
-                    sum.x = fmaf(u[i].x, f, sum.x), sum.y = fmaf(u[i].y, f, sum.y);
-                    sum.z = fmaf(v[i].x, f, sum.z), sum.w = fmaf(v[i].y, f, sum.w);
-                }
-                R = top;
-            }
-        }
-        if (groups > 1) {
-            float *mine = lds + threadIdx.x * 6;
-            mine[0] = R, mine[1] = L, mine[2] = sum.x, mine[3] = sum.y, mine[4] = sum.z, mine[5] = sum.w;
-            __syncthreads();
-            if (grp == 0 && x < items) {
-                for (int g = 1; g < groups; ++g) {
-                    const float *o = lds + (g * items + x) * 6;
-                    const float top = fmaxf(R, o[0]);
-                    const float f0 = R == -INFINITY ? 0.0f : exp2_hw(R - top);
-                    const float f1 = o[0] == -INFINITY ? 0.0f : exp2_hw(o[0] - top);
-                    R = top;
-                    L = L * f0 + o[1] * f1;
-                    sum.x = sum.x * f0 + o[2] * f1, sum.y = sum.y * f0 + o[3] * f1;
-                    sum.z = sum.z * f0 + o[4] * f1, sum.w = sum.w * f0 + o[5] * f1;
-                }
-            }
-        }
-        if (grp == 0 && x < items)
-            store_row<D>(w, a, seq, head, row0 + row, d, sum, R, L);
-    }
 }
 
 }  // namespace w4a8

@@ -290,12 +290,11 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
             m = max3(m, s[e], s[e + 1]);
         return max3(m, s[15], s[15]);
     };
-    // References are whole, so that a factor is a power of two and the pending
-    // weights w (of `pending` operands) keep their bits.
-    const auto rescale = [&](float m, h8 *w, int pending) {
+    // A new reference for the rows that need one; s: weights that are not in the output yet.
+    const auto rescale = [&](float m, float *s, int pending) {
         m = max_halves(m);
         if (m > bound) {
-            const float nref = ceilf(m) + (float)(scale_exp - kHeadroom);
+            const float nref = m + (float)(scale_exp - kHeadroom);
             const float alpha = exp2_hw(ref - nref);     // 0 before the first key
             l *= alpha;
             ref = nref;
@@ -307,9 +306,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
                     o[g][e] *= alpha;
 #pragma unroll
             for (int i = 0; i < pending; ++i)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    w[i][e] = (_Float16)((float)w[i][e] * alpha);
+                s[i] *= alpha;
         }
     };
     const auto weights = [&](float (&s)[16]) {
@@ -321,8 +318,9 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
-    // Weight times the value's scale, the one rounding to fp16: the operands of 32 keys.
-    const auto operands = [&](h8 (&w)[2][NG], const float (&s)[16], const float (&vs)[NG]) {
+    // O^T += V^T P^T of 32 keys; weight times the value's scale, the one rounding to fp16
+    const auto output = [&](const float (&s)[16], const float (&vs)[NG], auto xc, auto bc) {
+        constexpr int x = decltype(xc)::value, buf = decltype(bc)::value;
         each<2>([&](auto mc) {
             constexpr int m2 = decltype(mc)::value;
             each<NG>([&](auto gc) {
@@ -332,19 +330,14 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
                     constexpr int e = 8 * m2 + 2 * decltype(ic)::value;
                     y[decltype(ic)::value] = pack_h2(s[e] * row_lane<e>(vs[grp]), s[e + 1] * row_lane<e + 1>(vs[grp]));
                 });
-                w[m2][grp] = __builtin_bit_cast(h8, y);
+#pragma unroll
+                for (int g = grp * PER; g < (grp + 1) * PER; ++g)
+                    o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        __builtin_bit_cast(h8, vt[buf][32 * g + r32][4 * x + 2 * m2 + h]), __builtin_bit_cast(h8, y), o[g], 0, 0, 0);
             });
         });
     };
-    const auto output = [&](const h8 (&w)[2][NG], auto xc, auto bc) {
-        constexpr int x = decltype(xc)::value, buf = decltype(bc)::value;
-#pragma unroll
-        for (int m2 = 0; m2 < 2; ++m2)
-#pragma unroll
-            for (int g = 0; g < N32; ++g)
-                o[g] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                    __builtin_bit_cast(h8, vt[buf][32 * g + r32][2 * (2 * x + m2) + h]), w[m2][g / PER], o[g], 0, 0, 0);
-    };
+
     const auto compute = [&](int step, auto bc) {
         constexpr int buf = decltype(bc)::value;
         const int t0 = step * kKeys;
@@ -376,7 +369,6 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         const std::integral_constant<int, 0> first_half;
         const std::integral_constant<int, 1> second_half;
         float s0[16], s1[16];
-        h8 w0[2][NG], w1[2][NG];
         scores(s0, ks[0], first_half, bc);
         if (some_hidden)
             hide(s0, ks0, t0);
@@ -386,22 +378,20 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         // keeps the lane moves of the scales in this block, where they fold into the products
 #pragma unroll
         for (int g = 0; g < NG; ++g)
-            asm("" : "+v"(vs[0][g]), "+v"(ks[1][g]));
-        scores(s1, ks[1], second_half, bc);
+            asm("" : "+v"(ks[1][g]));
+        scores(s1, ks[1], second_half, bc);              // beside these keys' products: the first half's weights
         weights(s0);
-        operands(w0, s0, vs[0]);
         if (some_hidden)
             hide(s1, ks1, t0 + 32);
         const float m1 = largest(s1);
         if (__ballot(m1 > bound))
-            rescale(m1, &w0[0][0], 2 * NG);
+            rescale(m1, s0, 16);
 #pragma unroll
         for (int g = 0; g < NG; ++g)
-            asm("" : "+v"(vs[1][g]));
-        output(w0, first_half, bc);
+            asm("" : "+v"(vs[0][g]), "+v"(vs[1][g]));
+        output(s0, vs[0], first_half, bc);
         weights(s1);
-        operands(w1, s1, vs[1]);
-        output(w1, second_half, bc);
+        output(s1, vs[1], second_half, bc);
     };
 
     if (s0 < s1) {
@@ -425,42 +415,77 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
             one(step + 1, std::integral_constant<int, 1>());
     }
 
-    // ---- results: the lane's row, dims 32 g + 8 i + 4 h ..+3
     l = sum_halves(l);
-    if (parts == 1) {
-        if (row < rows) {
-            const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-            const int64_t at = (int64_t)(seq.q0 + qi) * a.q_heads + head * group + hh;
-#pragma unroll
-            for (int g = 0; g < N32; ++g)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint2 *>(a.out + at * D + 32 * g + 8 * i + 4 * h) =
-                        make_uint2(pack_h2(o[g][4 * i] * inv, o[g][4 * i + 1] * inv), pack_h2(o[g][4 * i + 2] * inv, o[g][4 * i + 3] * inv));
-            if (a.lse && h == 0)
-                a.lse[at] = l > 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-        }
-        return;
-    }
-    if (row < rows) {
-        float *dst = w.base + ((int64_t)(slot0 + part - part0) * w.slot_rows + 32 * wave + r32) * (D + 2);
+    if (parts > 1) {
+        // ---- parts: left in the workspace in the order of the registers (a wave's
+        // lanes side by side); the last to arrive takes all up again, in order
+        const auto slot_of = [&](int p) { return w.base + (int64_t)(slot0 + p) * w.slot_rows * (D + 2); };
+        const int at_o = wave * (N32 * 1024) + lane * 2, at_l = kRows * D + (32 * wave + r32) * 2;
+        constexpr int AT_ONCE = D < 256 ? 2 : 1;         // parts whose loads are in flight
+        float *mine = slot_of(part - part0);
 #pragma unroll
         for (int g = 0; g < N32; ++g)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                store_shared(dst + 32 * g + 8 * i + 4 * h, o[g][4 * i], o[g][4 * i + 1]);
-                store_shared(dst + 32 * g + 8 * i + 4 * h + 2, o[g][4 * i + 2], o[g][4 * i + 3]);
-            }
+            for (int e = 0; e < 16; e += 2)
+                store_shared(mine + at_o + g * 1024 + e * 64, o[g][e], o[g][e + 1]);
         if (h == 0)
-            store_shared(dst + D, l > 0.0f ? ref : -INFINITY, l);
+            store_shared(mine + at_l, l > 0.0f ? ref : -INFINITY, l);
+        __builtin_amdgcn_s_waitcnt(0);                   // this wave's stores are complete
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = arrive(counter, parts) ? 1 : 0;
+        __syncthreads();
+        if (!last)
+            return;
+        ref = -INFINITY;
+        l = 0.0f;
+        for (int p = 0; p < parts; p += AT_ONCE) {
+            float2 rl[AT_ONCE], x[AT_ONCE][N32 * 8];
+#pragma unroll
+            for (int y = 0; y < AT_ONCE; ++y) {
+                rl[y] = make_float2(-INFINITY, 0.0f);
+                if (p + y < parts) {
+                    const float *src = slot_of(p + y);
+                    rl[y] = load_shared(src + at_l);
+#pragma unroll
+                    for (int i = 0; i < N32 * 8; ++i)
+                        x[y][i] = load_shared(src + at_o + i * 128);
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < AT_ONCE; ++y) {
+                if (p + y >= parts)
+                    break;
+                const float nref = fmaxf(ref, rl[y].y > 0.0f ? rl[y].x : -INFINITY);
+                const float f0 = ref == -INFINITY ? 0.0f : exp2_hw(ref - nref);
+                const float f1 = rl[y].y > 0.0f ? exp2_hw(rl[y].x - nref) : 0.0f;
+                l = l * f0 + rl[y].y * f1;
+                ref = nref;
+#pragma unroll
+                for (int g = 0; g < N32; ++g)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 v = x[y][g * 8 + e / 2];
+                        o[g][e] = fmaf(v.x, f1, p + y ? o[g][e] * f0 : 0.0f);
+                        o[g][e + 1] = fmaf(v.y, f1, p + y ? o[g][e + 1] * f0 : 0.0f);
+                    }
+            }
+        }
     }
-    __builtin_amdgcn_s_waitcnt(0);                       // this wave's stores are complete
-    __syncthreads();
-    if (threadIdx.x == 0)
-        last = arrive(counter, parts) ? 1 : 0;
-    __syncthreads();
-    if (last)
-        join_parts<D, kThreads>(w, a, seq, head, row0, rows_here, slot0, parts, reinterpret_cast<float *>(&kt[0][0][0]));
+
+    // ---- results: the lane's row, dims 32 g + 8 i + 4 h ..+3
+    if (row < rows) {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const int64_t at = (int64_t)(seq.q0 + qi) * a.q_heads + head * group + hh;
+#pragma unroll
+        for (int g = 0; g < N32; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint2 *>(a.out + at * D + 32 * g + 8 * i + 4 * h) =
+                    make_uint2(pack_h2(o[g][4 * i] * inv, o[g][4 * i + 1] * inv), pack_h2(o[g][4 * i + 2] * inv, o[g][4 * i + 3] * inv));
+        if (a.lse && h == 0)
+            a.lse[at] = l > 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    }
 }
 
 }  // namespace
