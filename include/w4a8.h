@@ -349,7 +349,7 @@ typedef struct {
  * (fp16 [T, kv_heads, head_dim], token strides k_stride and v_stride) goes to
  * slot slots[t] (int64 [T]).  Slots outside [0, pages * page_size) write
  * nothing (padding rows carry -1; their values may be anything); the others
- * have to differ, and their values to be finite. */
+ * have to differ, and their values to be finite.  T * kv_heads <= 2^29. */
 w4a8_status_t kv4_write(const w4a8_f16 *k, int64_t k_stride, const w4a8_f16 *v, int64_t v_stride,
                         const int64_t *slots, int64_t T, const kv4_cache_t *cache,
                         w4a8_stream_t stream);
@@ -376,16 +376,18 @@ size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t h
  * window > 0 (causal only) only j > p - window.  Over the keys seen,
  *     s_j = scale * sum_d q[d] k_j[d],  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
  * where k_j, v_j are the values code * scale.  A query that sees nothing gets
- * out = 0 and lse = -infinity.  Scores, maxima, sums and outputs are held in
- * fp32; the codes enter the fp16 matrix products exactly, and the one rounding
- * besides the output's is that of the weights softmax * v_scale to fp16.
+ * out = 0 and lse = -infinity.  Scores, sums and outputs are held in fp32; the
+ * codes enter the fp16 matrix products exactly.  Besides the output's rounding
+ * the weights softmax * v_scale are rounded: to 22 bits where a sequence has at
+ * most 32 rows (queries x query heads of a kv head), to fp16 where it has more.
  * out fp16 [T, q_heads, head_dim] contiguous; lse fp32 [T, q_heads] or NULL.
  * What the device-side tables hold is bounded, not trusted: kv_lens are cut to
  * [0, max_pages * page_size], tokens of pages outside [0, pages) are not seen,
  * queries outside [0, T) are not computed; nothing that is not seen has any
  * influence, whatever its bytes are.  workspace: device buffer of
- * kv4_attention_workspace_size() bytes, 256-byte aligned; each call writes
- * what it reads there. */
+ * kv4_attention_workspace_size() bytes, 256-byte aligned, which needs no
+ * initial content; calls that overlap need workspaces of their own.  At most
+ * 2^30 tokens a sequence, 2^20 sequences, T * q_heads < 2^31. */
 w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int32_t q_heads,
                             const kv4_cache_t *cache, const int32_t *page_table,
                             int32_t max_pages, const int32_t *kv_lens, const int32_t *q_starts,

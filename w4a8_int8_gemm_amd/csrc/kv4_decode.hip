@@ -380,7 +380,7 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
             for (int t = 0; t < RT; ++t)
                 bound[t] = ref[t] + (float)(kRange - scale_exp);
         }
-        h8 wt[RT][P / 2][NG];
+        h8 wt[RT][P / 2][NG], wl[RT][P / 2][NG];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             float m = max3(s[t][0][0], s[t][0][1], s[t][0][2]);
@@ -409,18 +409,24 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
                     s[t][p][j] = exp2_hw(s[t][p][j] - ref[t]);
                 l[t] += (s[t][p][0] + s[t][p][1]) + (s[t][p][2] + s[t][p][3]);
             }
-            // weight times the value's scale, the one rounding to fp16
+            // Weight times the value's scale as the sum of two fp16 values, 22 bits:
+            // where a row has few keys one rounding would be in every element of its
+            // output, and the matrix unit has the time.
             each<P / 2>([&](auto hc) {
                 constexpr int h = decltype(hc)::value;
                 each<NG>([&](auto gc) {
                     constexpr int g = decltype(gc)::value;
-                    u32x4 x;
+                    u32x4 x, y;
                     each<4>([&](auto ic) {
                         constexpr int x2 = decltype(ic)::value / 2, j = decltype(ic)::value % 2 * 2;
-                        x[decltype(ic)::value] = pack_h2(s[t][2 * h + x2][j] * row_lane<8 * x2 + 4 + j>(sc[h][g]),
-                                                         s[t][2 * h + x2][j + 1] * row_lane<8 * x2 + 5 + j>(sc[h][g]));
+                        const float a0 = s[t][2 * h + x2][j] * row_lane<8 * x2 + 4 + j>(sc[h][g]);
+                        const float a1 = s[t][2 * h + x2][j + 1] * row_lane<8 * x2 + 5 + j>(sc[h][g]);
+                        const uint32_t top = pack_h2(a0, a1);
+                        x[decltype(ic)::value] = top;
+                        y[decltype(ic)::value] = pack_h2(a0 - lo_h2f(top), a1 - hi_h2f(top));
                     });
                     wt[t][h][g] = __builtin_bit_cast(h8, x);
+                    wl[t][h][g] = __builtin_bit_cast(h8, y);
                 });
             });
         }
@@ -429,16 +435,18 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
             constexpr int h = decltype(hc)::value;
             each<N32>([&](auto gc) {
                 constexpr int g = decltype(gc)::value;
-                const auto &v0 = cur.v[2 * h], &v1 = cur.v[2 * h + 1];
-                const uint32_t x0 = byte_pair<g % 4>(v0[0][g / 4], v0[1][g / 4]), x1 = byte_pair<g % 4>(v0[2][g / 4], v0[3][g / 4]);
-                const uint32_t x2 = byte_pair<g % 4>(v1[0][g / 4], v1[1][g / 4]), x3 = byte_pair<g % 4>(v1[2][g / 4], v1[3][g / 4]);
+                const auto &p0 = cur.v[2 * h], &p1 = cur.v[2 * h + 1];
+                const uint32_t x0 = byte_pair<g % 4>(p0[0][g / 4], p0[1][g / 4]), x1 = byte_pair<g % 4>(p0[2][g / 4], p0[3][g / 4]);
+                const uint32_t x2 = byte_pair<g % 4>(p1[0][g / 4], p1[1][g / 4]), x3 = byte_pair<g % 4>(p1[2][g / 4], p1[3][g / 4]);
                 const u32x4 e0 = {codes_low(x0), codes_low(x1), codes_low(x2), codes_low(x3)};
                 const u32x4 e1 = {codes_high(x0), codes_high(x1), codes_high(x2), codes_high(x3)};
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    const h8 x = wt[t][h][g / PER];
-                    o[t][2 * g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, e0), x, o[t][2 * g], 0, 0, 0);
-                    o[t][2 * g + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, e1), x, o[t][2 * g + 1], 0, 0, 0);
+                    const h8 v0 = __builtin_bit_cast(h8, e0), v1 = __builtin_bit_cast(h8, e1);
+                    o[t][2 * g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, wt[t][h][g / PER], o[t][2 * g], 0, 0, 0);
+                    o[t][2 * g + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, wt[t][h][g / PER], o[t][2 * g + 1], 0, 0, 0);
+                    o[t][2 * g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, wl[t][h][g / PER], o[t][2 * g], 0, 0, 0);
+                    o[t][2 * g + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, wl[t][h][g / PER], o[t][2 * g + 1], 0, 0, 0);
                 }
             });
         });
