@@ -305,6 +305,10 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
     int scale_exp = kNoScale;
     uint32_t scale_cap = 0;                              // bits of 2^(scale_exp + 1)
     const float score_scale = a.scale * kLog2e;
+    // Where a row has few keys, one rounding of a weight is in every element of
+    // its output: the weights are taken as two fp16 values, 22 bits.  (With more
+    // keys the roundings average out and the second product costs 6 to 9 %.)
+    const bool fine = seq.n <= kLeastKeys;
 
     const auto compute = [&](const Step<P, N32, NG> &cur, int step) {
         const int t0 = step * KEYS;
@@ -380,7 +384,6 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
             for (int t = 0; t < RT; ++t)
                 bound[t] = ref[t] + (float)(kRange - scale_exp);
         }
-        h8 wt[RT][P / 2][NG], wl[RT][P / 2][NG];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             float m = max3(s[t][0][0], s[t][0][1], s[t][0][2]);
@@ -409,47 +412,54 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
                     s[t][p][j] = exp2_hw(s[t][p][j] - ref[t]);
                 l[t] += (s[t][p][0] + s[t][p][1]) + (s[t][p][2] + s[t][p][3]);
             }
-            // Weight times the value's scale as the sum of two fp16 values, 22 bits:
-            // where a row has few keys one rounding would be in every element of its
-            // output, and the matrix unit has the time.
+        }
+        // weights times the values' scales, rounded to fp16; what is left of them after that
+        const auto weights = [&](h8 (&wt)[RT][P / 2][NG], bool rest) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                each<P / 2>([&](auto hc) {
+                    constexpr int h = decltype(hc)::value;
+                    each<NG>([&](auto gc) {
+                        constexpr int g = decltype(gc)::value;
+                        u32x4 x;
+                        each<4>([&](auto ic) {
+                            constexpr int x2 = decltype(ic)::value / 2, j = decltype(ic)::value % 2 * 2;
+                            const float a0 = s[t][2 * h + x2][j] * row_lane<8 * x2 + 4 + j>(sc[h][g]);
+                            const float a1 = s[t][2 * h + x2][j + 1] * row_lane<8 * x2 + 5 + j>(sc[h][g]);
+                            const uint32_t top = pack_h2(a0, a1);
+                            x[decltype(ic)::value] = rest ? pack_h2(a0 - lo_h2f(top), a1 - hi_h2f(top)) : top;
+                        });
+                        wt[t][h][g] = __builtin_bit_cast(h8, x);
+                    });
+                });
+        };
+        // O^T += V^T P^T: 16 rows 32 g + 2 r + e of the values for byte g's two nibbles e
+        const auto output = [&](const h8 (&wt)[RT][P / 2][NG]) {
             each<P / 2>([&](auto hc) {
                 constexpr int h = decltype(hc)::value;
-                each<NG>([&](auto gc) {
+                each<N32>([&](auto gc) {
                     constexpr int g = decltype(gc)::value;
-                    u32x4 x, y;
-                    each<4>([&](auto ic) {
-                        constexpr int x2 = decltype(ic)::value / 2, j = decltype(ic)::value % 2 * 2;
-                        const float a0 = s[t][2 * h + x2][j] * row_lane<8 * x2 + 4 + j>(sc[h][g]);
-                        const float a1 = s[t][2 * h + x2][j + 1] * row_lane<8 * x2 + 5 + j>(sc[h][g]);
-                        const uint32_t top = pack_h2(a0, a1);
-                        x[decltype(ic)::value] = top;
-                        y[decltype(ic)::value] = pack_h2(a0 - lo_h2f(top), a1 - hi_h2f(top));
-                    });
-                    wt[t][h][g] = __builtin_bit_cast(h8, x);
-                    wl[t][h][g] = __builtin_bit_cast(h8, y);
+                    const auto &p0 = cur.v[2 * h], &p1 = cur.v[2 * h + 1];
+                    const uint32_t x0 = byte_pair<g % 4>(p0[0][g / 4], p0[1][g / 4]), x1 = byte_pair<g % 4>(p0[2][g / 4], p0[3][g / 4]);
+                    const uint32_t x2 = byte_pair<g % 4>(p1[0][g / 4], p1[1][g / 4]), x3 = byte_pair<g % 4>(p1[2][g / 4], p1[3][g / 4]);
+                    const u32x4 e0 = {codes_low(x0), codes_low(x1), codes_low(x2), codes_low(x3)};
+                    const u32x4 e1 = {codes_high(x0), codes_high(x1), codes_high(x2), codes_high(x3)};
+#pragma unroll
+                    for (int t = 0; t < RT; ++t) {
+                        const h8 x = wt[t][h][g / PER];
+                        o[t][2 * g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, e0), x, o[t][2 * g], 0, 0, 0);
+                        o[t][2 * g + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, e1), x, o[t][2 * g + 1], 0, 0, 0);
+                    }
                 });
             });
+        };
+        h8 wt[RT][P / 2][NG];
+        weights(wt, false);
+        output(wt);
+        if (fine) {
+            weights(wt, true);
+            output(wt);
         }
-        // O^T += V^T P^T: 16 rows 32 g + 2 r + e of the values for byte g's two nibbles e
-        each<P / 2>([&](auto hc) {
-            constexpr int h = decltype(hc)::value;
-            each<N32>([&](auto gc) {
-                constexpr int g = decltype(gc)::value;
-                const auto &p0 = cur.v[2 * h], &p1 = cur.v[2 * h + 1];
-                const uint32_t x0 = byte_pair<g % 4>(p0[0][g / 4], p0[1][g / 4]), x1 = byte_pair<g % 4>(p0[2][g / 4], p0[3][g / 4]);
-                const uint32_t x2 = byte_pair<g % 4>(p1[0][g / 4], p1[1][g / 4]), x3 = byte_pair<g % 4>(p1[2][g / 4], p1[3][g / 4]);
-                const u32x4 e0 = {codes_low(x0), codes_low(x1), codes_low(x2), codes_low(x3)};
-                const u32x4 e1 = {codes_high(x0), codes_high(x1), codes_high(x2), codes_high(x3)};
-#pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    const h8 v0 = __builtin_bit_cast(h8, e0), v1 = __builtin_bit_cast(h8, e1);
-                    o[t][2 * g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, wt[t][h][g / PER], o[t][2 * g], 0, 0, 0);
-                    o[t][2 * g + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, wt[t][h][g / PER], o[t][2 * g + 1], 0, 0, 0);
-                    o[t][2 * g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, wl[t][h][g / PER], o[t][2 * g], 0, 0, 0);
-                    o[t][2 * g + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, wl[t][h][g / PER], o[t][2 * g + 1], 0, 0, 0);
-                }
-            });
-        });
     };
     // The next step's loads are in flight during one, its pages (scalar loads)
     // are a step further ahead; other waves hide the rest.  The step stands in
