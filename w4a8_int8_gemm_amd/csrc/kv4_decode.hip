@@ -2,8 +2,11 @@
 // kv4_attention): up to 32 rows (queries x query heads of a kv head) a sequence
 // and kv head, so that the cache is read once.
 //
-// What bounds it: HBM.  A key and value of one head take D + 8 D / G bytes
-// and 4 D operations per query row.
+// What bounds it: for long caches reading it, D + 8 D / G bytes for a key and
+// value of one head; for short ones the chain of loads, steps and joins.
+// Measured: one sequence of 131075 keys (151 MB) 39 us, 3.9 TB/s over the whole
+// call; 32 sequences of up to 4516 (81.5 MB) 24 us; one of 517 10 us.  About
+// 60 % of a workgroup's cycles are steps in the first, 40 % in the second.
 //
 // One wavefront takes steps of 32 keys.  S^T =
 // K Q^T on 16x16x32 matrix instructions with the codes as fp16 (exact) and the

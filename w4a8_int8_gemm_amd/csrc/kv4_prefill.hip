@@ -2,10 +2,12 @@
 // kv4_attention): sequences with more rows a kv head than the kernel for few
 // rows takes.
 //
-// What bounds it: the vector unit.  A tile of 64 keys and 32 rows a wave takes
-// 1024 cycles of the matrix unit, and the scores' scaling, maximum, exponential,
-// sum, weight and rounding some 300 vector operations at 4 cycles each, plus
-// the wave's share of turning codes into fp16.
+// What bounds it: a wave's own chain of LDS reads, products and softmax, with
+// two waves a SIMD to cover it.  For D = 128, a wave's tile of 64 keys and 32
+// rows takes 32 matrix instructions and 418 vector instructions (scaling,
+// maximum, exponential, sum, rounding, and its share of turning codes into
+// fp16).  Of all cycles the vector unit is busy 57 %, the matrix unit 33 %.
+// Measured: a causal prompt of 4516 tokens, 167 GFLOP, 221 us (756 TFLOP/s).
 //
 // A workgroup has 128 rows (queries x query heads of one kv head), 32 a wave,
 // and walks over its keys in tiles of 64.  Two of its waves turn the tile's V
