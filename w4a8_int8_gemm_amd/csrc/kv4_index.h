@@ -44,10 +44,8 @@ KV4_HD int kv4_hi(int n, int m, int i, bool causal)
 }
 KV4_HD int kv4_lo(int n, int m, int i, int window)
 {
-    if (window <= 0)
-        return 0;
-    const int lo = n - m + i + 1 - window;
-    return lo < 0 ? 0 : lo;
+    const int p1 = n - m + i + 1;                       // p1 - window may leave 32 bits where p1 < 0
+    return window > 0 && p1 > window ? p1 - window : 0;
 }
 
 // Steps of `keys` keys that a sequence's queries need together; one (empty)
@@ -112,6 +110,28 @@ KV4_HD Kv4Tiles kv4_prefill_tiles(int64_t T, int64_t B, int group, int heads, in
     Kv4Tiles t;
     t.slots = each < 2 ? 0 : items * each < 2 * kTileShares ? items * each : 2 * kTileShares;
     t.grid = items + t.slots;
+    return t;
+}
+
+// Part `part` of `cuts` even ones of a sequence's steps (r.first, r.count) for a
+// tile with the queries i0 .. i1: it has the steps [s0, s1), and of the tile's
+// parts [part0, part0 + parts) hold any step that a query of it sees (one does
+// where none is seen).
+struct Kv4TilePart {
+    int part0, parts, s0, s1;
+};
+KV4_HD Kv4TilePart kv4_tile_part(const Kv4Seq &s, bool causal, int window, int keys, int i0, int i1, const Kv4Steps &r,
+                                 int cuts, int part)
+{
+    const int lo = kv4_lo(s.n, s.m, i0, window), hi = kv4_hi(s.n, s.m, i1, causal);
+    const int width = (r.count + cuts - 1) / cuts;
+    const int begin = lo / keys - r.first, past = (hi + keys - 1) / keys - r.first, end = past > begin ? past : begin;
+    Kv4TilePart t;
+    t.part0 = begin / width < cuts - 1 ? begin / width : cuts - 1;
+    const int last = end > 0 ? (end - 1) / width : 0;
+    t.parts = (last > t.part0 ? last : t.part0) - t.part0 + 1;
+    t.s0 = r.first + (begin > part * width ? begin : part * width);
+    t.s1 = r.first + (end < (part + 1) * width ? end : (part + 1) * width);
     return t;
 }
 

@@ -63,7 +63,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         steps += wave_sum64((int64_t)tl * nl);
     }
     const int limit = kv4_tile_limit(steps * c.heads, kKeys);
-    int b = -1, tiles = 0, cuts = 0, count = 0, id = blockIdx.x, split = 0;   // split: slots before b's
+    int b = -1, tiles = 0, cuts = 0, id = blockIdx.x, split = 0;   // split: slots before b's
     Kv4Seq seq = {0, 0, 0};
     for (int base = 0; base < B; base += 64) {
         if (B > 64)
@@ -75,7 +75,6 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
             const int at = __builtin_ctzll(past);
             b = base + at;
             tiles = __builtin_amdgcn_readlane(tl, at);
-            count = __builtin_amdgcn_readlane(nl, at);
             cuts = __builtin_amdgcn_readlane(k, at);
             seq.q0 = __builtin_amdgcn_readlane(sl.q0, at);
             seq.m = __builtin_amdgcn_readlane(sl.m, at);
@@ -92,19 +91,14 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
     // Head first, so that neighbours (other chiplets) have other heads' keys;
     // the last rows, which see the most keys, first.
     const int head = id % c.heads, part = id / c.heads % cuts, tile = tiles - 1 - id / c.heads / cuts;
-    const int width = (count + cuts - 1) / cuts;
     const int rows = seq.m * group, row0 = tile * kRows, rows_here = min(kRows, rows - row0);
-    // steps that some row of the tile sees
+    // the steps that some row of the tile sees, and the parts that hold any of them
     const int i_first = query_of(row0, w.over_group, group), i_last = query_of(row0 + rows_here - 1, w.over_group, group);
-    const int first = kv4_steps(seq, a.causal, a.window, kKeys).first;
-    const int lo_tile = kv4_lo(seq.n, seq.m, i_first, a.window), hi_tile = kv4_hi(seq.n, seq.m, i_last, a.causal);
-    const int begin = lo_tile / kKeys - first, end = max((hi_tile + kKeys - 1) / kKeys - first, begin);
-    // the parts that hold any of them
-    const int part0 = min(begin / width, cuts - 1), part1 = max(part0, end > 0 ? (end - 1) / width : 0);
-    if (part < part0 || part > part1)
+    const Kv4TilePart span = kv4_tile_part(seq, a.causal, a.window, kKeys, i_first, i_last,
+                                           kv4_steps(seq, a.causal, a.window, kKeys), cuts, part);
+    const int part0 = span.part0, parts = span.parts, s0 = span.s0, s1 = span.s1;
+    if (part < part0 || part >= part0 + parts)
         return;
-    const int parts = part1 - part0 + 1;
-    const int s0 = first + max(begin, part * width), s1 = first + min(end, (part + 1) * width);
     // slots and counters of the sequence's tiles: [tile][head][part]
     const int tile_head = tile * c.heads + head;
     if (cuts > 1 && split + (tile_head + 1) * cuts > w.slots)
