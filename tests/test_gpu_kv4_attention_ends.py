@@ -5,7 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-import w4a8_int8_gemm_amd as w  # noqa: E402
+from tests.kv4_util import attention  # noqa: E402
 from tests.test_gpu_kv4_attention import Case, dev  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -18,3 +18,100 @@ TOP = 2 ** 31 - 1
 def test_the_largest_windows(kv, m, window):
     """More queries than keys, so that the first key of a window lies below -2^31."""
     Case(kv, m, 4, 2, 128, 128, 16, seed=21).check(window=window)
+
+
+HOSTILE = {"nan": np.nan, "inf": np.inf, "-inf": -np.inf, "huge": 3e38, "-huge": -3e38, "mixed": None}
+
+
+def spoil(c, b, keys, kind, names="kv", groups=slice(None), seed=0):
+    """Hostile scales and arbitrary codes for some keys of sequence b."""
+    r = np.random.default_rng(seed)
+    for name in names:
+        codes, scales = getattr(c.c, name), getattr(c.c, name + "_scale")
+        for j in keys:
+            page, at = int(c.table[b, j // c.page]), j % c.page
+            codes[page, :, at] = dev(r.integers(0, 256, (c.hk, c.D // 2)).astype(np.uint8))
+            value = HOSTILE[kind] if kind != "mixed" else r.choice([np.nan, np.inf, -np.inf, 3e38, -3e38, -1.0])
+            scales[page, :, at, groups] = float(value)
+
+
+def check_rows(c, rows_of, causal=True, window=0):
+    """The rows that rows_of gives for a sequence, against the definition."""
+    out, lse = c.run(causal, window)
+    out, lse = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    for b in range(len(c.kv)):
+        first = c.starts[b]
+        want, logs, ob, lb = attention(c.q[first:c.starts[b + 1]], c.k[b], c.v[b], c.there[b], None, None, causal, window,
+                                       c.D ** -0.5, c.page)
+        for i in rows_of(b):
+            got = out[first + i]
+            assert np.isfinite(got).all(), f"sequence {b} row {i}: not finite"
+            assert (np.abs(got - want[i]) <= ob[i]).all(), f"sequence {b} row {i}"
+            same = logs[i] == lse[first + i]
+            with np.errstate(invalid="ignore"):
+                assert (same | (np.abs(lse[first + i] - logs[i]) <= lb[i])).all(), f"sequence {b} row {i}"
+    return out, lse
+
+
+@pytest.mark.parametrize("kind", HOSTILE)
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("m", [[1, 1, 1], [3, 8, 1], [60, 33, 80]])
+def test_keys_behind_the_window_have_no_influence(m, page, kind):
+    """What lies in front of every query's window may be anything: its page may have been given away."""
+    for D, G, window in ((128, 64, 50), (64, 64, 17), (256, 64, 33), (128, 128, 1)):
+        c = Case([120, 257, 80], m, 4, 2, D, G, page, seed=22)
+        for b, (n, q) in enumerate(zip(c.kv, m)):
+            spoil(c, b, range(max(0, n - q + 1 - window)), kind)
+        check_rows(c, lambda b: range(m[b]), window=window)
+
+
+@pytest.mark.parametrize("kind", HOSTILE)
+@pytest.mark.parametrize("names", ["k", "v"])
+@pytest.mark.parametrize("m", [[5, 2], [8, 16], [70, 140]])
+def test_a_later_token_does_not_change_an_earlier_row(m, names, kind):
+    """The last token's key and value are seen by the last query alone."""
+    for D, G in ((128, 64), (64, 64), (256, 128)):
+        c = Case([75, 140], m, 4, 2, D, G, 16, seed=23)
+        for b, n in enumerate(c.kv):
+            spoil(c, b, [n - 1], kind, names)
+        check_rows(c, lambda b: range(m[b] - 1))
+
+
+@pytest.mark.parametrize("kind", HOSTILE)
+@pytest.mark.parametrize("m", [[6, 3], [50, 70]])
+def test_a_token_that_left_the_window_does_not_change_a_row(m, kind):
+    """The first query alone still sees the key that is spoiled."""
+    c = Case([90, 200], m, 8, 2, 128, 32, 16, seed=24)
+    for b, (n, q) in enumerate(zip(c.kv, m)):
+        spoil(c, b, [max(0, n - q + 1 - 20)], kind)
+    check_rows(c, lambda b: range(1 if c.kv[b] - m[b] + 1 >= 20 else m[b], m[b]), window=20)
+
+
+@pytest.mark.parametrize("m", [[1], [4], [60]])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_seen_value_that_is_not_finite_stays_in_its_group(m, causal):
+    """Rows that see it are not finite in the elements of its scale group, and as they are in the others."""
+    c = Case([77], m, 4, 2, 128, 32, 16, seed=25)
+    good, logs = (t.cpu().numpy() for t in c.run(causal))
+    j = 76 - m[0] // 2
+    page, at = int(c.table[0, j // 16]), j % 16
+    c.c.v_scale[page, 1, at, 2] = float("nan")
+    out, lse = (t.cpu().numpy() for t in c.run(causal))
+    sees = np.arange(m[0]) + 77 - m[0] >= j if causal else np.ones(m[0], bool)
+    touched = np.zeros(out.shape, bool)
+    touched[np.ix_(sees, [2, 3], np.arange(64, 96))] = True
+    assert np.isnan(out[touched]).all() and sees.any()
+    # the other elements: the reference of the weights may differ, two roundings to fp16 on each side
+    assert (np.abs(out.astype(float) - good)[~touched] <= 4 * 2.0 ** -11 * 8).all()
+    assert np.array_equal(lse, logs) or (np.abs(lse - logs) <= 64 * 2.0 ** -24 * (1 + np.abs(logs))).all()
+
+
+@pytest.mark.parametrize("m", [[1, 5, 8], [70, 33, 64]])
+def test_values_far_larger_than_what_an_earlier_row_sees(m):
+    """A later token's values are 2^16 times the others, all within fp16."""
+    c = Case([90, 130, 64], m, 4, 2, 128, 64, 16, seed=26, gain=0.01)
+    for b, n in enumerate(c.kv):
+        page, at = int(c.table[b, (n - 1) // 16]), (n - 1) % 16
+        c.c.v_scale[page, :, at] *= 2.0 ** 16
+        c.v[b][n - 1] *= 2.0 ** 16
+    check_rows(c, lambda b: range(m[b]))

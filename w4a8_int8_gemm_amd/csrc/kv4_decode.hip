@@ -305,8 +305,14 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
             o[t][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
     }
     const int lo_most = kv4_lo(seq.n, seq.m, seq.m - 1, a.window), hi_least = kv4_hi(seq.n, seq.m, 0, a.causal);
-    int scale_exp = kNoScale;
-    uint32_t scale_cap = 0;                              // bits of 2^(scale_exp + 1)
+    // exponent of the largest value scale that a row has seen; bits of 2^(e + 1)
+    // for the smallest of them
+    int scale_exp[RT];
+    uint32_t scale_cap = 0;
+    uint32_t spoilt[RT];                                 // bit g: it has seen one of group g that is not finite
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+        scale_exp[t] = kNoScale, spoilt[t] = 0;
     const float score_scale = a.scale * kLog2e;
     // Where a row has few keys, one rounding of a weight is in every element of
     // its output: the weights are taken as two fp16 values, 22 bits.  (With more
@@ -349,8 +355,10 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
                 });
             });
         });
-        // a step that not every row sees whole: hide keys, and what garbage stands for them
+        // a step that not every row sees whole: hide keys, whatever stands for them
+        uint32_t some_hidden = 0;                        // a number: branching on the condition twice cost 17 registers
         if (cur.ok != (1u << P) - 1 || t0 < lo_most || t0 > hi_least - KEYS) {
+            some_hidden = kNotFinite;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 const bool page_ok = (cur.ok >> p) & 1;
@@ -363,29 +371,62 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
                         s[t][p][j] = there && key >= lo[t] && key < hi[t] ? s[t][p][j] : -INFINITY;
                 }
             }
-#pragma unroll
-            for (int h = 0; h < P / 2; ++h) {
-                const int mine = t0 + 32 * h + 2 * (r & 8) + 4 * b4 + (r & 3);
-                const bool there = (cur.ok >> (2 * h + (r >> 3)) & 1) && mine < seq.n;
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-                    sc[h][g] = there ? sc[h][g] : 0.0f;
-            }
         }
         uint32_t big = 0;                                // of the value scales
 #pragma unroll
         for (int h = 0; h < P / 2; ++h)
 #pragma unroll
             for (int g = 0; g < NG; ++g)
-                big = max(big, __float_as_uint(sc[h][g]));
+                big = max(big, abs_bits(sc[h][g]));
         big = (r & 4) ? big : 0u;
         if (__ballot(big >= scale_cap)) {                // rare: values larger than any before
-            big = max_rows_u32(group_max_u32<16>(big));
-            scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
-            scale_cap = cap_of(scale_exp);
+            big = max_rows_u32(group_max_u32<16>(big)) | some_hidden;
+            if (__builtin_amdgcn_readfirstlane(big) >= kNotFinite) {
+                // only what a row sees counts for it (a hidden key's score is -infinity)
+                uint32_t seen[RT][NG] = {};
+                each<4 * P>([&](auto ic) {
+                    constexpr int p = decltype(ic)::value / 4, j = decltype(ic)::value % 4;
+                    uint32_t keep[RT];
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        keep[t] = s[t][p][j] != -INFINITY ? 0x7fffffffu : 0u;
+                    each<NG>([&](auto gc) {
+                        constexpr int g = decltype(gc)::value;
+                        const uint32_t v = __float_as_uint(row_lane<8 * (p % 2) + 4 + j>(sc[p / 2][g]));
+#pragma unroll
+                        for (int t = 0; t < RT; ++t)
+                            seen[t][g] = max(seen[t][g], v & keep[t]);
+                    });
+                });
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t most = max_rows_u32(seen[t][g]);
+                        const bool finite = most < kNotFinite;
+                        scale_exp[t] = max(scale_exp[t], finite ? exponent_of(most) : kNoScale);
+                        spoilt[t] |= finite ? 0u : 1u << g;
+                    }
+                // and the weight 0 of an unseen key stays 0
+#pragma unroll
+                for (int h = 0; h < P / 2; ++h)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        sc[h][g] = abs_bits(sc[h][g]) >= kNotFinite ? 0.0f : sc[h][g];
+                int least = scale_exp[0];
+#pragma unroll
+                for (int t = 1; t < RT; ++t)
+                    least = min(least, scale_exp[t]);
+                scale_cap = cap_of(__builtin_amdgcn_readfirstlane(group_min_exponent<16>(least)));
+            } else {
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    scale_exp[t] = max(scale_exp[t], exponent_of(big));
+                scale_cap = max(scale_cap, cap_of(__builtin_amdgcn_readfirstlane(max(kNoScale, exponent_of(big)))));
+            }
 #pragma unroll
             for (int t = 0; t < RT; ++t)
-                bound[t] = ref[t] + (float)(kRange - scale_exp);
+                bound[t] = ref[t] + (float)(kRange - scale_exp[t]);
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
@@ -396,11 +437,11 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
             if (__ballot(m > bound[t])) {                // rare after the first steps
                 m = max_rows(m, m);
                 if (m > bound[t]) {
-                    const float nref = m + (float)(scale_exp - kHeadroom);
+                    const float nref = m + (float)(scale_exp[t] - kHeadroom);
                     const float alpha = exp2_hw(ref[t] - nref);   // 0 before the first key
                     l[t] *= alpha;
                     ref[t] = nref;
-                    bound[t] = nref + (float)(kRange - scale_exp);
+                    bound[t] = nref + (float)(kRange - scale_exp[t]);
 #pragma unroll
                     for (int k = 0; k < 2 * N32; ++k)
 #pragma unroll
@@ -497,9 +538,10 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
 #pragma unroll
             for (int x = 0; x < kWaves; ++x)
                 R = fmaxf(R, refs[x][16 * t + r]);
-            const float f = l[t] > 0.0f ? exp2_hw(ref[t] - R) : 0.0f;
+            const float keep = l[t] > 0.0f ? exp2_hw(ref[t] - R) : 0.0f;
 #pragma unroll
             for (int g = 0; g < N32; ++g) {
+                const float f = spoilt[t] >> (g / PER) & 1 ? NAN : keep;
                 // lane: dims 32 g + 8 b4 + 2 reg + e
                 float4 *dst = reinterpret_cast<float4 *>(&os[wave][r][32 * g + 8 * b4]);
                 dst[0] = make_float4(o[t][2 * g][0] * f, o[t][2 * g + 1][0] * f, o[t][2 * g][1] * f, o[t][2 * g + 1][1] * f);

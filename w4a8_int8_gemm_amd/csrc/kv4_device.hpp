@@ -79,6 +79,12 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+// The least of exponents over -128 over groups of lanes.
+template <int width> __device__ __forceinline__ int group_min_exponent(int e)
+{
+    return 128 - (int)group_max_u32<width>((uint32_t)(128 - e));
+}
+
 // Sum over groups of lanes, and the sum over the lanes up to and with one's own.
 template <int width> __device__ __forceinline__ uint32_t group_sum_u32(uint32_t v)
 {
@@ -135,6 +141,11 @@ __device__ __forceinline__ uint32_t max_rows_u32(uint32_t v)
     const auto q = __builtin_amdgcn_permlane32_swap(m, m, false, false);
     return max(q[0], q[1]);
 }
+__device__ __forceinline__ uint32_t max_halves_u32(uint32_t v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max(r[0], r[1]);
+}
 __device__ __forceinline__ float sum_halves(float v)
 {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -148,7 +159,10 @@ __device__ __forceinline__ float sum_rows(float v)
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// The exponent floor(log2 v) of a scale's bits, -127 for 0.
+// A scale's bits without its sign: numbers in their order, what is not finite
+// above them.  The exponent floor(log2 v) of a finite one, -127 for 0.
+constexpr uint32_t kNotFinite = 0x7f800000u;
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >> 23) - 127; }
 
 // Weights p = 2^(score - ref) are multiplied with their value's scale and
@@ -160,10 +174,13 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >>
 // keep all their bits (a row's heaviest key may have a code of 0 in some
 // element, whose result then comes from light keys alone; 7 binades of
 // headroom were too few there).  Sum and output have the same reference, and
-// any gives the same quotient.
+// any gives the same quotient.  e is a row's own, from the scales of the keys
+// that it sees: another's may be anything.  An unseen key's weight is 0, but 0
+// times a scale that is not finite is not: such scales are taken out of the
+// products, and rows that see one get NaN in the elements of its group.
 constexpr int kHeadroom = 12, kRange = 14;
 constexpr float kFarBelow = -1e30f;           // reference before any key: under every score
-constexpr int kNoScale = -100;                // exponent of the largest scale before any key
+constexpr int kNoScale = -100;                // exponent of the largest scale before any key, and the least
 __device__ __forceinline__ uint32_t cap_of(int e) { return (uint32_t)(e + 128) << 23; }   // bits of 2^(e + 1)
 
 // Values that other workgroups, on other chiplets with L2 caches of their

@@ -240,8 +240,9 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         for (int e = 0; e < 16; ++e)
             o[g][e] = 0.0f;
     float ref = kFarBelow, bound = kFarBelow, l = 0.0f;
-    int scale_exp = kNoScale;
-    uint32_t scale_cap = 0;                              // bits of 2^(scale_exp + 1)
+    int scale_exp = kNoScale;                            // of the largest value scale that the lane's row has seen
+    uint32_t scale_cap = 0;                              // bits of 2^(e + 1) for the least of the rows' scale_exp
+    uint32_t spoilt = 0;                                 // bit g: it has seen one of group g that is not finite
     const float score_scale = a.scale * kLog2e;
     // key of lane % 16 in the runs of four that the lane's half has of 32 keys
     const int lane_key = (lane & 15) / 4 * 8 + 4 * h + (lane & 3);
@@ -347,15 +348,45 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
             for (int g = 0; g < NG; ++g) {
                 ks[x][g] = ksc[buf][g][32 * x + lane_key];
                 vs[x][g] = vsc[buf][g][32 * x + lane_key];
-                big = max(big, __float_as_uint(vs[x][g]));
+                big = max(big, abs_bits(vs[x][g]));
             }
+        const bool some_hidden = t0 < lo_all || t0 + kKeys > hi_all || __ballot(fminf(ks[0][0], ks[1][0]) < 0.0f);
         if (__ballot(big >= scale_cap)) {                // rare: values larger than any before
             big = max_rows_u32(group_max_u32<16>(big));
-            scale_exp = max(scale_exp, __builtin_amdgcn_readfirstlane(exponent_of(big)));
-            scale_cap = cap_of(scale_exp);
+            if (some_hidden || big >= kNotFinite) {
+                // only what a row sees counts for it
+                uint32_t seen[NG] = {};
+                each<32>([&](auto ic) {
+                    constexpr int x = decltype(ic)::value / 16, e = decltype(ic)::value % 16;
+                    const int key = t0 + 32 * x + e / 4 * 8 + 4 * h + e % 4;
+                    const float there = row_lane<e>(ks[x][0]);
+                    const uint32_t keep = ((key >= lo) & (key < hi) & (there >= 0.0f)) ? 0x7fffffffu : 0u;
+                    each<NG>([&](auto gc) {
+                        constexpr int g = decltype(gc)::value;
+                        seen[g] = max(seen[g], __float_as_uint(row_lane<e>(vs[x][g])) & keep);
+                    });
+                });
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const uint32_t most = max_halves_u32(seen[g]);
+                    const bool finite = most < kNotFinite;
+                    scale_exp = max(scale_exp, finite ? exponent_of(most) : kNoScale);
+                    spoilt |= finite ? 0u : 1u << g;
+                }
+                // and the weight 0 of an unseen key stays 0
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int g = 0; g < NG; ++g)
+                        vs[x][g] = abs_bits(vs[x][g]) >= kNotFinite ? 0.0f : vs[x][g];
+                const int least = group_min_exponent<16>(scale_exp);
+                scale_cap = cap_of(min(__builtin_amdgcn_readlane(least, 0), __builtin_amdgcn_readlane(least, 16)));
+            } else {
+                scale_exp = max(scale_exp, exponent_of(big));
+                scale_cap = max(scale_cap, cap_of(__builtin_amdgcn_readfirstlane(max(kNoScale, exponent_of(big)))));
+            }
             bound = ref + (float)(kRange - scale_exp);
         }
-        const bool some_hidden = t0 < lo_all || t0 + kKeys > hi_all || __ballot(fminf(ks[0][0], ks[1][0]) < 0.0f);
         const float ks0 = ks[0][0], ks1 = ks[1][0];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
@@ -411,6 +442,13 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
             one(step + 1, std::integral_constant<int, 1>());
     }
 
+    if (spoilt) {
+#pragma unroll
+        for (int g = 0; g < N32; ++g)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                o[g][e] = spoilt >> (g / PER) & 1 ? NAN : o[g][e];
+    }
     l = sum_halves(l);
     if (parts > 1) {
         // ---- parts: left in the workspace in the order of the registers (a wave's
