@@ -370,7 +370,8 @@ size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t h
  *   kv_lens      int32 [sequences]: tokens in the cache, the queries' own among them
  *   q_starts     int32 [sequences + 1]: sequence b's queries are rows q_starts[b] up to
  *                q_starts[b + 1]; NULL: one query a sequence (T == sequences)
- *   max_q        no sequence has more queries than this (rows past it are not computed)
+ *   max_q        no sequence has more queries than this (rows past it are not computed
+ *                and their outputs not written; the others are as they are with a larger max_q)
  * With n = kv_lens[b] and m queries, query i of sequence b stands at position
  * p = n - m + i and sees the keys j < n; with `causal` only j <= p, and with
  * window > 0 (causal only) only j > p - window.  Over the keys seen,

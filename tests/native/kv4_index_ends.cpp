@@ -18,3 +18,13 @@ void steps(int m, int n, int causal, int window, int keys, int *out)
     out[0] = r.first, out[1] = r.count;
 }
 }
+
+extern "C" {
+void cut_and_see(int start, int end, int len, int T, int max_q, int most, int i, int causal, int window, int *out)
+{
+    const Kv4Seq s = kv4_cut(start, end, len, T, max_q, most);
+    const Kv4Steps r = kv4_steps(s, causal != 0, window, 32);
+    out[0] = s.q0, out[1] = s.m, out[2] = kv4_lo(s, i, window), out[3] = kv4_hi(s, i, causal != 0);
+    out[4] = r.first, out[5] = r.count;
+}
+}

@@ -5,6 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import w4a8_int8_gemm_amd as w  # noqa: E402
 from tests.kv4_util import attention  # noqa: E402
 from tests.test_gpu_kv4_attention import Case, dev  # noqa: E402
 
@@ -115,3 +116,21 @@ def test_values_far_larger_than_what_an_earlier_row_sees(m):
         c.c.v_scale[page, :, at] *= 2.0 ** 16
         c.v[b][n - 1] *= 2.0 ** 16
     check_rows(c, lambda b: range(m[b]))
+
+
+@pytest.mark.parametrize("m,most", [([6, 3], 4), ([6, 3], 1), ([70, 5], 40), ([70, 200], 64), ([33, 2], 3)])
+@pytest.mark.parametrize("window", [0, 9])
+def test_rows_past_max_q_are_not_computed_and_do_not_move_the_others(m, most, window):
+    c = Case([100, 210], m, 8, 2, 128, 64, 16, seed=27)
+    T = sum(m)
+    out = torch.full((T, 8, 128), float("nan"), dtype=torch.float16, device="cuda")
+    lse = torch.full((T, 8), float("nan"), device="cuda")
+    w.kv4_attention(dev(c.q), c.c, dev(c.table), dev(np.array(c.kv, np.int32)), q_starts=dev(c.starts), max_q=most,
+                    window=window, out=out, lse=lse)
+    out, lse = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    for b in range(2):
+        rows = slice(c.starts[b], c.starts[b + 1])
+        want, logs, ob, lb = attention(c.q[rows], c.k[b], c.v[b], c.there[b], None, None, True, window, 128 ** -0.5, 16)
+        kept = min(m[b], most)
+        assert (np.abs(out[rows] - want) <= ob)[:kept].all() and (np.abs(lse[rows] - logs) <= lb)[:kept].all()
+        assert np.isnan(out[rows][kept:]).all() and np.isnan(lse[rows][kept:]).all()

@@ -64,3 +64,20 @@ def test_a_tiles_parts_cover_its_keys_once(L):
                     if part0 <= part < part0 + parts:
                         got += range(s0, s1)
                 assert sorted(got) == sorted(want) and all(s <= max(0, n - 1) // 64 for s in got)
+
+
+def test_queries_past_max_q_do_not_move_the_others(L):
+    out = (ctypes.c_int * 6)()
+    for n, q, max_q, window, causal in itertools.product([0, 3, 100, 1 << 30], [1, 6, 200], [1, 4, 6, 1000], [0, 2, 50, TOP],
+                                                         [0, 1]):
+        if window and not causal:
+            continue
+        kept = min(q, max_q)
+        for i in {0, kept // 2, kept - 1}:
+            L.cut_and_see(3, 3 + q, n, 500, max_q, 1 << 30, i, causal, window, out)
+            lo, hi = seen_range(n, q, i, causal, window)
+            assert tuple(out[:4]) == (3, kept, lo, hi)
+            if lo < hi:
+                assert 32 * out[4] <= lo and hi <= 32 * (out[4] + out[5])
+    L.cut_and_see(0, TOP, 5, TOP, 1, 64, 0, 1, TOP, out)
+    assert tuple(out[:4]) == (0, 1, 0, 0)                       # far before the first key

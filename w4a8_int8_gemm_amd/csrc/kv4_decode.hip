@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
     }
     const int limit = kv4_part_limit(steps * c.heads, longest, KEYS);
     int b = -1, count = 0, parts = 0, id = blockIdx.x;   // id: within the sequences from b on
-    Kv4Seq seq = {0, 0, 0};
+    Kv4Seq seq = {0, 0, 0, 0};
     for (int base = 0; base < B; base += 64) {
         if (B > 64)
             lookup(base);
@@ -241,6 +241,7 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
             seq.q0 = __builtin_amdgcn_readlane(sl.q0, at);
             seq.m = __builtin_amdgcn_readlane(sl.m, at);
             seq.n = __builtin_amdgcn_readlane(sl.n, at);
+            seq.rest = __builtin_amdgcn_readlane(sl.rest, at);
             id -= __builtin_amdgcn_readlane(inc, at) - parts * c.heads;
             break;
         }
@@ -296,15 +297,15 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
 #pragma unroll
         for (int k = 0; k < N32; ++k)
             q[t][k] = order8(*reinterpret_cast<const uint4 *>(qp + 32 * k));
-        lo[t] = kv4_lo(seq.n, seq.m, i, a.window);
-        hi[t] = kv4_hi(seq.n, seq.m, i, a.causal);
+        lo[t] = kv4_lo(seq, i, a.window);
+        hi[t] = kv4_hi(seq, i, a.causal);
         ref[t] = bound[t] = kFarBelow;
         l[t] = 0.0f;
 #pragma unroll
         for (int k = 0; k < 2 * N32; ++k)
             o[t][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const int lo_most = kv4_lo(seq.n, seq.m, seq.m - 1, a.window), hi_least = kv4_hi(seq.n, seq.m, 0, a.causal);
+    const int lo_most = kv4_lo(seq, seq.m - 1, a.window), hi_least = kv4_hi(seq, 0, a.causal);
     // exponent of the largest value scale that a row has seen; bits of 2^(e + 1)
     // for the smallest of them
     int scale_exp[RT];

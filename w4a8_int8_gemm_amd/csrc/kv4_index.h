@@ -20,6 +20,7 @@ struct Kv4Seq {
     int q0;                     // first query row
     int m;                      // queries, all rows [q0, q0 + m) inside [0, T)
     int n;                      // keys, all inside the table's pages
+    int rest;                   // queries past max_q: not computed, but the last of them stands at the last key
 };
 
 // From the tables' entries: `start`, `end` the sequence's rows, `len` its keys
@@ -31,8 +32,9 @@ KV4_HD Kv4Seq kv4_cut(int start, int end, int len, int T, int max_q, int most)
     s.n = len < 0 ? 0 : len < most ? len : most;
     s.q0 = start < 0 ? 0 : start < T ? start : T;
     end = end < T ? end : T;
-    s.m = end > s.q0 ? end - s.q0 : 0;
-    s.m = s.m < max_q ? s.m : max_q;
+    const int all = end > s.q0 ? end - s.q0 : 0;
+    s.m = all < max_q ? all : max_q;
+    s.rest = all - s.m;
     return s;
 }
 
@@ -48,6 +50,10 @@ KV4_HD int kv4_lo(int n, int m, int i, int window)
     return window > 0 && p1 > window ? p1 - window : 0;
 }
 
+// Of a sequence's query i.
+KV4_HD int kv4_hi(const Kv4Seq &s, int i, bool causal) { return kv4_hi(s.n, s.m + s.rest, i, causal); }
+KV4_HD int kv4_lo(const Kv4Seq &s, int i, int window) { return kv4_lo(s.n, s.m + s.rest, i, window); }
+
 // Steps of `keys` keys that a sequence's queries need together; one (empty)
 // step where they see nothing, none without queries.
 struct Kv4Steps {
@@ -58,7 +64,7 @@ KV4_HD Kv4Steps kv4_steps(const Kv4Seq &s, bool causal, int window, int keys)
     Kv4Steps r = {0, 0};
     if (s.m == 0)
         return r;
-    const int hi = kv4_hi(s.n, s.m, s.m - 1, causal), lo = kv4_lo(s.n, s.m, 0, window);
+    const int hi = kv4_hi(s, s.m - 1, causal), lo = kv4_lo(s, 0, window);
     r.first = lo / keys;
     r.count = (int)(((int64_t)hi + keys - 1) / keys) - r.first;
     r.count = r.count < 1 ? 1 : r.count;
@@ -123,7 +129,7 @@ struct Kv4TilePart {
 KV4_HD Kv4TilePart kv4_tile_part(const Kv4Seq &s, bool causal, int window, int keys, int i0, int i1, const Kv4Steps &r,
                                  int cuts, int part)
 {
-    const int lo = kv4_lo(s.n, s.m, i0, window), hi = kv4_hi(s.n, s.m, i1, causal);
+    const int lo = kv4_lo(s, i0, window), hi = kv4_hi(s, i1, causal);
     const int width = (r.count + cuts - 1) / cuts;
     const int begin = lo / keys - r.first, past = (hi + keys - 1) / keys - r.first, end = past > begin ? past : begin;
     Kv4TilePart t;

@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
     }
     const int limit = kv4_tile_limit(steps * c.heads, kKeys);
     int b = -1, tiles = 0, cuts = 0, id = blockIdx.x, split = 0;   // split: slots before b's
-    Kv4Seq seq = {0, 0, 0};
+    Kv4Seq seq = {0, 0, 0, 0};
     for (int base = 0; base < B; base += 64) {
         if (B > 64)
             lookup(base);
@@ -79,6 +79,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
             seq.q0 = __builtin_amdgcn_readlane(sl.q0, at);
             seq.m = __builtin_amdgcn_readlane(sl.m, at);
             seq.n = __builtin_amdgcn_readlane(sl.n, at);
+            seq.rest = __builtin_amdgcn_readlane(sl.rest, at);
             id -= __builtin_amdgcn_readlane(inc, at) - tiles * cuts * c.heads;
             split += cuts > 1 ? __builtin_amdgcn_readlane(sinc, at) - tiles * cuts * c.heads : 0;
             break;
@@ -120,12 +121,12 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
         for (int k = 0; k < D / 16; ++k)
             q[k] = order8(*reinterpret_cast<const uint4 *>(qp + 16 * k));
     }
-    const int lo = kv4_lo(seq.n, seq.m, qi, a.window), hi = kv4_hi(seq.n, seq.m, qi, a.causal);
+    const int lo = kv4_lo(seq, qi, a.window), hi = kv4_hi(seq, qi, a.causal);
     // of the wave's rows: keys that all see, keys that any sees
     const int wrow0 = min(row0 + 32 * wave, rows - 1), wrow1 = min(row0 + 32 * wave + 31, rows - 1);
     const int wi0 = query_of(wrow0, w.over_group, group), wi1 = query_of(wrow1, w.over_group, group);
-    const int lo_any = kv4_lo(seq.n, seq.m, wi0, a.window), lo_all = kv4_lo(seq.n, seq.m, wi1, a.window);
-    const int hi_all = kv4_hi(seq.n, seq.m, wi0, a.causal), hi_any = kv4_hi(seq.n, seq.m, wi1, a.causal);
+    const int lo_any = kv4_lo(seq, wi0, a.window), lo_all = kv4_lo(seq, wi1, a.window);
+    const int hi_all = kv4_hi(seq, wi0, a.causal), hi_any = kv4_hi(seq, wi1, a.causal);
 
     // ---- the producer's side of a thread
     const int32_t *table = a.table + (int64_t)b * a.max_pages;
