@@ -134,3 +134,43 @@ def test_rows_past_max_q_are_not_computed_and_do_not_move_the_others(m, most, wi
         kept = min(m[b], most)
         assert (np.abs(out[rows] - want) <= ob)[:kept].all() and (np.abs(lse[rows] - logs) <= lb)[:kept].all()
         assert np.isnan(out[rows][kept:]).all() and np.isnan(lse[rows][kept:]).all()
+
+
+@pytest.mark.parametrize("n", [70001, 131075])
+@pytest.mark.parametrize("m,hq", [(1, 8), (2, 8), (40, 2)])
+def test_zero_values_of_many_keys(n, m, hq):
+    """All scores are 0: the log of the sum is log n; then values behind n - 4000 zero ones."""
+    page, D, G = 1024, 64, 32
+    pages = -(-n // page)
+    c = w.KV4Cache.empty(pages, 1, page, D, G)
+    for t in (c.k, c.v, c.k_scale, c.v_scale):
+        t.zero_()
+    q = torch.zeros((m, hq, D), dtype=torch.float16, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+
+    def call():
+        out, lse = w.kv4_attention(q, c, table, lens, q_starts=starts, max_q=m, causal=False, return_lse=True)
+        # a sum of n ones in fp32: n u; the log and its factor a few steps
+        assert bool(((lse.double() - float(np.log(n))).abs() <= n * 2.0 ** -24 + 64 * 2.0 ** -24).all())
+        return out.double()
+
+    assert bool((call() == 0).all())
+    at = torch.arange(n - 4000, n, device="cuda")
+    c.v[at // page, 0, at % page] = 0x77
+    c.v_scale[at // page, 0, at % page] = 2.0
+    want = 14.0 * 4000 / n
+    # the output's rounding and the weights', and the two sums
+    assert bool(((call() - want).abs() <= want * (2 * 2.0 ** -11 + 2 * n * 2.0 ** -24)).all())
+
+
+@pytest.mark.parametrize("m", [1, 40])
+@pytest.mark.parametrize("exponent", [-24, -27, -36])
+def test_the_smallest_values(m, exponent):
+    """Scales down to the smallest that the writer makes (2^-24 / 7), and below: what fp16 holds of them."""
+    c = Case([90], [m], 4, 2, 64, 32, 16, seed=28)
+    f = np.float32(2.0) ** exponent
+    c.c.v_scale.mul_(float(f))
+    c.v[0] = c.v[0] * float(f)
+    check_rows(c, lambda b: range(m))

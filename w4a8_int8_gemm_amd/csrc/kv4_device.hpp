@@ -180,7 +180,10 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >>
 // products, and rows that see one get NaN in the elements of its group.
 constexpr int kHeadroom = 12, kRange = 14;
 constexpr float kFarBelow = -1e30f;           // reference before any key: under every score
-constexpr int kNoScale = -100;                // exponent of the largest scale before any key, and the least
+// Exponent of the largest scale before any key, and the least that is told
+// apart: smaller scales' values round to 0 in fp16 (8 * 2^-40 < 2^-25) and
+// are taken as that, and weights stay below 2^55, sums of 2^30 of them in range.
+constexpr int kNoScale = -40;
 __device__ __forceinline__ uint32_t cap_of(int e) { return (uint32_t)(e + 128) << 23; }   // bits of 2^(e + 1)
 
 // Values that other workgroups, on other chiplets with L2 caches of their
