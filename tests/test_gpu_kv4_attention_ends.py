@@ -174,3 +174,14 @@ def test_the_smallest_values(m, exponent):
     c.c.v_scale.mul_(float(f))
     c.v[0] = c.v[0] * float(f)
     check_rows(c, lambda b: range(m))
+
+
+@pytest.mark.parametrize("hq,hk", [(8, 2), (40, 1)])
+@pytest.mark.parametrize("scale", [1e28, 1e31, 1e36, 2.0 ** 120])
+def test_scores_far_below_zero(hq, hk, scale):
+    """A row's only key has all its weight whatever its score is (|scores| up to about 2^125)."""
+    c = Case([1, 1, 1, 1], [1, 1, 1, 1], hq, hk, 64, 32, 16, seed=29)
+    out = c.check(scale=scale)
+    for b in range(4):
+        v = np.repeat(c.v[b][0], hq // hk, 0)
+        assert (np.abs(out[b] - v) <= 2 * 2.0 ** -11 * np.abs(v) + 2.0 ** -25).all()

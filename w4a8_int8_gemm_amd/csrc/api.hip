@@ -907,8 +907,8 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
     if (window < 0 || (window > 0 && !causal))
         return fail(W4A8_ERR_INVALID_ARG, "%s: window=%d needs causal and must not be negative", fn,
                     (int)window);
-    if (!(scale > 0.0f) || scale > 3.0e38f)
-        return fail(W4A8_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+    if (!(scale > 0.0f) || scale > 0x1p127f)             // scale * log2(e) has to be finite
+        return fail(W4A8_ERR_INVALID_ARG, "%s: scale must be positive and at most 2^127", fn);
     if (!q_starts && (T != sequences || (T > 0 && max_q < 1)))
         return fail(W4A8_ERR_SHAPE, "%s: without q_starts, T=%lld must equal sequences=%lld and "
                     "max_q be at least 1", fn, (long long)T, (long long)sequences);

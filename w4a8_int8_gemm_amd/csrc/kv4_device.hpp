@@ -179,7 +179,7 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >>
 // times a scale that is not finite is not: such scales are taken out of the
 // products, and rows that see one get NaN in the elements of its group.
 constexpr int kHeadroom = 12, kRange = 14;
-constexpr float kFarBelow = -1e30f;           // reference before any key: under every score
+constexpr float kFarBelow = -3.4028234664e38f; // reference before any key: under every score
 // Exponent of the largest scale before any key, and the least that is told
 // apart: smaller scales' values round to 0 in fp16 (8 * 2^-40 < 2^-25) and
 // are taken as that, and weights stay below 2^55, sums of 2^30 of them in range.
