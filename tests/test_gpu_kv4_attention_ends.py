@@ -185,3 +185,24 @@ def test_scores_far_below_zero(hq, hk, scale):
     for b in range(4):
         v = np.repeat(c.v[b][0], hq // hk, 0)
         assert (np.abs(out[b] - v) <= 2 * 2.0 ** -11 * np.abs(v) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("m", [[1, 3], [40, 70]])
+@pytest.mark.parametrize("gain,scale", [(1e-3, s) for s in (1e7, 1e8, 1e9, 4e9, 1e10, 3e10, 1e11, 1e12)] +
+                         [(1.0, 1e6), (1.0, 1e7), (1e-6, 1e14), (100.0, 1e4), (1000.0, 1e3)])
+def test_scores_whose_steps_are_larger_than_one(m, gain, scale):
+    """Scores past 2^24, which fp32 holds in steps of 2 and more: one key has all the weight."""
+    c = Case([300, 129], m, 4, 2, 128, 32, 16, seed=30, gain=gain)
+    out = c.check(scale=scale)
+    first = 0
+    for b, q in enumerate(m):
+        for i in range(q):
+            n = c.kv[b] - q + i + 1
+            for h in range(4):
+                s = c.k[b][:n, h // 2] @ c.q[first + i, h].astype(np.float64) * scale
+                top = np.argsort(s)[-2:]
+                reach = (np.abs(c.k[b][:n, h // 2]) @ np.abs(c.q[first + i, h].astype(np.float64))).max() * scale
+                if s[top[1]] - s[top[0]] > 2 * (128 + 8) * 2.0 ** -23 * reach + 40:    # a second key's weight is under e^-40
+                    v = c.v[b][top[1], h // 2]
+                    assert (np.abs(out[first + i, h] - v) <= 2 * 2.0 ** -11 * np.abs(v) + 16 * 2.0 ** -25).all()
+        first += q

@@ -427,7 +427,7 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
             }
 #pragma unroll
             for (int t = 0; t < RT; ++t)
-                bound[t] = ref[t] + (float)(kRange - scale_exp[t]);
+                bound[t] = bound_for(ref[t], scale_exp[t]);
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
@@ -438,11 +438,11 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
             if (__ballot(m > bound[t])) {                // rare after the first steps
                 m = max_rows(m, m);
                 if (m > bound[t]) {
-                    const float nref = m + (float)(scale_exp[t] - kHeadroom);
+                    const float nref = reference_for(ref[t], m, scale_exp[t]);
                     const float alpha = exp2_hw(ref[t] - nref);   // 0 before the first key
                     l[t] *= alpha;
                     ref[t] = nref;
-                    bound[t] = nref + (float)(kRange - scale_exp[t]);
+                    bound[t] = bound_for(nref, scale_exp[t]);
 #pragma unroll
                     for (int k = 0; k < 2 * N32; ++k)
 #pragma unroll

@@ -184,6 +184,20 @@ constexpr float kFarBelow = -3.4028234664e38f; // reference before any key: unde
 // apart: smaller scales' values round to 0 in fp16 (8 * 2^-40 < 2^-25) and
 // are taken as that, and weights stay below 2^55, sums of 2^30 of them in range.
 constexpr int kNoScale = -40;
+// The reference for a row whose largest score is m (it never falls), and the
+// bound above one.  Scores from 2^24 on are held in steps of 2 and more: where a
+// sum is off by more than a binade the reference is m itself, and where the
+// bound would be up by more than half a one it is the reference.
+__device__ __forceinline__ float reference_for(float ref, float m, int e)
+{
+    const float below = (float)(kHeadroom - e), next = m - below;
+    return fmaxf(ref, fabsf((m - next) - below) > 1.0f ? m : next);
+}
+__device__ __forceinline__ float bound_for(float ref, int e)
+{
+    const float above = (float)(kRange - e), bound = ref + above;
+    return (bound - ref) - above > 0.5f ? ref : bound;
+}
 __device__ __forceinline__ uint32_t cap_of(int e) { return (uint32_t)(e + 128) << 23; }   // bits of 2^(e + 1)
 
 // Values that other workgroups, on other chiplets with L2 caches of their

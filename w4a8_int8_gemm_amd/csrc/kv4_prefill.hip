@@ -292,11 +292,11 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
     const auto rescale = [&](float m, float *s, int pending) {
         m = max_halves(m);
         if (m > bound) {
-            const float nref = m + (float)(scale_exp - kHeadroom);
+            const float nref = reference_for(ref, m, scale_exp);
             const float alpha = exp2_hw(ref - nref);     // 0 before the first key
             l *= alpha;
             ref = nref;
-            bound = ref + (float)(kRange - scale_exp);
+            bound = bound_for(ref, scale_exp);
 #pragma unroll
             for (int g = 0; g < N32; ++g)
 #pragma unroll
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
                 scale_exp = max(scale_exp, exponent_of(big));
                 scale_cap = max(scale_cap, cap_of(__builtin_amdgcn_readfirstlane(max(kNoScale, exponent_of(big)))));
             }
-            bound = ref + (float)(kRange - scale_exp);
+            bound = bound_for(ref, scale_exp);
         }
         const float ks0 = ks[0][0], ks1 = ks[1][0];
 #pragma unroll
