@@ -306,6 +306,7 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
             o[t][k] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
     }
     const int lo_most = kv4_lo(seq, seq.m - 1, a.window), hi_least = kv4_hi(seq, 0, a.causal);
+    const int lo_first = kv4_lo(seq, 0, a.window), hi_last = kv4_hi(seq, seq.m - 1, a.causal);
     // exponent of the largest value scale that a row has seen; bits of 2^(e + 1)
     // for the smallest of them
     int scale_exp[RT];
@@ -359,18 +360,26 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
         // a step that not every row sees whole: hide keys, whatever stands for them
         uint32_t some_hidden = 0;                        // a number: branching on the condition twice cost 17 registers
         if (cur.ok != (1u << P) - 1 || t0 < lo_most || t0 > hi_least - KEYS) {
-            some_hidden = kNotFinite;
+            some_hidden = seq.m > 1 ? kNotFinite : 0u;   // one query's rows all see the same
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                const bool page_ok = (cur.ok >> p) & 1;
+                const bool there = (cur.ok >> p) & 1;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int key = t0 + 16 * p + 4 * b4 + j;
-                    const bool there = page_ok && key < seq.n;
 #pragma unroll
                     for (int t = 0; t < RT; ++t)
                         s[t][p][j] = there && key >= lo[t] && key < hi[t] ? s[t][p][j] : -INFINITY;
                 }
+            }
+            // values that no row sees
+#pragma unroll
+            for (int h = 0; h < P / 2; ++h) {
+                const int mine = t0 + 32 * h + 2 * (r & 8) + 4 * b4 + (r & 3);
+                const bool there = (cur.ok >> (2 * h + (r >> 3)) & 1) && mine >= lo_first && mine < hi_last;
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+                    sc[h][g] = there ? sc[h][g] : 0.0f;
             }
         }
         uint32_t big = 0;                                // of the value scales

@@ -79,6 +79,26 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+// Maximum over the lanes up to one's own of 16, and from one's own on; the value of the next lane of 16.
+__device__ __forceinline__ uint32_t prefix_max16(uint32_t v)
+{
+    v = max(v, (uint32_t)W4A8_DPP((int)v, 0x111, 0xf));   // row_shr:1, 2, 4, 8
+    v = max(v, (uint32_t)W4A8_DPP((int)v, 0x112, 0xf));
+    v = max(v, (uint32_t)W4A8_DPP((int)v, 0x114, 0xf));
+    return max(v, (uint32_t)W4A8_DPP((int)v, 0x118, 0xf));
+}
+__device__ __forceinline__ uint32_t suffix_max16(uint32_t v)
+{
+    v = max(v, (uint32_t)W4A8_DPP((int)v, 0x101, 0xf));   // row_shl:1, 2, 4, 8
+    v = max(v, (uint32_t)W4A8_DPP((int)v, 0x102, 0xf));
+    v = max(v, (uint32_t)W4A8_DPP((int)v, 0x104, 0xf));
+    return max(v, (uint32_t)W4A8_DPP((int)v, 0x108, 0xf));
+}
+__device__ __forceinline__ float next_of_16(float v)
+{
+    return __uint_as_float((uint32_t)W4A8_DPP((int)__float_as_uint(v), 0x12f, 0xf));   // row_ror:15
+}
+
 // The least of exponents over -128 over groups of lanes.
 template <int width> __device__ __forceinline__ int group_min_exponent(int e)
 {

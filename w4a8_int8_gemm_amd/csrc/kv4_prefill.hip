@@ -31,7 +31,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr int kRows = kTileRows, kKeys = 64, kThreads = 2 * kRows;
 
 template <int D, int NG>
-__global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
+__global__ __launch_bounds__(kThreads, D == 64 ? 3 : D < 256 ? 2 : 1) void kv4_prefill_kernel(Kv4Cache c, Kv4AttnArgs a, Partial w)
 {
     constexpr int N32 = D / 32, PER = N32 / NG, KC = D / 8, VC = kKeys / 8;
     // a piece more in a row than it holds: 16 rows' pieces are on different banks
@@ -349,24 +349,58 @@ __global__ __launch_bounds__(kThreads, D < 256 ? 2 : 1) void kv4_prefill_kernel(
             for (int g = 0; g < NG; ++g) {
                 ks[x][g] = ksc[buf][g][32 * x + lane_key];
                 vs[x][g] = vsc[buf][g][32 * x + lane_key];
-                big = max(big, abs_bits(vs[x][g]));
+                big = max(big, __float_as_uint(vs[x][g]));   // a sign counts as not finite: it is looked at
             }
         const bool some_hidden = t0 < lo_all || t0 + kKeys > hi_all || __ballot(fminf(ks[0][0], ks[1][0]) < 0.0f);
         if (__ballot(big >= scale_cap)) {                // rare: values larger than any before
             big = max_rows_u32(group_max_u32<16>(big));
             if (some_hidden || big >= kNotFinite) {
                 // only what a row sees counts for it
+                const auto before = [&](int edge, int x) {   // how many of the lane's 16 keys of half x
+                    const int u = min(max(edge - t0 - 32 * x - 4 * h, 0), 32);
+                    return (u >> 3) * 4 + min(u & 7, 4);
+                };
+                const int from0 = before(lo, 0), from1 = before(lo, 1), to0 = before(hi, 0), to1 = before(hi, 1);
+                const int row16 = lane & 48;
                 uint32_t seen[NG] = {};
-                each<32>([&](auto ic) {
-                    constexpr int x = decltype(ic)::value / 16, e = decltype(ic)::value % 16;
-                    const int key = t0 + 32 * x + e / 4 * 8 + 4 * h + e % 4;
-                    const float there = row_lane<e>(ks[x][0]);
-                    const uint32_t keep = ((key >= lo) & (key < hi) & (there >= 0.0f)) ? 0x7fffffffu : 0u;
-                    each<NG>([&](auto gc) {
-                        constexpr int g = decltype(gc)::value;
-                        seen[g] = max(seen[g], __float_as_uint(row_lane<e>(vs[x][g])) & keep);
-                    });
-                });
+                if (t0 >= lo_all) {
+                    // the rows see the first so many of a half: maxima over as many lanes
+                    const int at0 = row16 + max(to0 - 1, 0), at1 = row16 + max(to1 - 1, 0);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t v0 = __shfl(prefix_max16(abs_bits(vs[0][g])), at0);
+                        const uint32_t v1 = __shfl(prefix_max16(abs_bits(vs[1][g])), at1);
+                        seen[g] = max(to0 ? v0 : 0u, to1 ? v1 : 0u);
+                    }
+                } else if (!__ballot((from0 > 0 && from0 < to0 && to0 < 16) || (from1 > 0 && from1 < to1 && to1 < 16))) {
+                    // or the last so many
+                    const int at0 = row16 + (from0 ? from0 & 15 : max(to0 - 1, 0));
+                    const int at1 = row16 + (from1 ? from1 & 15 : max(to1 - 1, 0));
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t v0 = abs_bits(vs[0][g]), v1 = abs_bits(vs[1][g]);
+                        const uint32_t f0 = __shfl(prefix_max16(v0), at0), l0 = __shfl(suffix_max16(v0), at0);
+                        const uint32_t f1 = __shfl(prefix_max16(v1), at1), l1 = __shfl(suffix_max16(v1), at1);
+                        seen[g] = max(from0 < to0 ? (from0 ? l0 : f0) : 0u, from1 < to1 ? (from1 ? l1 : f1) : 0u);
+                    }
+                } else {
+                    // or some between: each lane's scales go round the 16 lanes
+                    const uint32_t sees0 = (1u << to0) - (1u << min(to0, from0));
+                    const uint32_t sees1 = (1u << to1) - (1u << min(to1, from1));
+                    uint32_t at = lane & 15;
+#pragma unroll 1
+                    for (int i = 0; i < 16; ++i) {
+                        const bool keep0 = sees0 >> at & 1, keep1 = sees1 >> at & 1;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            seen[g] = max(seen[g], keep0 ? abs_bits(vs[0][g]) : 0u);
+                            seen[g] = max(seen[g], keep1 ? abs_bits(vs[1][g]) : 0u);
+                            vs[0][g] = next_of_16(vs[0][g]);
+                            vs[1][g] = next_of_16(vs[1][g]);
+                        }
+                        at = (at + 1) & 15;
+                    }
+                }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const uint32_t most = max_halves_u32(seen[g]);
