@@ -380,7 +380,9 @@ size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t h
  * out = 0 and lse = -infinity.  Scores, sums and outputs are held in fp32; the
  * codes enter the fp16 matrix products exactly.  Besides the output's rounding
  * the weights softmax * v_scale are rounded: to 22 bits where a sequence has at
- * most 32 rows (queries x query heads of a kv head) and 1024 keys, else to fp16.
+ * most 32 rows (queries x query heads of a kv head) and its first query sees at
+ * most 1024 keys, else to fp16 (to fp16 too where T = sequences * max_q for more
+ * than 32 rows, which leaves no shorter sequence if q_starts covers all T rows).
  * out fp16 [T, q_heads, head_dim] contiguous; lse fp32 [T, q_heads] or NULL.
  * What the device-side tables hold is bounded, not trusted: kv_lens are cut to
  * [0, max_pages * page_size], tokens of pages outside [0, pages) are not seen,

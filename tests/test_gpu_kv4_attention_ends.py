@@ -206,3 +206,25 @@ def test_scores_whose_steps_are_larger_than_one(m, gain, scale):
                     v = c.v[b][top[1], h // 2]
                     assert (np.abs(out[first + i, h] - v) <= 2 * 2.0 ** -11 * np.abs(v) + 16 * 2.0 ** -25).all()
         first += q
+
+
+def check_two_part_weights(c, out, causal=True, window=0):
+    """The bound of the definition with weights of 22 bits: p |v| is the output of |v|."""
+    for b in range(len(c.kv)):
+        rows = slice(c.starts[b], c.starts[b + 1])
+        args = (c.there[b], None, None, causal, window, c.D ** -0.5, c.page)
+        want, _, ob, _ = attention(c.q[rows], c.k[b], c.v[b], *args)
+        reach = attention(c.q[rows], c.k[b], np.abs(c.v[b]), *args)[0]
+        tight = ob - (2.0 ** -11 - 2.0 ** -22) * 1.01 * reach
+        assert (np.abs(out[rows] - want) <= tight).all(), float((np.abs(out[rows] - want) / tight).max())
+
+
+@pytest.mark.parametrize("kv,m,window", [([900, 30], [1, 3], 0), ([5000], [1], 16), ([5000, 2000], [5, 1], 100),
+                                         ([3000], [4], 1024), ([1024 + 3], [4], 0)])
+def test_weights_have_22_bits_where_a_row_sees_few_keys(kv, m, window):
+    """Few keys seen, not few keys in the cache: a window behind a long context counts as a short one."""
+    c = Case(kv, m, 4, 2, 128, 64, 16, seed=31)
+    c.q[:] = 0                                            # equal weights: no error of the scores hides their rounding
+    c.check(window=window)
+    out, _ = c.run(window=window)
+    check_two_part_weights(c, out.cpu().numpy().astype(np.float64), window=window)

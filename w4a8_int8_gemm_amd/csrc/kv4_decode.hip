@@ -316,10 +316,11 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
     for (int t = 0; t < RT; ++t)
         scale_exp[t] = kNoScale, spoilt[t] = 0;
     const float score_scale = a.scale * kLog2e;
-    // Where a row has few keys, one rounding of a weight is in every element of
-    // its output: the weights are taken as two fp16 values, 22 bits.  (With more
-    // keys the roundings average out and the second product costs 6 to 9 %.)
-    const bool fine = seq.n <= kLeastKeys;
+    // Where a row sees few keys, one rounding of a weight is in every element of
+    // its output: the weights are taken as two fp16 values, 22 bits, if any row
+    // of the sequence sees so few.  (With more keys the roundings average out and
+    // the second product costs 6 to 9 %.)
+    const bool fine = hi_least - lo_first <= kFewKeys;
 
     const auto compute = [&](const Step<P, N32, NG> &cur, int step) {
         const int t0 = step * KEYS;

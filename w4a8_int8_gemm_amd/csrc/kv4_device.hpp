@@ -199,6 +199,8 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >>
 // times a scale that is not finite is not: such scales are taken out of the
 // products, and rows that see one get NaN in the elements of its group.
 constexpr int kHeadroom = 12, kRange = 14;
+// The kernel for few rows takes weights as two fp16 values where a row sees at most this many keys.
+constexpr int kFewKeys = 1024;
 constexpr float kFarBelow = -3.4028234664e38f; // reference before any key: under every score
 // Exponent of the largest scale before any key, and the least that is told
 // apart: smaller scales' values round to 0 in fp16 (8 * 2^-40 < 2^-25) and
