@@ -369,7 +369,8 @@ size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t h
  *   page_table   int32 [sequences, max_pages]: page of tokens [p page_size, (p + 1) page_size)
  *   kv_lens      int32 [sequences]: tokens in the cache, the queries' own among them
  *   q_starts     int32 [sequences + 1]: sequence b's queries are rows q_starts[b] up to
- *                q_starts[b + 1]; NULL: one query a sequence (T == sequences)
+ *                q_starts[b + 1]; NULL: one query a sequence (T == sequences).  Rows that no
+ *                sequence has are not read, and their outputs not written
  *   max_q        no sequence has more queries than this (rows past it are not computed
  *                and their outputs not written; the others are as they are with a larger max_q)
  * With n = kv_lens[b] and m queries, query i of sequence b stands at position

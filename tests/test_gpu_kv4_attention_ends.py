@@ -228,3 +228,23 @@ def test_weights_have_22_bits_where_a_row_sees_few_keys(kv, m, window):
     c.check(window=window)
     out, _ = c.run(window=window)
     check_two_part_weights(c, out.cpu().numpy().astype(np.float64), window=window)
+
+
+@pytest.mark.parametrize("m", [[1, 1, 1], [3, 1, 0], [40, 2, 7]])
+def test_a_buffer_of_full_size_with_shorter_ranges(m):
+    """As a captured call has it: rows for max_q queries of every sequence, q_starts gives fewer; the rows
+    of no sequence are not written."""
+    c = Case([100, 210, 64], m, 8, 2, 128, 64, 16, seed=32)
+    T, most = 3 * 40, 40
+    q = torch.full((T, 8, 128), float("nan"), dtype=torch.float16, device="cuda")
+    q[:sum(m)] = dev(c.q)
+    out = torch.full((T, 8, 128), float("nan"), dtype=torch.float16, device="cuda")
+    lse = torch.full((T, 8), float("nan"), device="cuda")
+    w.kv4_attention(q, c.c, dev(c.table), dev(np.array(c.kv, np.int32)), q_starts=dev(c.starts), max_q=most, out=out,
+                    lse=lse)
+    out, lse = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    for b in range(3):
+        rows = slice(c.starts[b], c.starts[b + 1])
+        want, logs, ob, lb = attention(c.q[rows], c.k[b], c.v[b], c.there[b], None, None, True, 0, 128 ** -0.5, 16)
+        assert (np.abs(out[rows] - want) <= ob).all() and (np.abs(lse[rows] - logs) <= lb).all()
+    assert np.isnan(out[sum(m):]).all() and np.isnan(lse[sum(m):]).all()

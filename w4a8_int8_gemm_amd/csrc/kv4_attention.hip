@@ -39,8 +39,11 @@ size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int 
 void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st)
 {
     const bool many = (int64_t)a.group * a.max_q > kDecodeRows;
-    // Where all sequences have max_q queries, or one query is too many rows for
-    // the kernel for few, the other kernel takes them all.
+    // Where one query is too many rows for the kernel for few, or all sequences
+    // have max_q queries (they do if T = B max_q and q_starts covers all rows),
+    // the other kernel takes them all: one launch instead of two.  It is right
+    // for every sequence, so that ranges which cover fewer rows cost time only,
+    // and the weights' second part.
     const bool few = a.group <= kDecodeRows && !(many && a.T == (int64_t)a.B * a.max_q);
     if (few)
         launch_kv4_decode(c, a, decode_rows(a.group, a.max_q), st);
