@@ -248,3 +248,17 @@ def test_a_buffer_of_full_size_with_shorter_ranges(m):
         want, logs, ob, lb = attention(c.q[rows], c.k[b], c.v[b], c.there[b], None, None, True, 0, 128 ** -0.5, 16)
         assert (np.abs(out[rows] - want) <= ob).all() and (np.abs(lse[rows] - logs) <= lb).all()
     assert np.isnan(out[sum(m):]).all() and np.isnan(lse[sum(m):]).all()
+
+
+@pytest.mark.parametrize("m", [[5, 3], [70, 40]])
+def test_without_max_q_every_row_is_computed(m):
+    """q_starts alone says how many queries a sequence has."""
+    c = Case([100, 90], m, 8, 2, 128, 64, 16, seed=33)
+    good, logs = c.run()
+    args = dev(c.q), c.c, dev(c.table), dev(np.array(c.kv, np.int32))
+    out, lse = w.kv4_attention(*args, q_starts=dev(c.starts), return_lse=True)
+    assert torch.equal(out, good) and torch.equal(lse, logs)
+    ws = w.kv4_attention_workspace(c.c, 8, sum(m), 2)     # of one query a sequence: too small is said, not taken
+    if max(m) * 4 > 32:
+        with pytest.raises(w.W4A8Error, match="workspace"):
+            w.kv4_attention(*args, q_starts=dev(c.starts), workspace=ws)

@@ -217,13 +217,14 @@ def kv4_attention_workspace(cache, q_heads: int, tokens: int, sequences: int, ma
     return torch.empty((need,), dtype=torch.uint8, device=cache.device)
 
 
-def kv4_attention(q, cache, page_table, kv_lens, q_starts=None, max_q: int = 1, causal: bool = True,
+def kv4_attention(q, cache, page_table, kv_lens, q_starts=None, max_q=None, causal: bool = True,
                   window: int = 0, scale=None, workspace=None, out=None, lse=None,
                   return_lse: bool = False):
     """Attention of T query rows (fp16 [T, q_heads, head_dim], tokens may be strided) over the
     cache: page_table int32 [sequences, max_pages], kv_lens int32 [sequences] (the queries' own
     tokens counted), q_starts int32 [sequences + 1] (default: one query a sequence), max_q an
-    upper bound of a sequence's queries.  scale defaults to head_dim ** -0.5.  workspace: of
+    upper bound of a sequence's queries (default: T with q_starts, which suits any; rows past it
+    and rows in no sequence are not written).  scale defaults to head_dim ** -0.5.  workspace: of
     kv4_attention_workspace (default: a new one).  Returns out fp16 [T, q_heads, head_dim], with
     return_lse (out, lse fp32 [T, q_heads])."""
     index = _cache(cache)._index
@@ -244,6 +245,8 @@ def kv4_attention(q, cache, page_table, kv_lens, q_starts=None, max_q: int = 1, 
                          f"for {B} sequences")
     else:
         starts = None
+    if max_q is None:
+        max_q = 1 if q_starts is None else T
     L = lib()
     if workspace is None:
         need = L.kv4_attention_workspace_size(heads, cache.kv_heads, D, T, B, max_q)
