@@ -1,10 +1,12 @@
 """Arguments of the attention block at the ends of their ranges (no GPU needed)."""
+import ctypes
+
 import pytest
 
 pytest.importorskip("torch")
 
 import w4a8_int8_gemm_amd as w  # noqa: E402
-from tests.test_kv4_checks import MIS, S, attention  # noqa: E402
+from tests.test_kv4_checks import MIS, S, attention, cache, cpu_ok, f16, i32, i64  # noqa: E402,F401
 
 
 @pytest.mark.parametrize("scale", [2.0 ** 127 * 1.01, 3e38, 3.4e38])
@@ -13,3 +15,39 @@ def test_scales_whose_exponent_leaves_fp32(scale):
     assert attention(scale=scale) == S.ERR_INVALID_ARG
     assert attention(scale=2.0 ** 127, q=MIS) == S.ERR_ALIGNMENT      # taken; what is refused comes later
     assert w.lib().w4a8_last_error()
+
+
+class Recorder:
+    """The C library's kv4_attention, its numbers kept instead of run."""
+
+    def __init__(self, monkeypatch):
+        from w4a8_int8_gemm_amd import kv4
+        real = w.lib()
+        rec = self
+
+        class Lib:
+            kv4_attention_workspace_size = staticmethod(real.kv4_attention_workspace_size)
+            kv4_attention = "kv4_attention"
+
+        monkeypatch.setattr(kv4, "lib", Lib)
+        monkeypatch.setattr(kv4, "_call", lambda index, fn, *args: setattr(rec, "args", (fn, args)))
+
+
+@pytest.mark.parametrize("given,passed", [(0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+                                          (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 70, 2 ** 31 - 1), (-1, -1), (-2 ** 32 + 5, -1)])
+def test_windows_past_32_bits(cpu_ok, monkeypatch, given, passed):
+    """A window longer than any cache hides nothing; it is not taken modulo 2^32."""
+    r = Recorder(monkeypatch)
+    w.kv4_attention(f16(3, 4, 64), cache(), i32(3, 2), i32(3), window=given)
+    fn, args = r.args
+    at = w._lib._SIGNATURES[fn]
+    assert len(args) + 1 == len(at) and ctypes.c_int32(args[12]).value == args[12] == passed
+
+
+@pytest.mark.parametrize("given,passed", [(2, 2), (50, 3), (2 ** 32 + 1, 3), (2 ** 70, 3), (-2 ** 32 + 1, -1)])
+def test_max_q_past_32_bits(cpu_ok, monkeypatch, given, passed):
+    r = Recorder(monkeypatch)
+    w.kv4_attention(f16(3, 4, 64), cache(), i32(1, 2), i32(1), q_starts=i32(2), max_q=given)
+    assert r.args[1][10] == passed
+    size = w.kv4_attention_workspace_size
+    assert size(4, 2, 64, 3, 1, given) == size(4, 2, 64, 3, 1, passed)

@@ -41,6 +41,14 @@ def _call(index, fn, *args):
         check(status)
 
 
+_LARGEST = 2 ** 31 - 1
+
+
+def _at_most(n, most):
+    """n cut to [-1, most]: ctypes would take a longer number modulo 2^32."""
+    return -1 if n < 0 else n if n < most else most
+
+
 def _rows(t, name, index=None, heads=None, head_dim=None):
     """fp16 [T, heads, head_dim] whose heads are contiguous in a token; tokens may be strided.
     Returns (T, elements from one token to the next)."""
@@ -205,7 +213,7 @@ def kv4_read(cache, slots, k=None, v=None):
 def kv4_attention_workspace_size(q_heads: int, kv_heads: int, head_dim: int, tokens: int,
                                  sequences: int, max_q: int = 1) -> int:
     return int(lib().kv4_attention_workspace_size(q_heads, kv_heads, head_dim, tokens, sequences,
-                                                  max_q))
+                                                  _at_most(max_q, tokens)))
 
 
 def kv4_attention_workspace(cache, q_heads: int, tokens: int, sequences: int, max_q: int = 1):
@@ -247,6 +255,7 @@ def kv4_attention(q, cache, page_table, kv_lens, q_starts=None, max_q=None, caus
         starts = None
     if max_q is None:
         max_q = 1 if q_starts is None else T
+    max_q = _at_most(max_q, T)
     L = lib()
     if workspace is None:
         need = L.kv4_attention_workspace_size(heads, cache.kv_heads, D, T, B, max_q)
@@ -263,6 +272,6 @@ def kv4_attention(q, cache, page_table, kv_lens, q_starts=None, max_q=None, caus
     elif return_lse:
         lse = torch.empty((T, heads), dtype=torch.float32, device=cache.device)
     _call(index, L.kv4_attention, q.data_ptr(), stride, T, heads, cache._ref, page_table.data_ptr(), max_pages,
-          kv_lens.data_ptr(), starts, B, max_q, causal, window, D ** -0.5 if scale is None else scale,
+          kv_lens.data_ptr(), starts, B, max_q, causal, _at_most(window, _LARGEST), D ** -0.5 if scale is None else scale,
           out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return (out, lse) if return_lse else out
