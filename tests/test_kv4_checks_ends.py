@@ -51,3 +51,21 @@ def test_max_q_past_32_bits(cpu_ok, monkeypatch, given, passed):
     assert r.args[1][10] == passed
     size = w.kv4_attention_workspace_size
     assert size(4, 2, 64, 3, 1, given) == size(4, 2, 64, 3, 1, passed)
+
+
+@pytest.mark.parametrize("bad", [None, [[0, 1]], 3])
+def test_what_is_no_tensor_is_named(cpu_ok, bad):
+    import torch
+    c = cache()
+    calls = [lambda: w.rotary_axes(bad, i64(1, 2), torch.ones(32)), lambda: w.rotary_axes(f16(2, 3, 64), bad, torch.ones(32)),
+             lambda: w.rotary_axes(f16(2, 3, 64), i64(1, 2), bad), lambda: w.kv4_write(f16(3, 2, 64), f16(3, 2, 64), bad, c),
+             lambda: w.kv4_write(bad, f16(3, 2, 64), i64(3), c), lambda: w.kv4_read(c, bad),
+             lambda: w.kv4_attention(f16(3, 4, 64), c, bad, i32(3)), lambda: w.kv4_attention(f16(3, 4, 64), c, i32(3, 2), bad),
+             lambda: w.KV4Cache(bad, c.k_scale, c.v, c.v_scale), lambda: w.KV4Cache(c.k, bad, c.v, c.v_scale)]
+    for call in calls:
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            call()
+    if bad is not None:
+        for kw in (dict(q_starts=bad), dict(workspace=bad), dict(out=bad), dict(lse=bad)):
+            with pytest.raises(TypeError, match="must be a torch.Tensor"):
+                w.kv4_attention(f16(3, 4, 64), c, i32(3, 2), i32(3), **kw)

@@ -49,11 +49,16 @@ def _at_most(n, most):
     return -1 if n < 0 else n if n < most else most
 
 
+def _tensor(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
+
+
 def _rows(t, name, index=None, heads=None, head_dim=None):
     """fp16 [T, heads, head_dim] whose heads are contiguous in a token; tokens may be strided.
     Returns (T, elements from one token to the next)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    _tensor(t, name)
     if index is None:
         if t.device.type != ops._DEVICE_TYPE:
             raise ValueError(f"{name} must be a device tensor, got {t.device}")
@@ -74,8 +79,7 @@ def _rows(t, name, index=None, heads=None, head_dim=None):
 
 def _flat(t, dtype, shape, name, index):
     """t must be a contiguous `dtype` tensor of exactly `shape` on device `index`."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    _tensor(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
@@ -160,14 +164,15 @@ def rotary_axes(x, positions, inv_freq, sections=None, interleaved: bool = False
     T, stride = _rows(x, "x")
     _, heads, D = x.shape
     index = x.get_device()
-    half = inv_freq.numel()
+    half = _tensor(inv_freq, "inv_freq").numel()
     _flat(inv_freq, torch.float32, (half,), "inv_freq", index)
     if half == 0 or half % 8 or 2 * half > D:
         raise ValueError(f"inv_freq must have rotary_dim / 2 values, a multiple of 8 up to {D // 2}, "
                          f"got {half}")
     counts = _sections((half,) if sections is None else tuple(sections), half)
     axes = len(counts)
-    _flat(positions, torch.int64, (T,) if positions.dim() == 1 and axes == 1 else (axes, T), "positions", index)
+    flat = _tensor(positions, "positions").dim() == 1 and axes == 1
+    _flat(positions, torch.int64, (T,) if flat else (axes, T), "positions", index)
     if out is None:
         out = torch.empty((T, heads, D), dtype=torch.float16, device=x.device)
         out_stride = heads * D
@@ -195,7 +200,7 @@ def kv4_write(k, v, slots, cache):
 def kv4_read(cache, slots, k=None, v=None):
     """The keys and values of T slots (int64 [T]) as fp16 [T, kv_heads, head_dim] each."""
     index = _cache(cache)._index
-    T = slots.numel()
+    T = _tensor(slots, "slots").numel()
     _flat(slots, torch.int64, (T,), "slots", index)
     shape = (T, cache.kv_heads, cache.head_dim)
     if k is None:
@@ -241,7 +246,7 @@ def kv4_attention(q, cache, page_table, kv_lens, q_starts=None, max_q=None, caus
     if D != cache.head_dim or heads == 0 or heads % cache.kv_heads:
         raise ValueError(f"q must have head_dim {cache.head_dim} and a multiple of {cache.kv_heads} "
                          f"heads, got shape {tuple(q.shape)}")
-    if page_table.dim() != 2:
+    if _tensor(page_table, "page_table").dim() != 2:
         raise ValueError(f"page_table must have 2 dims, got shape {tuple(page_table.shape)}")
     B, max_pages = page_table.shape
     _flat(page_table, torch.int32, (B, max_pages), "page_table", index)
@@ -261,7 +266,7 @@ def kv4_attention(q, cache, page_table, kv_lens, q_starts=None, max_q=None, caus
         need = L.kv4_attention_workspace_size(heads, cache.kv_heads, D, T, B, max_q)
         workspace = torch.empty((need,), dtype=torch.uint8, device=cache.device)
     else:
-        _flat(workspace, torch.uint8, (workspace.numel(),), "workspace", index)     # its size: by the library
+        _flat(workspace, torch.uint8, (_tensor(workspace, "workspace").numel(),), "workspace", index)     # its size: by the library
     shape = (T, heads, D)
     if out is None:
         out = torch.empty(shape, dtype=torch.float16, device=cache.device)
