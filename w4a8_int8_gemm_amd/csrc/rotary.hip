@@ -30,6 +30,7 @@ __device__ __forceinline__ int axis_of(const Sections &s, int i)
 }
 
 constexpr int kMaxHalf = 512;
+constexpr int64_t kGridRow = 1 << 22;       // tokens along x: a dimension of a grid has under 2^32 threads
 
 __global__ __launch_bounds__(256) void rotary_kernel(const uint16_t *x, int64_t x_stride,
                                                      const int64_t *__restrict__ pos,
@@ -38,7 +39,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(const uint16_t *x, int64_t 
                                                      uint16_t *out, int64_t out_stride)
 {
     __shared__ float cs[kMaxHalf], sn[kMaxHalf];
-    const int64_t t = blockIdx.x;
+    const int64_t t = blockIdx.y * kGridRow + blockIdx.x;
+    if (t >= T)
+        return;
     const int half = R / 2;
     for (int i = threadIdx.x; i < half; i += 256) {
         const double turns = (double)pos[axis_of(sec, i) * T + t] * (double)inv_freq[i] *
@@ -88,7 +91,8 @@ void launch_rotary(const uint16_t *x, int64_t x_stride, const int64_t *pos, cons
     for (int a = 0; a < 3; ++a)
         s.n[a] = a < axes ? sections[a] : 0;
     s.interleaved = interleaved ? 1 : 0;
-    hipLaunchKernelGGL(rotary_kernel, dim3((unsigned)T), dim3(256), 0, st, x, x_stride, pos,
+    const dim3 grid((unsigned)(T < kGridRow ? T : kGridRow), (unsigned)((T + kGridRow - 1) / kGridRow));
+    hipLaunchKernelGGL(rotary_kernel, grid, dim3(256), 0, st, x, x_stride, pos,
                        inv_freq, T, heads, D, R, s, out, out_stride);
 }
 
