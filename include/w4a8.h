@@ -392,7 +392,8 @@ size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t h
  * that is not finite gets NaN in the elements of that group.  workspace: device buffer of
  * kv4_attention_workspace_size() bytes, 256-byte aligned, which needs no
  * initial content; calls that overlap need workspaces of their own.  At most
- * 2^30 tokens a sequence, 2^20 sequences, T * q_heads < 2^31, 0 < scale <= 2^127. */
+ * 2^30 tokens a sequence, 2^20 sequences (about 2^24 with their kv heads),
+ * T * q_heads < 2^31, 0 < scale <= 2^127. */
 w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int32_t q_heads,
                             const kv4_cache_t *cache, const int32_t *page_table,
                             int32_t max_pages, const int32_t *kv_lens, const int32_t *q_starts,

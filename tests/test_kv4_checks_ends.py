@@ -6,7 +6,7 @@ import pytest
 pytest.importorskip("torch")
 
 import w4a8_int8_gemm_amd as w  # noqa: E402
-from tests.test_kv4_checks import MIS, S, attention, cache, cpu_ok, f16, i32, i64  # noqa: E402,F401
+from tests.test_kv4_checks import MIS, S, attention, cache, cpu_ok, f16, i32, i64, struct  # noqa: E402,F401
 
 
 @pytest.mark.parametrize("scale", [2.0 ** 127 * 1.01, 3e38, 3.4e38])
@@ -69,3 +69,15 @@ def test_what_is_no_tensor_is_named(cpu_ok, bad):
         for kw in (dict(q_starts=bad), dict(workspace=bad), dict(out=bad), dict(lse=bad)):
             with pytest.raises(TypeError, match="must be a torch.Tensor"):
                 w.kv4_attention(f16(3, 4, 64), c, i32(3, 2), i32(3), **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(B=1 << 20, T=1 << 20, starts=None, max_q=1, heads=16), dict(B=1 << 20, T=1 << 20, heads=32),
+                                dict(B=1 << 20, T=1 << 20, max_q=1, heads=16 * 33)])
+def test_more_workgroups_than_a_launch_holds(kw):
+    """2^24 workgroups of 256 threads would wrap at 2^32 threads without an error."""
+    heads = kw["heads"]
+    c = struct(kv_heads=16)
+    assert attention(cache=c, stride=heads * 64, **kw) == S.ERR_INVALID_ARG
+    assert b"workgroups" in w.lib().w4a8_last_error()
+    kw = dict(kw, B=1 << 16, T=1 << 16, max_q=1)
+    assert attention(cache=c, stride=heads * 64, ws_bytes=0, **kw) == S.ERR_WORKSPACE    # taken; refused later

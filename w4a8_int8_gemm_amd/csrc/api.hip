@@ -931,6 +931,10 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
     a.max_q = (int)(max_q < T ? max_q : T);
     a.causal = causal != 0; a.window = window; a.scale = scale;
     a.out = out; a.lse = lse; a.workspace = workspace; a.tag = next_tag();
+    const Kv4Cache kc = make_cache(cache);
+    if (!kv4_attention_fits(kc, a))
+        return fail(W4A8_ERR_INVALID_ARG, "%s: sequences=%lld with %d kv heads take more workgroups "
+                    "than a launch holds", fn, (long long)sequences, (int)cache->kv_heads);
     const size_t need = kv4_attention_workspace_size(q_heads, cache->kv_heads, cache->head_dim, T,
                                                      sequences, max_q);
     if (need > 0 && (!workspace || workspace_bytes < need ||
@@ -940,7 +944,7 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
     st = check_device(&a.num_cu);
     if (st != W4A8_OK)
         return st;
-    launch_kv4_attention(make_cache(cache), a, (hipStream_t)stream);
+    launch_kv4_attention(kc, a, (hipStream_t)stream);
     return check_launch(fn);
 }
 

@@ -54,6 +54,9 @@ void launch_kv4_read(const Kv4Cache &c, const int64_t *slots, int64_t T, uint16_
                      hipStream_t st);
 
 size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int B, int max_q);
+// Whether the call's workgroups (of 256 threads) stay under the 2^32 threads of a launch, past which it
+// would wrap without an error.
+bool kv4_attention_fits(const Kv4Cache &c, const Kv4AttnArgs &a);
 void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st);
 
 // Sequences of at most this many query rows a kv head (queries x query heads):

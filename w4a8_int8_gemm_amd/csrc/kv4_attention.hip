@@ -36,19 +36,41 @@ size_t kv4_attention_workspace(int q_heads, int kv_heads, int D, int64_t T, int 
     return bytes;
 }
 
-void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st)
+namespace {
+
+struct Launches {
+    bool few, many;
+};
+Launches launches_of(const Kv4AttnArgs &a)
 {
-    const bool many = (int64_t)a.group * a.max_q > kDecodeRows;
+    Launches l;
+    l.many = (int64_t)a.group * a.max_q > kDecodeRows;
     // Where one query is too many rows for the kernel for few, or all sequences
     // have max_q queries (they do if T = B max_q and q_starts covers all rows),
     // the other kernel takes them all: one launch instead of two.  It is right
     // for every sequence, so that ranges which cover fewer rows cost time only,
     // and the weights' second part.
-    const bool few = a.group <= kDecodeRows && !(many && a.T == (int64_t)a.B * a.max_q);
-    if (few)
+    l.few = a.group <= kDecodeRows && !(l.many && a.T == (int64_t)a.B * a.max_q);
+    return l;
+}
+
+}  // namespace
+
+bool kv4_attention_fits(const Kv4Cache &c, const Kv4AttnArgs &a)
+{
+    const Launches l = launches_of(a);
+    const int64_t most = (int64_t)a.max_pages << c.shift, limit = (int64_t(1) << 24) - 1;
+    return (!l.few || kv4_decode_grid(a.B, c.heads, most) <= limit) &&
+           (!l.many || kv4_prefill_tiles(a.T, a.B, a.group, c.heads, most).grid <= limit);
+}
+
+void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st)
+{
+    const Launches l = launches_of(a);
+    if (l.few)
         launch_kv4_decode(c, a, decode_rows(a.group, a.max_q), st);
-    if (many)
-        launch_kv4_prefill(c, a, few ? kDecodeRows : 0,
+    if (l.many)
+        launch_kv4_prefill(c, a, l.few ? kDecodeRows : 0,
                            static_cast<char *>(a.workspace) +
                                decode_bytes(a.group * c.heads, c.heads, c.D, a.T, a.B, a.max_q), st);
 }
