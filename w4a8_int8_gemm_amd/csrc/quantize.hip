@@ -144,6 +144,14 @@ void launch_token(const uint16_t *x, int8_t *q, float *s, int64_t rows, int K, f
 void launch_quantize_rows(const uint16_t *x, int64_t rows, int K, int gs, float qmax, void *q,
                           float *scale, bool int4, hipStream_t st)
 {
+    // four rows a workgroup of 256 threads: a launch of 2^26 rows would wrap at 2^32 threads
+    constexpr int64_t kRowsALaunch = 1 << 25;
+    for (; rows > kRowsALaunch; rows -= kRowsALaunch) {
+        launch_quantize_rows(x, kRowsALaunch, K, gs, qmax, q, scale, int4, st);
+        x += kRowsALaunch * K;
+        q = static_cast<uint8_t *>(q) + kRowsALaunch * K / (int4 ? 2 : 1);
+        scale += kRowsALaunch * (gs ? K / gs : 1);
+    }
     const unsigned blocks = (unsigned)((rows + 3) / 4);
     if (gs == 0) {
         int8_t *q8 = static_cast<int8_t *>(q);
