@@ -1,5 +1,6 @@
 """Arguments of the attention block at the ends of their ranges (no GPU needed)."""
 import ctypes
+import subprocess
 
 import pytest
 
@@ -81,3 +82,9 @@ def test_more_workgroups_than_a_launch_holds(kw):
     assert b"workgroups" in w.lib().w4a8_last_error()
     kw = dict(kw, B=1 << 16, T=1 << 16, max_q=1)
     assert attention(cache=c, stride=heads * 64, ws_bytes=0, **kw) == S.ERR_WORKSPACE    # taken; refused later
+
+
+def test_no_entry_point_can_throw_for_want_of_random_numbers():
+    """std::random_device throws where its source cannot be read, through a C entry point."""
+    out = subprocess.run(["nm", "-D", "--undefined-only", w.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    assert "random_device" not in out and "__cxa_throw" not in out

@@ -4,8 +4,10 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <time.h>
+#include <unistd.h>
+
 #include <atomic>
-#include <random>
 
 #include "../../include/w4a8.h"
 #include "kernels.hpp"
@@ -446,11 +448,21 @@ Kv4Cache make_cache(const kv4_cache_t *c)
 }
 
 // A tag per call of kv4_attention for the counters in its workspace: 48 bits
-// over a 16-bit count, other than those of the calls before and, by a random
-// start, of other processes'.
+// over a 16-bit count, other than those of the calls before and, by a start
+// from the clock, the process and where it lies, of other processes'.  (No
+// std::random_device: it may throw, and this is behind a C entry point.)
+uint64_t first_tag()
+{
+    struct timespec now = {0, 0};
+    clock_gettime(CLOCK_REALTIME, &now);
+    const uint64_t x = ((uint64_t)now.tv_sec * 1000000000u + (uint64_t)now.tv_nsec) ^ ((uint64_t)getpid() << 32) ^
+                       (uint64_t)reinterpret_cast<uintptr_t>(&now);
+    return (x * 0x9e3779b97f4a7c15u) >> 17;              // 2^64 over the golden ratio: every bit reaches the upper ones
+}
+
 uint64_t next_tag()
 {
-    static std::atomic<uint64_t> tag{std::random_device{}() ^ ((uint64_t)std::random_device{}() << 20)};
+    static std::atomic<uint64_t> tag{first_tag()};
     return (tag.fetch_add(1, std::memory_order_relaxed) | (uint64_t(1) << 47)) << 16;
 }
 
