@@ -262,3 +262,31 @@ def test_without_max_q_every_row_is_computed(m):
     if max(m) * 4 > 32:
         with pytest.raises(w.W4A8Error, match="workspace"):
             w.kv4_attention(*args, q_starts=dev(c.starts), workspace=ws)
+
+
+@pytest.mark.parametrize("m", [[1, 3], [40, 60]])
+@pytest.mark.parametrize("name", ["k", "v"])
+@pytest.mark.parametrize("D,G", [(64, 64), (128, 32), (256, 128)])
+def test_negative_scales(m, name, D, G):
+    """A value is code * scale, whatever the sign: some keys' scales in some groups are turned."""
+    c = Case([77, 130], m, 4, 2, D, G, 16, seed=34)
+    r = np.random.default_rng(5)
+    for b, n in enumerate(c.kv):
+        for j in range(0, n, 3):
+            page, at, g = int(c.table[b, j // 16]), j % 16, int(r.integers(0, D // G))
+            getattr(c.c, name + "_scale")[page, :, at, g] *= -1
+            getattr(c, name)[b][j, :, g * G:(g + 1) * G] *= -1
+    c.check()
+
+
+@pytest.mark.parametrize("m", [1, 40])
+@pytest.mark.parametrize("bits", [0x7fc00000, 0xffffffff, 0xffc00001])
+def test_a_key_scale_that_is_not_a_number_makes_the_rows_that_see_it_not_a_number(m, bits):
+    c = Case([77], [m], 4, 2, 128, 64, 16, seed=35)
+    good, _ = c.run()
+    page, at = int(c.table[0, 70 // 16]), 70 % 16
+    c.c.k_scale.view(torch.int32)[page, 1, at, 0] = bits - 2 ** 32 if bits >= 2 ** 31 else bits
+    out, lse = c.run()
+    sees = torch.arange(m, device="cuda") + 77 - m >= 70
+    assert bool(out[sees][:, 2:].isnan().all()) and bool(sees.any())
+    assert torch.equal(out[:, :2], good[:, :2]) and torch.equal(out[~sees], good[~sees])

@@ -28,6 +28,9 @@ namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
+constexpr uint32_t kNotThere = 0xffffffffu;             // bits of a value that is no number, one of many
+__device__ __forceinline__ bool not_there(float k_scale) { return __float_as_uint(k_scale) == kNotThere; }
+
 constexpr int kRows = kTileRows, kKeys = 64, kThreads = 2 * kRows;
 
 template <int D, int NG>
@@ -198,7 +201,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : D < 256 ? 2 : 1) void kv4_p
             }
         }
     };
-    // codes to LDS; a hidden key's K scale is -1 and its V scale 0
+    // codes to LDS; a key that is not there has kNotThere for its first K scale, which
+    // a key's own cannot be, and the V scale 0
     const auto produce = [&](auto bc) {
         constexpr int buf = decltype(bc)::value;
         if (for_v) {
@@ -226,8 +230,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : D < 256 ? 2 : 1) void kv4_p
                     kt[buf][key][4 * i + b4] = __builtin_bit_cast(u32x4, codes8(code[N32 * x + i]));
                 if (b4 == 0) {
 #pragma unroll
-                    for (int g = 0; g < NG; ++g)
-                        ksc[buf][g][key] = there[x] ? scale[x][g] : -1.0f;
+                    for (int g = 1; g < NG; ++g)
+                        ksc[buf][g][key] = scale[x][g];
+                    const float own = not_there(scale[x][0]) ? NAN : scale[x][0];
+                    ksc[buf][0][key] = there[x] ? own : __uint_as_float(kNotThere);
                 }
             }
         }
@@ -277,7 +283,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : D < 256 ? 2 : 1) void kv4_p
             constexpr int e = decltype(ec)::value;
             const int key = t0 + e / 4 * 8 + 4 * h + e % 4;
             const float there = row_lane<e>(ks0);        // by all lanes: no lane may be off when it is read
-            s[e] = ((key >= lo) & (key < hi) & (there >= 0.0f)) ? s[e] : -INFINITY;
+            s[e] = ((key >= lo) & (key < hi) & !not_there(there)) ? s[e] : -INFINITY;
         });
     };
     // The largest of a lane's scores.
@@ -355,7 +361,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : D < 256 ? 2 : 1) void kv4_p
                 vs[x][g] = vsc[buf][g][32 * x + lane_key];
                 big = max(big, __float_as_uint(vs[x][g]));   // a sign counts as not finite: it is looked at
             }
-        const bool some_hidden = t0 < lo_all || t0 + kKeys > hi_all || __ballot(fminf(ks[0][0], ks[1][0]) < 0.0f);
+        const bool some_hidden = t0 < lo_all || t0 + kKeys > hi_all || __ballot(not_there(ks[0][0]) || not_there(ks[1][0]));
         if (__ballot(big >= scale_cap)) {                // rare: values larger than any before
             big = max_rows_u32(group_max_u32<16>(big));
             if (some_hidden || big >= kNotFinite) {
