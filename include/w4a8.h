@@ -389,7 +389,8 @@ size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t h
  * [0, max_pages * page_size], tokens of pages outside [0, pages) are not seen,
  * queries outside [0, T) are not computed; nothing that a row does not see has
  * any influence on it, whatever its bytes are.  A row that sees a value scale
- * that is not finite gets NaN in the elements of that group.  workspace: device buffer of
+ * that is not finite gets NaN in the elements of that group, one with a score
+ * that is NaN in all of them and in lse.  workspace: device buffer of
  * kv4_attention_workspace_size() bytes, 256-byte aligned, which needs no
  * initial content; calls that overlap need workspaces of their own.  At most
  * 2^30 tokens a sequence, 2^20 sequences (about 2^24 with their kv heads),

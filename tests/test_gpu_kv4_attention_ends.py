@@ -290,3 +290,25 @@ def test_a_key_scale_that_is_not_a_number_makes_the_rows_that_see_it_not_a_numbe
     sees = torch.arange(m, device="cuda") + 77 - m >= 70
     assert bool(out[sees][:, 2:].isnan().all()) and bool(sees.any())
     assert torch.equal(out[:, :2], good[:, :2]) and torch.equal(out[~sees], good[~sees])
+
+
+@pytest.mark.parametrize("kv,m", [([77], [1]), ([77], [40]), ([3000], [2]), ([3000], [150])])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_the_log_of_a_row_that_is_not_a_number(kv, m, bad):
+    """Not the log of a row that sees nothing; also where its keys are cut into parts."""
+    c = Case(kv, m, 4, 2, 128, 64, 16, seed=36)
+    good, logs = c.run()
+    last = sum(m) - 1
+    c.q[last, 1, 5] = bad
+    out, lse = c.run()
+    assert bool(lse[last, 1].isnan()) and bool(out[last, 1].isnan().all())
+    keep = torch.ones(lse.shape, dtype=torch.bool)
+    keep[last, 1] = False
+    assert torch.equal(lse[keep.cuda()], logs[keep.cuda()]) and torch.equal(out[keep.cuda()], good[keep.cuda()])
+    page, at = int(c.table[0, 50 // 16]), 50 % 16                # in the first of the parts
+    c = Case(kv, m, 4, 2, 128, 64, 16, seed=36)
+    c.c.k_scale[page, 0, at] = float("nan")
+    out, lse = c.run()
+    sees = torch.arange(m[0], device="cuda") + kv[0] - m[0] >= 50
+    assert bool(lse[sees][:, :2].isnan().all()) and bool(out[sees][:, :2].isnan().all())
+    assert torch.equal(lse[:, 2:], logs[:, 2:]) and torch.equal(lse[~sees], logs[~sees])

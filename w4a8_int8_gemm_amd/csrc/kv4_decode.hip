@@ -107,18 +107,19 @@ __device__ __forceinline__ void load_step(Step<P, D / 32, NG> &s, const Kv4Cache
     }
 }
 
-// A row's output and log of the softmax sum from its joined part.
+// A row's output and log of the softmax sum from its joined part.  Here and
+// below a sum of 0 is a row that sees nothing; one that is no number stays so.
 template <int D>
 __device__ __forceinline__ void store_row(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq &seq, int head, int row,
                                           int d, float4 sum, float ref, float l)
 {
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     const int i = query_of(row, w.over_group, a.group);
     const int64_t at = (int64_t)(seq.q0 + i) * a.q_heads + head * a.group + (row - i * a.group);
     *reinterpret_cast<uint2 *>(a.out + at * D + d) =
         make_uint2(pack_h2(sum.x * inv, sum.y * inv), pack_h2(sum.z * inv, sum.w * inv));
     if (a.lse && d == 0)
-        a.lse[at] = l > 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+        a.lse[at] = l != 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 // Joins the parts in `parts` slots from slot p0 on: `rows` rows of their
@@ -156,13 +157,13 @@ __device__ void join_parts(const Partial &w, const Kv4AttnArgs &a, const Kv4Seq 
                 float top = R;
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i)
-                    top = fmaxf(top, rl[i].y > 0.0f ? rl[i].x : -INFINITY);
+                    top = fmaxf(top, rl[i].y != 0.0f ? rl[i].x : -INFINITY);
                 const float keep = R == -INFINITY ? 0.0f : exp2_hw(R - top);
                 L *= keep;
                 sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
-                    const float f = rl[i].y > 0.0f ? exp2_hw(rl[i].x - top) : 0.0f;
+                    const float f = rl[i].y != 0.0f ? exp2_hw(rl[i].x - top) : 0.0f;
                     L = fmaf(rl[i].y, f, L);
                     sum.x = fmaf(u[i].x, f, sum.x), sum.y = fmaf(u[i].y, f, sum.y);
                     sum.z = fmaf(v[i].x, f, sum.z), sum.w = fmaf(v[i].y, f, sum.w);
@@ -534,7 +535,7 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
     for (int t = 0; t < RT; ++t) {
         l[t] = sum_rows(l[t]);
         if (lane < 16) {
-            refs[wave][16 * t + r] = l[t] > 0.0f ? ref[t] : -INFINITY;
+            refs[wave][16 * t + r] = l[t] != 0.0f ? ref[t] : -INFINITY;
             ls[wave][16 * t + r] = l[t];
         }
     }
@@ -549,7 +550,7 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
 #pragma unroll
             for (int x = 0; x < kWaves; ++x)
                 R = fmaxf(R, refs[x][16 * t + r]);
-            const float keep = l[t] > 0.0f ? exp2_hw(ref[t] - R) : 0.0f;
+            const float keep = l[t] != 0.0f ? exp2_hw(ref[t] - R) : 0.0f;
 #pragma unroll
             for (int g = 0; g < N32; ++g) {
                 const float f = spoilt[t] >> (g / PER) & 1 ? NAN : keep;
@@ -570,7 +571,7 @@ __global__ __launch_bounds__(kThreads, RT * D == 512 ? 1 : 2) void kv4_decode_ke
                 RR = fmaxf(RR, refs[y][row]);
 #pragma unroll
             for (int y = 0; y < kWaves; ++y)
-                L += ls[y][row] > 0.0f ? ls[y][row] * exp2_hw(refs[y][row] - RR) : 0.0f;
+                L += ls[y][row] != 0.0f ? ls[y][row] * exp2_hw(refs[y][row] - RR) : 0.0f;
             float4 sum = *reinterpret_cast<const float4 *>(&os[0][rr][d]);
 #pragma unroll
             for (int y = 1; y < kWaves; ++y) {

@@ -508,7 +508,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : D < 256 ? 2 : 1) void kv4_p
             for (int e = 0; e < 16; e += 2)
                 store_shared(mine + at_o + g * 1024 + e * 64, o[g][e], o[g][e + 1]);
         if (h == 0)
-            store_shared(mine + at_l, l > 0.0f ? ref : -INFINITY, l);
+            store_shared(mine + at_l, l != 0.0f ? ref : -INFINITY, l);
         __builtin_amdgcn_s_waitcnt(0);                   // this wave's stores are complete
         __syncthreads();
         if (threadIdx.x == 0)
@@ -535,9 +535,9 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : D < 256 ? 2 : 1) void kv4_p
             for (int y = 0; y < AT_ONCE; ++y) {
                 if (p + y >= parts)
                     break;
-                const float nref = fmaxf(ref, rl[y].y > 0.0f ? rl[y].x : -INFINITY);
+                const float nref = fmaxf(ref, rl[y].y != 0.0f ? rl[y].x : -INFINITY);
                 const float f0 = ref == -INFINITY ? 0.0f : exp2_hw(ref - nref);
-                const float f1 = rl[y].y > 0.0f ? exp2_hw(rl[y].x - nref) : 0.0f;
+                const float f1 = rl[y].y != 0.0f ? exp2_hw(rl[y].x - nref) : 0.0f;
                 l = l * f0 + rl[y].y * f1;
                 ref = nref;
 #pragma unroll
@@ -554,7 +554,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : D < 256 ? 2 : 1) void kv4_p
 
     // ---- results: the lane's row, dims 32 g + 8 i + 4 h ..+3
     if (row < rows) {
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
         const int64_t at = (int64_t)(seq.q0 + qi) * a.q_heads + head * group + hh;
 #pragma unroll
         for (int g = 0; g < N32; ++g)
@@ -563,7 +563,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : D < 256 ? 2 : 1) void kv4_p
                 *reinterpret_cast<uint2 *>(a.out + at * D + 32 * g + 8 * i + 4 * h) =
                     make_uint2(pack_h2(o[g][4 * i] * inv, o[g][4 * i + 1] * inv), pack_h2(o[g][4 * i + 2] * inv, o[g][4 * i + 3] * inv));
         if (a.lse && h == 0)
-            a.lse[at] = l > 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+            a.lse[at] = l != 0.0f ? (ref + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
     }
 }
 
