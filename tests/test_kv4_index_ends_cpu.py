@@ -6,6 +6,8 @@ import subprocess
 
 import pytest
 
+from tests.test_kv4_index_cpu import L as rules  # noqa: F401
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 TOP = 2 ** 31 - 1
 
@@ -81,3 +83,13 @@ def test_queries_past_max_q_do_not_move_the_others(L):
                 assert 32 * out[4] <= lo and hi <= 32 * (out[4] + out[5])
     L.cut_and_see(0, TOP, 5, TOP, 1, 64, 0, 1, TOP, out)
     assert tuple(out[:4]) == (0, 1, 0, 0)                       # far before the first key
+
+
+def test_parts_are_few_more_than_pairs(rules):
+    """What the workspace holds slots for, whatever the lengths are."""
+    more = rules.parts_more()
+    for B, heads, most in itertools.product([1, 3, 200], [1, 8, 40], [0, 1000, 5000, 1 << 20, 1 << 30]):
+        steps = [max(1, -(-most // 32))] * B
+        limit = rules.part_limit(heads * sum(steps), max(steps), 32)
+        assert heads * sum(-(-n // limit) for n in steps) <= B * heads + more
+        assert rules.decode_grid(B, heads, most) <= B * heads + more

@@ -953,7 +953,7 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
                      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
         return fail(W4A8_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) needed, got "
                     "%zu", fn, need, workspace_bytes);
-    st = check_device(&a.num_cu);
+    st = check_device();
     if (st != W4A8_OK)
         return st;
     launch_kv4_attention(kc, a, (hipStream_t)stream);

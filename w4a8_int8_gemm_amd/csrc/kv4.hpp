@@ -41,7 +41,6 @@ struct Kv4AttnArgs {
     float *lse;                 // [T, q_heads] or null
     void *workspace;
     uint64_t tag;               // of this call among the counters in the workspace
-    int num_cu;
 };
 
 void launch_rotary(const uint16_t *x, int64_t x_stride, const int64_t *pos, const float *inv_freq,

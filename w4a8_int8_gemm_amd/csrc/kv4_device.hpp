@@ -266,7 +266,7 @@ struct Partial {
     uint64_t *counters;         // [items][kCounterStride]
     int grid;
     int row_limit;              // rows a kv head: the most for the kernel of few rows, one less for the other
-    uint32_t over_group;        // division of a row by the group, see row_of()
+    uint32_t over_group;        // division of a row by the group, see query_of()
 };
 
 // Row = query * group + head of the group.  The quotient of rows < 2^16 by

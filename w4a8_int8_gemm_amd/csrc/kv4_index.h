@@ -141,7 +141,7 @@ KV4_HD Kv4TilePart kv4_tile_part(const Kv4Seq &s, bool causal, int window, int k
     return t;
 }
 
-// Where a page's 16-token piece lies, and whether the table's entry names a page at all.
+// Whether the table's entry names a page at all.
 KV4_HD bool kv4_page_ok(int page, int64_t pages) { return page >= 0 && page < pages; }
 
 }  // namespace w4a8
