@@ -58,7 +58,8 @@ def _tensor(t, name):
 def _rows(t, name, index=None, heads=None, head_dim=None):
     """fp16 [T, heads, head_dim] whose heads are contiguous in a token; tokens may be strided.
     Returns (T, elements from one token to the next)."""
-    _tensor(t, name)
+    if not isinstance(t, torch.Tensor):
+        _tensor(t, name)
     if index is None:
         if t.device.type != ops._DEVICE_TYPE:
             raise ValueError(f"{name} must be a device tensor, got {t.device}")
@@ -79,7 +80,8 @@ def _rows(t, name, index=None, heads=None, head_dim=None):
 
 def _flat(t, dtype, shape, name, index):
     """t must be a contiguous `dtype` tensor of exactly `shape` on device `index`."""
-    _tensor(t, name)
+    if not isinstance(t, torch.Tensor):
+        _tensor(t, name)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
@@ -164,14 +166,17 @@ def rotary_axes(x, positions, inv_freq, sections=None, interleaved: bool = False
     T, stride = _rows(x, "x")
     _, heads, D = x.shape
     index = x.get_device()
-    half = _tensor(inv_freq, "inv_freq").numel()
+    if not isinstance(inv_freq, torch.Tensor) or not isinstance(positions, torch.Tensor):
+        _tensor(inv_freq, "inv_freq")
+        _tensor(positions, "positions")
+    half = inv_freq.numel()
     _flat(inv_freq, torch.float32, (half,), "inv_freq", index)
     if half == 0 or half % 8 or 2 * half > D:
         raise ValueError(f"inv_freq must have rotary_dim / 2 values, a multiple of 8 up to {D // 2}, "
                          f"got {half}")
     counts = _sections((half,) if sections is None else tuple(sections), half)
     axes = len(counts)
-    flat = _tensor(positions, "positions").dim() == 1 and axes == 1
+    flat = positions.dim() == 1 and axes == 1
     _flat(positions, torch.int64, (T,) if flat else (axes, T), "positions", index)
     if out is None:
         out = torch.empty((T, heads, D), dtype=torch.float16, device=x.device)
