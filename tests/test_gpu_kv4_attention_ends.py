@@ -312,3 +312,22 @@ def test_the_log_of_a_row_that_is_not_a_number(kv, m, bad):
     sees = torch.arange(m[0], device="cuda") + kv[0] - m[0] >= 50
     assert bool(lse[sees][:, :2].isnan().all()) and bool(out[sees][:, :2].isnan().all())
     assert torch.equal(lse[:, 2:], logs[:, 2:]) and torch.equal(lse[~sees], logs[~sees])
+
+
+@pytest.mark.parametrize("kv,m,window", [([75, 300], [6, 4], 0), ([75, 300], [50, 140], 0), ([75, 1300], [20, 90], 40),
+                                         ([2300, 1100], [8, 2], 0), ([2300], [200], 700)])
+@pytest.mark.parametrize("gain", [1e-3, 1.0, 1e4])
+def test_earlier_rows_keep_their_bits(kv, m, window, gain):
+    """Whatever the last token's key and value are, the rows before it come out the same to the bit."""
+    c = Case(kv, m, 8, 2, 128, 64, 16, seed=37)
+    good, logs = c.run(window=window)
+    for b, n in enumerate(kv):
+        page, at = int(c.table[b, (n - 1) // 16]), (n - 1) % 16
+        for name in "kv":
+            getattr(c.c, name)[page, :, at] ^= 0x35
+            getattr(c.c, name + "_scale")[page, :, at] *= gain
+    out, lse = c.run(window=window)
+    keep = torch.ones(sum(m), dtype=torch.bool, device="cuda")
+    keep[torch.from_numpy(c.starts[1:] - 1).long().cuda()] = False
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], logs[keep])
+    assert not torch.equal(out[~keep], good[~keep])

@@ -59,8 +59,10 @@ bool kv4_attention_fits(const Kv4Cache &c, const Kv4AttnArgs &a);
 void launch_kv4_attention(const Kv4Cache &c, const Kv4AttnArgs &a, hipStream_t st);
 
 // Sequences of at most this many query rows a kv head (queries x query heads):
-// two blocks of 16.  Four blocks were no faster than the other kernel's tile of
-// 128 (11 sequences of up to 13 queries x 8 heads: 25 us with four, 15.5 without).
+// two blocks of 16.  Four blocks against the other kernel's tile of 128: short
+// sequences are faster there (11 of up to 71 tokens, 13 queries x 8 heads: 25 us
+// with four, 15.7 without), long ones a little slower (2 x 14 queries x 4 heads
+// behind 4625 keys: 39 us with four, 43 without).
 constexpr int kDecodeRows = 32;
 // A counter for each (sequence, head), on lines of their own: arrivals on one line queue up.
 constexpr int kCounterStride = 16;

@@ -10,8 +10,8 @@
 // words b n .. b n + n - 1; V's bytes 4 b n .. 4 b n + 4 n - 1, after a
 // transposition of 4 x 4 bytes in registers).  A scale's maximum is taken over
 // a lane's own elements and the four lanes.  Measured at 8 heads of 128: reading
-// 65533 tokens (G = 32, 353 MB) 77 us, 4.6 TB/s; 4516 tokens (G = 64) written
-// in 9.4 us and read in 7.3 us.
+// 65533 tokens (G = 32, 353 MB) 77 us, 4.6 TB/s; 4516 tokens (G = 64, 23.7 MB)
+// written in 9.2 us and read in 7.2 us, half the rate of the long read.
 #include "kv4.hpp"
 
 namespace w4a8 {

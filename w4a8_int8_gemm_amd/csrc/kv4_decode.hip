@@ -4,8 +4,8 @@
 //
 // What bounds it: for long caches reading it, D + 8 D / G bytes for a key and
 // value of one head; for short ones the chain of loads, steps and joins.
-// Measured: one sequence of 131075 keys (151 MB) 39 us, 3.9 TB/s over the whole
-// call; 32 sequences of up to 4516 (81.5 MB) 24 us; one of 517 10 us.  About
+// Measured: one sequence of 131075 keys (151 MB) 39.5 us, 3.8 TB/s over the whole
+// call; 32 sequences of up to 4516 (81.5 MB) 23.4 us; one of 517 9.7 us.  About
 // 60 % of a workgroup's cycles are steps in the first, 40 % in the second.
 //
 // One wavefront takes steps of 32 keys.  S^T =

@@ -4,10 +4,11 @@
 //
 // What bounds it: a wave's own chain of LDS reads, products and softmax, with
 // two waves a SIMD to cover it.  For D = 128, a wave's tile of 64 keys and 32
-// rows takes 32 matrix instructions and 418 vector instructions (scaling,
+// rows takes 32 matrix instructions and 424 vector instructions (scaling,
 // maximum, exponential, sum, rounding, and its share of turning codes into
-// fp16).  Of all cycles the vector unit is busy 57 %, the matrix unit 33 %.
-// Measured: a causal prompt of 4516 tokens, 167 GFLOP, 221 us (756 TFLOP/s).
+// fp16).  Of all cycles the vector unit is busy 57 %, the matrix unit 32 %: the
+// two work almost one after the other.  Measured: a causal prompt of 4516
+// tokens, 167 GFLOP, 222 to 232 us on different boards (720 to 752 TFLOP/s).
 //
 // A workgroup has 128 rows (queries x query heads of one kv head), 32 a wave,
 // and walks over its keys in tiles of 64.  Two of its waves turn the tile's V

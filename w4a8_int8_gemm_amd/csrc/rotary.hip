@@ -5,7 +5,7 @@
 // a far position times a frequency loses the fraction of a turn in fp32
 // (10^6 * 2^-24 = 0.06 rad); reduced to a turn there, cosine and sine in fp32
 // (sincospif of the fraction).  Bound by memory: 2 bytes read and 2 written per
-// element.  4516 tokens of 40 heads of 128, 92.6 MB: 15.7 us; one token: 2.6 us,
+// element.  4516 tokens of 40 heads of 128, 92.6 MB: 15.6 us; one token: 2.5 us,
 // about an empty launch.
 #include "kv4.hpp"
 
