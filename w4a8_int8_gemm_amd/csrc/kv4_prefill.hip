@@ -8,7 +8,7 @@
 // maximum, exponential, sum, rounding, and its share of turning codes into
 // fp16).  Of all cycles the vector unit is busy 57 %, the matrix unit 32 %: the
 // two work almost one after the other.  Measured: a causal prompt of 4516
-// tokens, 167 GFLOP, 222 to 232 us on different boards (720 to 752 TFLOP/s).
+// tokens, 167 GFLOP, 222 to 232 us in different sessions (720 to 752 TFLOP/s).
 //
 // A workgroup has 128 rows (queries x query heads of one kv head), 32 a wave,
 // and walks over its keys in tiles of 64.  Two of its waves turn the tile's V
