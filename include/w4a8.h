@@ -372,7 +372,7 @@ size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t h
  *                q_starts[b + 1]; NULL: one query a sequence (T == sequences).  Rows that no
  *                sequence has are not read, and their outputs not written
  *   max_q        no sequence has more queries than this (rows past it are not computed
- *                and their outputs not written; the others are as they are with a larger max_q)
+ *                and their outputs not written; the others see the keys that they see with a larger max_q)
  * With n = kv_lens[b] and m queries, query i of sequence b stands at position
  * p = n - m + i and sees the keys j < n; with `causal` only j <= p, and with
  * window > 0 (causal only) only j > p - window.  Over the keys seen,
