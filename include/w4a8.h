@@ -73,7 +73,8 @@ typedef enum {
 typedef enum {
     W4A8_MODE_W8A8_PC = 0, /* int8 weights, one scale per output channel */
     W4A8_MODE_W8A8_PG = 1, /* int8 weights and activations, scales per group of gs along K */
-    W4A8_MODE_W4A8 = 2     /* packed int4 weights with per-group scales, per-token activations */
+    W4A8_MODE_W4A8 = 2,    /* packed int4 weights with per-group scales, per-token activations */
+    W4A8_MODE_F8 = 3       /* e4m3 weights in 128 x 128 blocks, e4m3 activations in blocks of 128 */
 } w4a8_mode_t;
 
 /* 1 if the current HIP device is a gfx950 (MI355X-class) GPU, else 0
@@ -189,6 +190,7 @@ size_t linear_workspace_size(w4a8_mode_t mode, int64_t M, int64_t K, int32_t gro
  * What linear accepts does not depend on M: the GEMM's rules.
  * x fp16 [M, K]; w is int8 [N, K] (PC, PG) or packed uint8 [N, K/2] (W4A8);
  * w_scale as the mode's GEMM takes it; group_size is ignored in PC mode.
+ * W4A8_MODE_F8 (group_size ignored): quantize_act_f8 then f8_gemm for every M.
  * workspace: device buffer of at least linear_workspace_size() bytes, 256-byte
  * aligned (may be NULL when that size is 0). */
 w4a8_status_t linear(w4a8_mode_t mode, const w4a8_f16 *x, int64_t M, int64_t K, const void *w,
@@ -401,6 +403,94 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
                             int64_t sequences, int32_t max_q, int32_t causal, int32_t window,
                             float scale, w4a8_f16 *out, float *lse, void *workspace,
                             size_t workspace_bytes, w4a8_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * 8-bit floating point with a scale for each block of 128: the linear layers'
+ * fourth mode (W4A8_MODE_F8), the gated first half of a feed-forward block in
+ * it, and the norm in front of the layers of every mode.  With
+ * KB = ceil(K / 128) and NB = ceil(N / 128), the last blocks short:
+ *   activations  uint8 [M, K] e4m3 codes, fp32 scales [KB, M]: one for 128
+ *                consecutive values of a token, the tokens side by side
+ *   weights      uint8 [N, K] e4m3 codes, fp32 scales [NB, KB]: one for a
+ *                128 x 128 block
+ * e4m3: a sign, 4 exponent and 3 mantissa bits, values up to 448, no infinity,
+ * codes 0x7f and 0xff are NaN.  The rule, for activations and weights alike:
+ *     s = fl32(amax / 448),  code = e4m3(fl32(x / s)) to nearest even;
+ * a block of zeros, or so small that s is below 2^-126, gets s = 0 and zero
+ * codes; one that holds a value that is not finite gets s = NaN and zero
+ * codes, so that its products are NaN and no other block's are.
+ * M <= 2^25; K a multiple of 16 (the quantizers: of 8), K <= 2^22.
+ * Code, weight, input and output buffers 16-byte aligned, scales 4-byte.
+ * ------------------------------------------------------------------------ */
+
+/* x fp16 [M, K] -> xq uint8 [M, K], x_scale fp32 [KB, M].  K % 8 == 0. */
+w4a8_status_t quantize_act_f8(const w4a8_f16 *x, int64_t M, int64_t K, uint8_t *xq, float *x_scale,
+                              w4a8_stream_t stream);
+
+/* w fp16 [N, K] -> wq uint8 [N, K], w_scale fp32 [NB, KB], offline.  K % 8 == 0,
+ * fewer than 2^24 blocks. */
+w4a8_status_t quantize_weight_f8(const w4a8_f16 *w, int64_t N, int64_t K, uint8_t *wq, float *w_scale,
+                                 w4a8_stream_t stream);
+
+/* The residual's addition, the root-mean-square norm and the quantization for
+ * the linear layer behind it, in one pass:
+ *     h = x + residual (x where residual is NULL),
+ *     v = h / sqrt(mean(h^2) + eps) * gain,
+ *     q, scale = v quantized as `mode` takes its activations:
+ *       W8A8_PC, W4A8  int8 [M, K], scale fp32 [M]
+ *       W8A8_PG        int8 [M, K], scale fp32 [M, K / group_size]
+ *       F8             e4m3 [M, K], scale fp32 [KB, M] (the rule above)
+ *     residual_out = fp16(h), where it is not NULL.
+ * x, residual, residual_out fp16 [M, K], gain fp16 [K]; group_size is ignored
+ * outside W8A8_PG.  h, the mean, v and the scales are held in fp32: v is not
+ * rounded to fp16 before it is quantized, and the norm is that of h, not of
+ * fp16(h).  The int8 rule is that of quantize_act, with s below 2^-126 taken
+ * as 0.  A row that holds a value of h that is not finite (or whose squares'
+ * sum is not) gets NaN scales and zero codes, a row of zeros scales of 0.
+ * residual_out may be residual or x itself; no other output may overlap an
+ * input.  K % 8 == 0, K <= 2^22, M <= 2^25, 0 <= eps <= 2^127. */
+w4a8_status_t rmsnorm_quant(w4a8_mode_t mode, const w4a8_f16 *x, const w4a8_f16 *residual,
+                            const w4a8_f16 *gain, float eps, int64_t M, int64_t K, int32_t group_size,
+                            void *q, float *scale, w4a8_f16 *residual_out, w4a8_stream_t stream);
+
+/* Bytes of device workspace f8_gemm() needs for these sizes. */
+size_t f8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/* The product of the F8 mode:
+ *     y[m, n] = fp16( sum_b x_scale[b, m] * w_scale[n / 128, b] * P_b[m, n] ),
+ *     P_b[m, n] = sum over k in block b of xq[m, k] * wq[n, k]
+ * P_b from the fp8 matrix unit, which adds each group of eight consecutive
+ * products to 13 bits below the largest of them; the sum over the blocks is
+ * held in fp32, the two scales multiplied in fp32.  y fp16 [M, N]; any M >= 0
+ * and N >= 0.  Same bits for the same call.  workspace: device buffer of
+ * f8_gemm_workspace_size() bytes, 256-byte aligned (may be NULL when that is
+ * 0), which needs no initial content; calls that overlap need their own. */
+w4a8_status_t f8_gemm(const uint8_t *xq, const float *x_scale, const uint8_t *wq, const float *w_scale,
+                      w4a8_f16 *y, int64_t M, int64_t N, int64_t K, void *workspace,
+                      size_t workspace_bytes, w4a8_stream_t stream);
+
+typedef enum {
+    W4A8_ACT_SILU = 0,     /* g / (1 + e^-g) */
+    W4A8_ACT_GELU_TANH = 1 /* 0.5 g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) */
+} w4a8_activation_t;
+
+/* Bytes of device workspace f8_gemm_gated() needs for these sizes; quantize:
+ * nonzero for the output in e4m3. */
+size_t f8_gemm_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t quantize);
+
+/* The first half of a gated feed-forward block, both products, the activation
+ * and the multiplication in one kernel:
+ *     v[m, n] = act(g[m, n]) * u[m, n]
+ * with g and u the sums of f8_gemm (before their rounding to fp16) of xq with
+ * w_gate [N, K] and w_up [N, K].  Either y fp16 [M, N] = fp16(v), yq and
+ * y_scale NULL; or y NULL, yq uint8 [M, N] and y_scale fp32 [NB, M] = v
+ * quantized by the e4m3 rule, ready for the f8_gemm behind it.  The rest as
+ * f8_gemm. */
+w4a8_status_t f8_gemm_gated(const uint8_t *xq, const float *x_scale, const uint8_t *w_gate,
+                            const float *gate_scale, const uint8_t *w_up, const float *up_scale,
+                            w4a8_activation_t activation, int64_t M, int64_t N, int64_t K, w4a8_f16 *y,
+                            uint8_t *yq, float *y_scale, void *workspace, size_t workspace_bytes,
+                            w4a8_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -47,6 +47,13 @@ _SIGNATURES = {
     "kv4_attention_workspace_size": [_i32, _i32, _i32, _i64, _i64, _i32],
     "kv4_attention": [_vp, _i64, _i64, _i32, _vp, _vp, _i32, _vp, _vp, _i64, _i32, _i32, _i32,
                       ctypes.c_float, _vp, _vp, _vp, _sz, _vp],
+    "quantize_act_f8": [_vp, _i64, _i64, _vp, _vp, _vp],
+    "quantize_weight_f8": [_vp, _i64, _i64, _vp, _vp, _vp],
+    "rmsnorm_quant": [ctypes.c_int, _vp, _vp, _vp, ctypes.c_float, _i64, _i64, _i32, _vp, _vp, _vp, _vp],
+    "f8_gemm_workspace_size": [_i64, _i64, _i64],
+    "f8_gemm": [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _sz, _vp],
+    "f8_gemm_gated_workspace_size": [_i64, _i64, _i64, _i32],
+    "f8_gemm_gated": [_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp],
     "gemm_tile_config": [ctypes.c_int, _i64, _i64, _i64, _i32, ctypes.POINTER(_i64)],
 }
 _RESTYPES = {
@@ -55,6 +62,8 @@ _RESTYPES = {
     "w4a8_last_error": ctypes.c_char_p,
     "linear_workspace_size": _sz,
     "kv4_attention_workspace_size": _sz,
+    "f8_gemm_workspace_size": _sz,
+    "f8_gemm_gated_workspace_size": _sz,
 }
 
 
@@ -78,6 +87,12 @@ class Mode(enum.IntEnum):
     W8A8_PC = 0
     W8A8_PG = 1
     W4A8 = 2
+    F8 = 3
+
+
+class Activation(enum.IntEnum):
+    SILU = 0
+    GELU_TANH = 1
 
 
 class GemmOp(enum.IntEnum):

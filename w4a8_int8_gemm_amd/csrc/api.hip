@@ -10,6 +10,7 @@
 #include <atomic>
 
 #include "../../include/w4a8.h"
+#include "f8.hpp"
 #include "kernels.hpp"
 #include "kv4.hpp"
 
@@ -193,6 +194,73 @@ w4a8_status_t check_mv_group(const char *fn, const void *x, const void *w, const
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// ---- 8-bit floating point
+
+constexpr int64_t kMaxRowsF8 = int64_t(1) << 25;   // rows a launch of one wavefront each can number
+
+// The sizes and buffers of a product's operands: x (codes, or fp16 of the
+// same alignment) with or without scales, one or two weights.
+w4a8_status_t check_f8(const char *fn, const void *x, const float *sx, bool need_sx, const void *w,
+                       const float *sw, const void *w2, const float *sw2, bool gated, int64_t M,
+                       int64_t N, int64_t K)
+{
+    if (M < 0 || N < 0 || K < 0 || M > kMaxRowsF8 || N > kMaxDim)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: sizes out of range (M=%lld N=%lld K=%lld)", fn,
+                    (long long)M, (long long)N, (long long)K);
+    if (K == 0 || K % 16 != 0 || K > kMaxKGemm)
+        return fail(W4A8_ERR_SHAPE, "%s: K=%lld must be a positive multiple of 16 up to %lld", fn,
+                    (long long)K, (long long)kMaxKGemm);
+    if (((M + 31) / 32) * ((N + 127) / 128) > kMaxTiles)
+        return fail(W4A8_ERR_SHAPE, "%s: output of %lld x %lld is too large", fn, (long long)M,
+                    (long long)N);
+    if (M == 0 || N == 0)
+        return W4A8_OK;
+    if (!x || !w || !sw || (need_sx && !sx) || (gated && (!w2 || !sw2)))
+        return fail(W4A8_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(x) || !aligned16(w) || !aligned16(w2) || !aligned4(sx) || !aligned4(sw) ||
+        !aligned4(sw2))
+        return fail(W4A8_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
+    return W4A8_OK;
+}
+
+w4a8_status_t check_workspace(const char *fn, size_t need, const void *workspace, size_t bytes)
+{
+    if (need > 0 && (!workspace || bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+        return fail(W4A8_ERR_WORKSPACE, "%s: workspace of %zu bytes (256-byte aligned) needed, got %zu",
+                    fn, need, bytes);
+    return W4A8_OK;
+}
+
+F8Args make_f8(const uint8_t *x, const float *sx, const uint8_t *w, const float *sw, const uint8_t *w2,
+               const float *sw2, int64_t M, int64_t N, int64_t K)
+{
+    F8Args a{};
+    a.x = x; a.sx = sx;
+    a.w[0] = w; a.sw[0] = sw; a.w[1] = w2; a.sw[1] = sw2;
+    a.M = (int)M; a.N = (int)N; a.K = (int)K;
+    return a;
+}
+
+// The product on checked arguments.
+w4a8_status_t run_f8(const char *fn, F8Args a, w4a8_stream_t stream)
+{
+    w4a8_status_t st = check_device(&a.num_cu);
+    if (st != W4A8_OK)
+        return st;
+    launch_f8_gemm(a, (hipStream_t)stream);
+    return check_launch(fn);
+}
+
+// linear()'s workspace in the F8 mode: codes, scales, and what the product
+// needs whatever N is.
+struct F8Linear {
+    size_t codes, scales;
+    F8Linear(int64_t M, int64_t K)
+        : codes(align256((size_t)M * (size_t)K)),
+          scales(align256((size_t)M * (size_t)((K + 127) / 128) * sizeof(float))) {}
+    size_t bytes() const { return codes + scales; }
+};
+
 // ---- the static scratch of linear_noalloc(): the activations' int8 codes
 // and fp32 scales live in this device array instead of a caller workspace.
 // Each device the library runs on holds its own copy (placed when the code
@@ -306,6 +374,15 @@ w4a8_status_t check_linear(const char *fn, w4a8_mode_t mode, const w4a8_f16 *x, 
                            int64_t N, w4a8_f16 *y, bool *empty)
 {
     *empty = false;
+    if (mode == W4A8_MODE_F8) {
+        w4a8_status_t st = check_f8(fn, x, nullptr, false, w, w_scale, nullptr, nullptr, false, M, N, K);
+        if (st != W4A8_OK)
+            return st;
+        *empty = M == 0 || N == 0;
+        if (!*empty && (!y || !aligned16(y)))
+            return fail(y ? W4A8_ERR_ALIGNMENT : W4A8_ERR_INVALID_ARG, "%s: bad y", fn);
+        return W4A8_OK;
+    }
     if (mode != W4A8_MODE_W8A8_PC && mode != W4A8_MODE_W8A8_PG && mode != W4A8_MODE_W4A8)
         return fail(W4A8_ERR_INVALID_ARG, "%s: unknown mode %d", fn, (int)mode);
     const bool pg = mode != W4A8_MODE_W8A8_PC;
@@ -331,6 +408,20 @@ w4a8_status_t linear_run(const char *fn, w4a8_mode_t mode, const w4a8_f16 *x, in
 {
     const int32_t act_gs = (mode == W4A8_MODE_W8A8_PG) ? group_size : 0;
     w4a8_status_t st;
+    if (mode == W4A8_MODE_F8) {
+        const F8Linear ws(M, K);
+        st = check_workspace(fn, ws.bytes(), workspace, workspace_bytes);
+        if (st != W4A8_OK)
+            return st;
+        uint8_t *xq = static_cast<uint8_t *>(workspace);
+        float *xs = reinterpret_cast<float *>(xq + ws.codes);
+        st = quantize_act_f8(x, M, K, xq, xs, stream);
+        if (st != W4A8_OK)
+            return st;
+        F8Args a = make_f8(xq, xs, static_cast<const uint8_t *>(w), w_scale, nullptr, nullptr, M, N, K);
+        a.y = y;
+        return run_f8(fn, a, stream);
+    }
     if (M == 1 && K <= kMaxKMv) {                 // decode: the matrix-vector kernels
         switch (mode) {
         case W4A8_MODE_W8A8_PC:
@@ -622,6 +713,8 @@ size_t linear_workspace_size(w4a8_mode_t mode, int64_t M, int64_t K, int32_t gro
 {
     if (M <= 0 || K <= 0)
         return 0;
+    if (mode == W4A8_MODE_F8)
+        return F8Linear(M, K).bytes();
     if (M == 1 && K <= kMaxKMv)                   // the matrix-vector kernels need none
         return 0;
     int64_t groups = 1;
@@ -880,6 +973,147 @@ w4a8_status_t kv4_read(const kv4_cache_t *cache, const int64_t *slots, int64_t T
     if (st != W4A8_OK)
         return st;
     launch_kv4_read(make_cache(cache), slots, T, k, v, (hipStream_t)stream);
+    return check_launch(fn);
+}
+
+w4a8_status_t quantize_act_f8(const w4a8_f16 *x, int64_t M, int64_t K, uint8_t *xq, float *x_scale,
+                              w4a8_stream_t stream)
+{
+    const char *fn = "quantize_act_f8";
+    if (M < 0 || K < 0 || M > kMaxRowsF8 || K > kMaxDim)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: sizes out of range (M=%lld K=%lld)", fn, (long long)M,
+                    (long long)K);
+    w4a8_status_t st = check_quant(fn, x, M, K, 0, xq, x_scale, false);
+    if (st != W4A8_OK)
+        return st;
+    if (M == 0)
+        return ok();
+    st = check_device();
+    if (st != W4A8_OK)
+        return st;
+    launch_quantize_act_f8(x, M, (int)K, xq, x_scale, (hipStream_t)stream);
+    return check_launch(fn);
+}
+
+w4a8_status_t quantize_weight_f8(const w4a8_f16 *w, int64_t N, int64_t K, uint8_t *wq, float *w_scale,
+                                 w4a8_stream_t stream)
+{
+    const char *fn = "quantize_weight_f8";
+    w4a8_status_t st = check_quant(fn, w, N, K, 0, wq, w_scale, false);
+    if (st != W4A8_OK)
+        return st;
+    if (((N + 127) / 128) * ((K + 127) / 128) >= (1 << 24))
+        return fail(W4A8_ERR_SHAPE, "%s: N=%lld x K=%lld has more than 2^24 - 1 blocks", fn, (long long)N,
+                    (long long)K);
+    if (N == 0)
+        return ok();
+    st = check_device();
+    if (st != W4A8_OK)
+        return st;
+    launch_quantize_weight_f8(w, N, (int)K, wq, w_scale, (hipStream_t)stream);
+    return check_launch(fn);
+}
+
+w4a8_status_t rmsnorm_quant(w4a8_mode_t mode, const w4a8_f16 *x, const w4a8_f16 *residual,
+                            const w4a8_f16 *gain, float eps, int64_t M, int64_t K, int32_t group_size,
+                            void *q, float *scale, w4a8_f16 *residual_out, w4a8_stream_t stream)
+{
+    const char *fn = "rmsnorm_quant";
+    if (mode != W4A8_MODE_W8A8_PC && mode != W4A8_MODE_W8A8_PG && mode != W4A8_MODE_W4A8 &&
+        mode != W4A8_MODE_F8)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: unknown mode %d", fn, (int)mode);
+    if (M < 0 || K < 0 || M > kMaxRowsF8 || K > kMaxKGemm)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: sizes out of range (M=%lld K=%lld)", fn, (long long)M,
+                    (long long)K);
+    const bool groups = mode == W4A8_MODE_W8A8_PG;
+    if (groups && group_size != 64 && group_size != 128)
+        return fail(W4A8_ERR_SHAPE, "%s: group_size=%d must be 64 or 128", fn, (int)group_size);
+    if (!(eps >= 0.0f) || eps > 0x1p127f)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
+    w4a8_status_t st = check_quant(fn, x, M, K, groups ? group_size : 0, q, scale, false);
+    if (st != W4A8_OK)
+        return st;
+    if (M == 0)
+        return ok();
+    if (!gain)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: null gain", fn);
+    if (!aligned16(gain) || !aligned16(residual) || !aligned16(residual_out))
+        return fail(W4A8_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
+    st = check_device();
+    if (st != W4A8_OK)
+        return st;
+    NormArgs a;
+    a.x = x; a.residual = residual; a.gain = gain; a.sum = residual_out;
+    a.q = static_cast<uint8_t *>(q); a.scale = scale;
+    a.M = M; a.K = (int)K; a.eps = eps;
+    const NormOut out = mode == W4A8_MODE_F8 ? NormOut::F8
+                        : !groups            ? NormOut::INT8_ROW
+                        : group_size == 64   ? NormOut::INT8_64
+                                             : NormOut::INT8_128;
+    launch_rmsnorm_quant(out, a, (hipStream_t)stream);
+    return check_launch(fn);
+}
+
+size_t f8_gemm_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    (void)M; (void)N; (void)K;
+    return 0;
+}
+
+w4a8_status_t f8_gemm(const uint8_t *xq, const float *x_scale, const uint8_t *wq, const float *w_scale,
+                      w4a8_f16 *y, int64_t M, int64_t N, int64_t K, void *workspace,
+                      size_t workspace_bytes, w4a8_stream_t stream)
+{
+    const char *fn = "f8_gemm";
+    w4a8_status_t st = check_f8(fn, xq, x_scale, true, wq, w_scale, nullptr, nullptr, false, M, N, K);
+    if (st != W4A8_OK)
+        return st;
+    if (M == 0 || N == 0)
+        return ok();
+    if (!y || !aligned16(y))
+        return fail(y ? W4A8_ERR_ALIGNMENT : W4A8_ERR_INVALID_ARG, "%s: bad y", fn);
+    st = check_workspace(fn, f8_gemm_workspace_size(M, N, K), workspace, workspace_bytes);
+    if (st != W4A8_OK)
+        return st;
+    F8Args a = make_f8(xq, x_scale, wq, w_scale, nullptr, nullptr, M, N, K);
+    a.y = y;
+    return run_f8(fn, a, stream);
+}
+
+size_t f8_gemm_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t quantize)
+{
+    (void)M; (void)N; (void)K; (void)quantize;
+    return 0;
+}
+
+w4a8_status_t f8_gemm_gated(const uint8_t *xq, const float *x_scale, const uint8_t *w_gate,
+                            const float *gate_scale, const uint8_t *w_up, const float *up_scale,
+                            w4a8_activation_t activation, int64_t M, int64_t N, int64_t K, w4a8_f16 *y,
+                            uint8_t *yq, float *y_scale, void *workspace, size_t workspace_bytes,
+                            w4a8_stream_t stream)
+{
+    const char *fn = "f8_gemm_gated";
+    w4a8_status_t st = check_f8(fn, xq, x_scale, true, w_gate, gate_scale, w_up, up_scale, true, M, N, K);
+    if (st != W4A8_OK)
+        return st;
+    if (activation != W4A8_ACT_SILU && activation != W4A8_ACT_GELU_TANH)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: unknown activation %d", fn, (int)activation);
+    if (M == 0 || N == 0)
+        return ok();
+    if (y ? (yq || y_scale) : (!yq || !y_scale))
+        return fail(W4A8_ERR_INVALID_ARG, "%s: either y, or yq and y_scale", fn);
+    if (!aligned16(y) || !aligned16(yq) || !aligned4(y_scale))
+        return fail(W4A8_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
+    st = check_workspace(fn, f8_gemm_gated_workspace_size(M, N, K, y ? 0 : 1), workspace, workspace_bytes);
+    if (st != W4A8_OK)
+        return st;
+    F8Args a = make_f8(xq, x_scale, w_gate, gate_scale, w_up, up_scale, M, N, K);
+    a.y = y; a.yq = yq; a.ys = y_scale;
+    a.gelu = activation == W4A8_ACT_GELU_TANH;
+    st = check_device(&a.num_cu);
+    if (st != W4A8_OK)
+        return st;
+    launch_f8_gated(a, (hipStream_t)stream);
     return check_launch(fn);
 }
 

@@ -205,18 +205,29 @@ def linear_workspace_size(mode, M: int, K: int, group_size: int = 0) -> int:
     return int(lib().linear_workspace_size(int(mode), M, K, group_size))
 
 
-def linear(mode, x, w, w_scale, group_size: int = 0, workspace=None, out=None):
-    """The whole layer: the mode's matrix-vector kernel when M == 1, else quantize + GEMM."""
-    mode = Mode(mode)
+_WEIGHT_DTYPE = {Mode.W4A8: torch.uint8, Mode.F8: torch.float8_e4m3fn}
+
+
+def _linear_shapes(mode, x, w, w_scale, group_size):
     _need(x, torch.float16, "x", 2)
-    packed = mode == Mode.W4A8
-    _need(w, torch.uint8 if packed else torch.int8, "w", 2, x)
+    _need(w, _WEIGHT_DTYPE.get(mode, torch.int8), "w", 2, x)
     M, K = x.shape
     N = w.shape[0]
-    if w.shape[1] * (2 if packed else 1) != K:
+    if w.shape[1] * (2 if mode == Mode.W4A8 else 1) != K:
         raise ValueError("weight shape does not match K")
-    sw_shape = (N,) if mode == Mode.W8A8_PC else (N, _groups(K, group_size))
+    if mode == Mode.F8:
+        sw_shape = ((N + 127) // 128, (K + 127) // 128)
+    else:
+        sw_shape = (N,) if mode == Mode.W8A8_PC else (N, _groups(K, group_size))
     _shaped(w_scale, torch.float32, sw_shape, "w_scale", x)
+    return M, N, K
+
+
+def linear(mode, x, w, w_scale, group_size: int = 0, workspace=None, out=None):
+    """The whole layer: the mode's matrix-vector kernel when M == 1 (the int8 modes), else quantize +
+    GEMM.  Mode.F8 takes the weights of quantize_weight_f8."""
+    mode = Mode(mode)
+    M, N, K = _linear_shapes(mode, x, w, w_scale, group_size)
     need = linear_workspace_size(mode, M, K, group_size)
     if workspace is None:
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
@@ -236,15 +247,7 @@ def linear_noalloc(mode, x, w, w_scale, group_size: int = 0, out=None):
     a static 64 MiB device array (no allocation in the call; calls that overlap
     on one GPU race).  Pass ``out`` to keep this wrapper allocation-free too."""
     mode = Mode(mode)
-    _need(x, torch.float16, "x", 2)
-    packed = mode == Mode.W4A8
-    _need(w, torch.uint8 if packed else torch.int8, "w", 2, x)
-    M, K = x.shape
-    N = w.shape[0]
-    if w.shape[1] * (2 if packed else 1) != K:
-        raise ValueError("weight shape does not match K")
-    sw_shape = (N,) if mode == Mode.W8A8_PC else (N, _groups(K, group_size))
-    _shaped(w_scale, torch.float32, sw_shape, "w_scale", x)
+    M, N, K = _linear_shapes(mode, x, w, w_scale, group_size)
     out = _out(out, (M, N), torch.float16, x, "out")
     with torch.cuda.device(x.device):
         check(lib().linear_noalloc(int(mode), _p(x), M, K, _p(w), _p(w_scale), group_size, N,
