@@ -47,5 +47,6 @@ struct F8Args {
 };
 void launch_f8_gemm(const F8Args &a, hipStream_t st);
 void launch_f8_gated(const F8Args &a, hipStream_t st);
+void launch_f8_large(const F8Args &a, bool gated, hipStream_t st);
 
 }  // namespace w4a8

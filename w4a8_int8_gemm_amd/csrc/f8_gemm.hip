@@ -154,7 +154,20 @@ static void launch(const F8Args &a, hipStream_t st)
                        tiles_m, tiles);
 }
 
-void launch_f8_gemm(const F8Args &a, hipStream_t st) { launch<false>(a, st); }
-void launch_f8_gated(const F8Args &a, hipStream_t st) { launch<true>(a, st); }
+void launch_f8_gemm(const F8Args &a, hipStream_t st)
+{
+    if (a.M > 64)
+        launch_f8_large(a, false, st);
+    else
+        launch<false>(a, st);
+}
+
+void launch_f8_gated(const F8Args &a, hipStream_t st)
+{
+    if (a.M > 64)
+        launch_f8_large(a, true, st);
+    else
+        launch<true>(a, st);
+}
 
 }  // namespace w4a8
