@@ -29,11 +29,20 @@ __device__ __forceinline__ void wait_lds()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// At most N of the wave's copies may still be on their way.
+template <int N> __device__ __forceinline__ void wait_copies()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<N>();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 template <bool GATED>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t ring[2 * LSB];
+    __shared__ __attribute__((aligned(256))) float scales[2][2][LBM];   // [stage parity][of x, of w][4 waves x 64]
     __shared__ uint32_t top[2][LBM];
 
     const int M = a.M, N = a.N, K = a.K;
@@ -61,45 +70,79 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
         n0 = (in / gm) * OUTN;
     };
 
-    // copies: lane l of a 1 KiB block (8 rows) writes row l / 8, place l % 8
+    // ---- copies.  The stages of all of the workgroup's tiles are one stream;
+    // the cursor is the stage whose x and first half of w come next, the
+    // second half follows one stage later (its own resource and k).  Lane l of
+    // a 1 KiB block (8 rows) writes row l / 8, place l % 8.
     const int chunk0 = 16 * ((lane & 7) ^ (lane >> 3));
     const uint32_t ring_at = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(ring));
-    v4i rx, rw0, rw1;
-    auto set_tile = [&](int m0, int n0) __attribute__((always_inline)) {
+    const uint32_t scales_at = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(scales));
+    v4i rx, rw0, rw1, rw1_now;
+    const float *scp;
+    int cur_tile = wl, cur_s = 0, cur_m0, w1_s = 0;
+    uint32_t cur_buf = 0;
+    auto set_tile = [&]() __attribute__((always_inline)) {
+        int m0, n0;
+        tile_origin(cur_tile, m0, n0);
+        cur_m0 = m0;
         rx = make_rsrc(a.x + (int64_t)m0 * K, (uint32_t)(min(LBM, M - m0) * K));
         const int n1 = GATED ? n0 : n0 + 128;
         rw0 = make_rsrc(a.w[0] + (int64_t)n0 * K, (uint32_t)(min(128, N - n0) * K));
-        const uint8_t *w1 = GATED ? a.w[1] : a.w[0];
-        rw1 = make_rsrc(w1 + (int64_t)min(n1, N) * K, (uint32_t)(max(0, min(128, N - n1)) * K));
+        rw1 = make_rsrc(a.w[GATED] + (int64_t)min(n1, N) * K, (uint32_t)(max(0, min(128, N - n1)) * K));
+        const int nb = n0 >> 7, nb1 = GATED ? nb : min(nb + 1, ((N + 127) >> 7) - 1);
+        if (group == 0)
+            scp = a.sx + min(m0 + wave * 64, M - 1);
+        else
+            scp = a.sw[GATED && (wave & 1)] + (int64_t)((wave & 1) ? nb1 : nb) * KB;
     };
-    // group 0 copies: its wave wm takes blocks 8 wm .. + 7 of X and of W (4 of each half)
-    auto issue_stage = [&](int s) __attribute__((always_inline)) {
-        const uint32_t k0 = (uint32_t)(s * 128);
-        const uint32_t base = ring_at + (uint32_t)((s & 1) * LSB);
+    auto advance = [&]() __attribute__((always_inline)) {
+        rw1_now = rw1;
+        w1_s = cur_s;
+        cur_buf ^= 1;
+        if (cur_s + 1 < KB) {
+            ++cur_s;
+        } else if (cur_tile + G < total) {            // past the end: the last stage again
+            cur_s = 0;
+            cur_tile += G;
+            set_tile();
+        }
+    };
+    // A lane's offset in a block of even (par 0) or odd number; chunks past the
+    // row's end (the last stage of a K that 128 does not divide) read zeros.
+    // Formed each time, not kept in registers.
+    auto lane_offset = [&](int par, int k0) __attribute__((always_inline)) {
         int ch = chunk0;
-        asm volatile("" : "+v"(ch));       // the offsets are formed here each time, not kept in registers
-        uint32_t vo[2];
-#pragma unroll
-        for (int par = 0; par < 2; ++par) {
-            const int c = ch ^ (16 * par);
-            // chunks past the row's end (the last stage of a K that 128 does not divide) read zeros
-            vo[par] = (uint32_t)((lane >> 3) * K + c) | ((int)k0 + c >= K ? 0x80000000u : 0u);
-        }
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            const int blk = wm * 8 + p;
-            set_m0(base + blk * 1024);
-            copy16_buf_to_lds<0>(rx, vo[p & 1] + (uint32_t)(blk * 8 * K), k0);
-        }
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            const int blk = wm * 4 + (p & 3);
-            set_m0(base + LXB + (p >> 2) * 16384 + blk * 1024);
-            copy16_buf_to_lds<0>(p < 4 ? rw0 : rw1, vo[p & 1] + (uint32_t)(blk * 8 * K), k0);
-        }
+        asm volatile("" : "+v"(ch));
+        const int c = ch ^ (16 * par);
+        return (uint32_t)((lane >> 3) * K + c) | (k0 + c >= K ? 0x80000000u : 0u);
+    };
+    auto copy_x = [&](int p) __attribute__((always_inline)) {         // p = 0 .. 3
+        const int blk = wave * 4 + p, k0 = cur_s * 128;
+        set_m0(ring_at + cur_buf * LSB + blk * 1024);
+        copy16_buf_to_lds<0>(rx, lane_offset(p & 1, k0) + (uint32_t)(blk * 8 * K), (uint32_t)k0);
+    };
+    auto copy_w0 = [&](int p) __attribute__((always_inline)) {        // p = 0, 1
+        const int blk = wave * 2 + p, k0 = cur_s * 128;
+        set_m0(ring_at + cur_buf * LSB + LXB + blk * 1024);
+        copy16_buf_to_lds<0>(rw0, lane_offset(p, k0) + (uint32_t)(blk * 8 * K), (uint32_t)k0);
+    };
+    auto copy_w1 = [&](int p) __attribute__((always_inline)) {        // of the stage before the cursor's
+        const int blk = wave * 2 + p, k0 = w1_s * 128;
+        set_m0(ring_at + (cur_buf ^ 1) * LSB + LXB + 16384 + blk * 1024);
+        copy16_buf_to_lds<0>(rw1_now, lane_offset(p, k0) + (uint32_t)(blk * 8 * K), (uint32_t)k0);
+    };
+    // waves 0-3: x's scales of 64 tokens; wave 4 (and 6): the first half's of
+    // w, wave 5 (and 7): the second's, in every lane
+    const int64_t sc_step = group == 0 ? M : 1;
+    const uint32_t sc_mask = group == 0 ? 63 : 0;
+    auto copy_scales = [&]() __attribute__((always_inline)) {
+        uint32_t l = (uint32_t)lane & sc_mask;
+        asm volatile("" : "+v"(l));
+        l = min(l, (uint32_t)max(0, M - 1 - cur_m0 - wm * 64));
+        copy4_to_lds(scp + cur_s * sc_step + l, scales_at + cur_buf * 2048 + wave * 256);
     };
 
-    // fragments: lane l reads row l % 16; of the eight 16-byte chunks of a
+    // ---- fragments: lane l reads row l % 16; of the eight 16-byte chunks of a
     // stage lane group h takes 0 1, 2 3, 5 4, 7 6
     const int lr = lane & 15, lh = lane >> 4;
     const int c0 = lh == 0 ? 0 : lh == 1 ? 2 : lh == 2 ? 5 : 7;
@@ -115,8 +158,9 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
     v4f pr[4];
     float sc[2][4];
 
-    // sixteen products of one half, each folded three products later
-    auto compute = [&](auto HALF) __attribute__((always_inline)) {
+    // sixteen products of one half, each folded three products later; `copy`
+    // runs between them
+    auto compute = [&](auto HALF, auto copy) __attribute__((always_inline)) {
         constexpr int h = decltype(HALF)::value;
 #pragma unroll
         for (int t = 0; t < 16 + 3; ++t) {
@@ -130,20 +174,40 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
                 for (int r = 0; r < 4; ++r)
                     acc[h][u >> 2][u & 3][r] = fmaf(pr[u & 3][r], sc[h][u & 3], acc[h][u >> 2][u & 3][r]);
             }
+            if (t < 16)
+                copy(t);
             __builtin_amdgcn_sched_barrier(0);
         }
+        // the sums are formed here, not where the compiler next needs them
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float *v = acc[h][i][j];
+                asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]));
+            }
     };
 
-    int tile = wl;
-    int m0, n0;
-    tile_origin(tile, m0, n0);
-    set_tile(m0, n0);
-    if (group == 0) {
-        issue_stage(0);
-    }
-    while (true) {
-        const int nb = n0 >> 7, nb1 = GATED ? nb : min(nb + 1, ((N + 127) >> 7) - 1);
-        const float *swp0 = a.sw[0] + (int64_t)nb * KB, *swp1 = a.sw[GATED] + (int64_t)nb1 * KB;
+    set_tile();
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        copy_x(p);
+    copy_w0(0);
+    copy_w0(1);
+    copy_scales();
+    advance();
+    copy_w1(0);
+    copy_w1(1);
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        copy_x(p);
+    copy_w0(0);
+    copy_w0(1);
+    copy_scales();
+    wait_vmcnt<9>();                                  // the first stage's x, w0 and scales
+    phase_barrier();
+    int b = 0;
+    for (int tile = wl; tile < total; tile += G) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -153,74 +217,65 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         acc[h][i][j][r] = 0.0f;
-        float sx[4], sw[2];
-        auto load_scales = [&](int s) __attribute__((always_inline)) {
-            const char *row = reinterpret_cast<const char *>(a.sx + (int64_t)s * M);
-            uint32_t at = lr;
-            asm volatile("" : "+v"(at));       // as above
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                sx[j] = *reinterpret_cast<const float *>(row + 4 * min(at + (uint32_t)(m0 + wm * 64 + 16 * j), (uint32_t)M - 1));
-            at = 0;
-            asm volatile("" : "+v"(at));       // the weights' scales by vector loads too: scalar ones and LDS reads
-            sw[0] = *reinterpret_cast<const float *>(reinterpret_cast<const char *>(swp0 + s) + at);   // share a counter
-            sw[1] = *reinterpret_cast<const float *>(reinterpret_cast<const char *>(swp1 + s) + at);
-        };
-        load_scales(0);
-        wait_vmcnt<0>();
-        phase_barrier();
         if (group == 1)
             phase_barrier();
 #pragma clang loop unroll(disable)
         for (int s = 0; s < KB; ++s) {
-            const uint8_t *buf = ring + (s & 1) * LSB;
+            const uint8_t *buf = ring + b * LSB;
             const uint8_t *xb = buf + wm * 64 * 128, *wb = buf + LXB + group * 64 * 128;
+            float sx[4], sw[2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 xf[i] = read_frag(xb + i * 2048);
                 wf[i] = read_frag(wb + i * 2048);
             }
 #pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sx[j] = scales[b][0][wm * 64 + 16 * j + lr];
+            sw[0] = scales[b][1][0];
+            sw[1] = scales[b][1][64];
+            __builtin_amdgcn_sched_barrier(0);
+            advance();
+            copy_w1(0);
+            wait_lds();
+#pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     sc[h][j] = sx[j] * sw[h];
-            __builtin_amdgcn_sched_barrier(0);
-            load_scales(min(s + 1, KB - 1));
-            if (group == 0 && s + 1 < KB)
-                issue_stage(s + 1);
-            wait_lds();
+            wait_copies<8>();                         // this stage's second half of w
             phase_barrier();
-            compute(std::integral_constant<int, 0>());
+            compute(std::integral_constant<int, 0>(), [&](int t) __attribute__((always_inline)) {
+                if (t == 4)
+                    copy_w1(1);
+            });
             phase_barrier();
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 wf[i] = read_frag(wb + 16384 + i * 2048);
-            wait_lds();
-            phase_barrier();
-            compute(std::integral_constant<int, 1>());
             __builtin_amdgcn_sched_barrier(0);
-            wait_vmcnt<0>();
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                copy_x(p);
+            wait_lds();
+            wait_copies<6>();                         // the next stage's x, first half of w and scales
             phase_barrier();
+            compute(std::integral_constant<int, 1>(), [&](int t) __attribute__((always_inline)) {
+                if (t == 2 || t == 6)
+                    copy_w0(t >> 2);
+                if (t == 10)
+                    copy_scales();
+            });
+            phase_barrier();
+            b ^= 1;
         }
         if (group == 0)
             phase_barrier();
-        // both groups are past their last reads: the next tile's stages may come
-        const int om = m0, on = n0;
-        tile += G;
-        const bool more = tile < total;
-        if (more) {
-            tile_origin(tile, m0, n0);
-            set_tile(m0, n0);
-            if (group == 0) {
-                issue_stage(0);
-            }
-        }
-        f8_store_tile<GATED, 4, 4>(a, acc, om + wm * 64, on + group * 64, on, 128, lane, group, wm * 64, top);
-        if (!more)
-            break;
+        int m0, n0;
+        tile_origin(tile, m0, n0);
+        f8_store_tile<GATED, 4, 4>(a, acc, m0 + wm * 64, n0 + group * 64, n0, 128, lane, group, wm * 64, top);
     }
-    wait_vmcnt<0>();
+    wait_vmcnt<0>();                                  // no copy may still be writing LDS at the end
 }
 
 }  // namespace
