@@ -22,7 +22,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_pc.hip", "gemm_skinny.hip", "gemm_rows.hip",
            "mv.hip", "w8a16.hip", "rotary.hip", "kv4_cache.hip", "kv4_attention.hip",
-           "kv4_decode.hip", "kv4_prefill.hip", "f8_quant.hip", "f8_gemm.hip", "f8_large.hip"]
+           "kv4_decode.hip", "kv4_prefill.hip", "f8_quant.hip", "f8_gemm.hip", "f8_few.hip",
+           "f8_large.hip"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -194,6 +194,25 @@ w4a8_status_t check_mv_group(const char *fn, const void *x, const void *w, const
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// A tag per call for the counters in its workspace: 48 bits
+// over a 16-bit count, other than those of the calls before and, by a start
+// from the clock, the process and where it lies, of other processes'.  (No
+// std::random_device: it may throw, and this is behind a C entry point.)
+uint64_t first_tag()
+{
+    struct timespec now = {0, 0};
+    clock_gettime(CLOCK_REALTIME, &now);
+    const uint64_t x = ((uint64_t)now.tv_sec * 1000000000u + (uint64_t)now.tv_nsec) ^ ((uint64_t)getpid() << 32) ^
+                       (uint64_t)reinterpret_cast<uintptr_t>(&now);
+    return (x * 0x9e3779b97f4a7c15u) >> 17;              // 2^64 over the golden ratio: every bit reaches the upper ones
+}
+
+uint64_t next_tag()
+{
+    static std::atomic<uint64_t> tag{first_tag()};
+    return (tag.fetch_add(1, std::memory_order_relaxed) | (uint64_t(1) << 47)) << 16;
+}
+
 // ---- 8-bit floating point
 
 constexpr int64_t kMaxRowsF8 = int64_t(1) << 25;   // rows a launch of one wavefront each can number
@@ -242,23 +261,24 @@ F8Args make_f8(const uint8_t *x, const float *sx, const uint8_t *w, const float 
 }
 
 // The product on checked arguments.
-w4a8_status_t run_f8(const char *fn, F8Args a, w4a8_stream_t stream)
+w4a8_status_t run_f8(const char *fn, F8Args a, bool gated, void *workspace, w4a8_stream_t stream)
 {
     w4a8_status_t st = check_device(&a.num_cu);
     if (st != W4A8_OK)
         return st;
-    launch_f8_gemm(a, (hipStream_t)stream);
+    launch_f8(a, gated, next_tag(), workspace, (hipStream_t)stream);
     return check_launch(fn);
 }
 
 // linear()'s workspace in the F8 mode: codes, scales, and what the product
 // needs whatever N is.
 struct F8Linear {
-    size_t codes, scales;
+    size_t codes, scales, product;
     F8Linear(int64_t M, int64_t K)
         : codes(align256((size_t)M * (size_t)K)),
-          scales(align256((size_t)M * (size_t)((K + 127) / 128) * sizeof(float))) {}
-    size_t bytes() const { return codes + scales; }
+          scales(align256((size_t)M * (size_t)((K + 127) / 128) * sizeof(float))),
+          product(f8_workspace_any(M, K)) {}
+    size_t bytes() const { return codes + scales + product; }
 };
 
 // ---- the static scratch of linear_noalloc(): the activations' int8 codes
@@ -420,7 +440,7 @@ w4a8_status_t linear_run(const char *fn, w4a8_mode_t mode, const w4a8_f16 *x, in
             return st;
         F8Args a = make_f8(xq, xs, static_cast<const uint8_t *>(w), w_scale, nullptr, nullptr, M, N, K);
         a.y = y;
-        return run_f8(fn, a, stream);
+        return run_f8(fn, a, false, xq + ws.codes + ws.scales, stream);
     }
     if (M == 1 && K <= kMaxKMv) {                 // decode: the matrix-vector kernels
         switch (mode) {
@@ -536,25 +556,6 @@ Kv4Cache make_cache(const kv4_cache_t *c)
     r.heads = c->kv_heads; r.shift = __builtin_ctz((unsigned)c->page_size);
     r.D = c->head_dim; r.G = c->group_size;
     return r;
-}
-
-// A tag per call of kv4_attention for the counters in its workspace: 48 bits
-// over a 16-bit count, other than those of the calls before and, by a start
-// from the clock, the process and where it lies, of other processes'.  (No
-// std::random_device: it may throw, and this is behind a C entry point.)
-uint64_t first_tag()
-{
-    struct timespec now = {0, 0};
-    clock_gettime(CLOCK_REALTIME, &now);
-    const uint64_t x = ((uint64_t)now.tv_sec * 1000000000u + (uint64_t)now.tv_nsec) ^ ((uint64_t)getpid() << 32) ^
-                       (uint64_t)reinterpret_cast<uintptr_t>(&now);
-    return (x * 0x9e3779b97f4a7c15u) >> 17;              // 2^64 over the golden ratio: every bit reaches the upper ones
-}
-
-uint64_t next_tag()
-{
-    static std::atomic<uint64_t> tag{first_tag()};
-    return (tag.fetch_add(1, std::memory_order_relaxed) | (uint64_t(1) << 47)) << 16;
 }
 
 // T tokens of a cache: four lanes a row, numbered in 32 bits.
@@ -1056,8 +1057,7 @@ w4a8_status_t rmsnorm_quant(w4a8_mode_t mode, const w4a8_f16 *x, const w4a8_f16 
 
 size_t f8_gemm_workspace_size(int64_t M, int64_t N, int64_t K)
 {
-    (void)M; (void)N; (void)K;
-    return 0;
+    return f8_workspace(M, N, K, false, false);
 }
 
 w4a8_status_t f8_gemm(const uint8_t *xq, const float *x_scale, const uint8_t *wq, const float *w_scale,
@@ -1077,13 +1077,12 @@ w4a8_status_t f8_gemm(const uint8_t *xq, const float *x_scale, const uint8_t *wq
         return st;
     F8Args a = make_f8(xq, x_scale, wq, w_scale, nullptr, nullptr, M, N, K);
     a.y = y;
-    return run_f8(fn, a, stream);
+    return run_f8(fn, a, false, workspace, stream);
 }
 
 size_t f8_gemm_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t quantize)
 {
-    (void)M; (void)N; (void)K; (void)quantize;
-    return 0;
+    return f8_workspace(M, N, K, true, quantize != 0);
 }
 
 w4a8_status_t f8_gemm_gated(const uint8_t *xq, const float *x_scale, const uint8_t *w_gate,
@@ -1110,11 +1109,7 @@ w4a8_status_t f8_gemm_gated(const uint8_t *xq, const float *x_scale, const uint8
     F8Args a = make_f8(xq, x_scale, w_gate, gate_scale, w_up, up_scale, M, N, K);
     a.y = y; a.yq = yq; a.ys = y_scale;
     a.gelu = activation == W4A8_ACT_GELU_TANH;
-    st = check_device(&a.num_cu);
-    if (st != W4A8_OK)
-        return st;
-    launch_f8_gated(a, (hipStream_t)stream);
-    return check_launch(fn);
+    return run_f8(fn, a, true, workspace, stream);
 }
 
 size_t kv4_attention_workspace_size(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t T,

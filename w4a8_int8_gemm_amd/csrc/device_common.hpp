@@ -33,6 +33,10 @@ __device__ __forceinline__ uint16_t f2h(float f)
     return __builtin_bit_cast(uint16_t, (_Float16)f);
 }
 
+// |v| as bits: the order of the bits is the order of the values, infinities
+// above every finite value and NaN above infinities.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
 // Two fp16 values (low, high half of a dword) to fp32.
 __device__ __forceinline__ float lo_h2f(uint32_t w) { return h2f((uint16_t)(w & 0xffffu)); }
 __device__ __forceinline__ float hi_h2f(uint32_t w) { return h2f((uint16_t)(w >> 16)); }

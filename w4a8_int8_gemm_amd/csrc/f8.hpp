@@ -45,8 +45,12 @@ struct F8Args {
     int gelu;                   // the gated product's activation: 0 silu, 1 gelu (tanh form)
     int num_cu;
 };
-void launch_f8_gemm(const F8Args &a, hipStream_t st);
-void launch_f8_gated(const F8Args &a, hipStream_t st);
+// The kernel for the sizes: the simple one, for few tokens (with a workspace of
+// f8_workspace() bytes and the call's tag among its counters), for large outputs.
+size_t f8_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool quantize);
+size_t f8_workspace_any(int64_t M, int64_t K);     // a product's, not gated, for every N
+void launch_f8(const F8Args &a, bool gated, uint64_t tag, void *workspace, hipStream_t st);
+void launch_f8_few(const F8Args &a, bool gated, uint64_t tag, void *workspace, hipStream_t st);
 void launch_f8_large(const F8Args &a, bool gated, hipStream_t st);
 
 }  // namespace w4a8

@@ -8,10 +8,6 @@ namespace w4a8 {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 
-// |v| as bits: the order of the bits is the order of the values, infinities
-// above every finite value and NaN above infinities.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
 // A block's scale and its reciprocal from the largest |v|, as bits.
 __device__ __forceinline__ void f8_block_scale(uint32_t amax_bits, float &s, float &r)
 {

@@ -18,7 +18,7 @@
 // 2^-14 of its group's largest vanishes; groups are then added as fp32).  That
 // is part of the hardware's product: relative to sum |x w| an error below
 // 8 2^-13, on Gaussian rows 1.4e-5 of the result's size.
-#include "f8.hpp"
+#include "f8_few.hpp"
 #include "f8_device.hpp"
 
 namespace w4a8 {
@@ -154,20 +154,23 @@ static void launch(const F8Args &a, hipStream_t st)
                        tiles_m, tiles);
 }
 
-void launch_f8_gemm(const F8Args &a, hipStream_t st)
+size_t f8_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool quantize)
 {
-    if (a.M > 64)
-        launch_f8_large(a, false, st);
-    else
-        launch<false>(a, st);
+    return M > 0 && N > 0 && K > 0 && M <= kF8FewTokens ? f8_few_workspace(M, N, K, gated, quantize) : 0;
 }
 
-void launch_f8_gated(const F8Args &a, hipStream_t st)
+size_t f8_workspace_any(int64_t, int64_t) { return 0; }
+
+void launch_f8(const F8Args &a, bool gated, uint64_t tag, void *workspace, hipStream_t st)
 {
-    if (a.M > 64)
-        launch_f8_large(a, true, st);
-    else
+    if (a.M <= kF8FewTokens)
+        launch_f8_few(a, gated, tag, workspace, st);
+    else if (a.M > 64)
+        launch_f8_large(a, gated, st);
+    else if (gated)
         launch<true>(a, st);
+    else
+        launch<false>(a, st);
 }
 
 }  // namespace w4a8

@@ -4,6 +4,8 @@
 
 #include <utility>
 
+#include "arrivals.hpp"
+#include "device_common.hpp"
 #include "kv4.hpp"
 
 namespace w4a8 {
@@ -179,10 +181,9 @@ __device__ __forceinline__ float sum_rows(float v)
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// A scale's bits without its sign: numbers in their order, what is not finite
+// A scale's bits without its sign (abs_bits): numbers in their order, what is not finite
 // above them.  The exponent floor(log2 v) of a finite one, -127 for 0.
 constexpr uint32_t kNotFinite = 0x7f800000u;
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >> 23) - 127; }
 
 // Weights p = 2^(score - ref) are multiplied with their value's scale and
@@ -221,43 +222,6 @@ __device__ __forceinline__ float bound_for(float ref, int e)
     return (bound - ref) - above > 0.5f ? ref : bound;
 }
 __device__ __forceinline__ uint32_t cap_of(int e) { return (uint32_t)(e + 128) << 23; }   // bits of 2^(e + 1)
-
-// Values that other workgroups, on other chiplets with L2 caches of their
-// own, wrote or will read within one launch: loads and stores at device scope.
-__device__ __forceinline__ void store_shared(float *p, float a, float b)
-{
-    const uint64_t v = ((uint64_t)__float_as_uint(b) << 32) | __float_as_uint(a);
-    __hip_atomic_store(reinterpret_cast<uint64_t *>(p), v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float2 load_shared(const float *p)
-{
-    const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
-
-// Arrivals at one counter of this call, without anything to clear before it:
-// the upper 48 bits name the call, the lower 16 count.  announce(), by every
-// workgroup before its arrival, gives a counter with another call's tag this
-// call's, once (the exchange fails for all but the first); arrive() then is
-// one addition, true for the last of `parts`, which clears the counter, so
-// that a captured call can run again.  (One exchange per arrival instead of
-// the addition would be tried again by all that lose it: 64 workgroups took
-// 100 us.)  The caller's stores are complete before arrive().
-__device__ __forceinline__ void announce(uint64_t *counter, uint64_t tag)
-{
-    uint64_t seen = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if ((seen & ~uint64_t(0xffff)) != tag)
-        __hip_atomic_compare_exchange_strong(counter, &seen, tag, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
-                                             __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ bool arrive(uint64_t *counter, int parts)
-{
-    const uint64_t n = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) & 0xffff;
-    if ((int)n != parts - 1)
-        return false;
-    __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return true;
-}
 
 // Where parts of a result that several workgroups compute meet.
 struct Partial {
