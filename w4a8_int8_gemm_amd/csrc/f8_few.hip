@@ -96,13 +96,17 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
 {
     constexpr int SIDES = GATED ? 2 : 1;
     constexpr int XB = HALF ? 1024 : MB * 2048;
-    constexpr int STAGE = XB + SIDES * RB * 2048 + 256;
-    constexpr int NI = XB / 1024 + SIDES * RB * 2 + 1;     // copies of a stage
+    // the scales of a stage: a lane a token and the last two for the weights, or
+    // where the tokens need all lanes a copy of their own for the weights'
+    constexpr int SC = MB <= 3 ? 1 : 2;
+    constexpr int SW = MB <= 3 ? 62 : 64;                   // where the weights' lie
+    constexpr int STAGE = XB + SIDES * RB * 2048 + SC * 256;
+    constexpr int NI = XB / 1024 + SIDES * RB * 2 + SC;     // copies of a stage
     constexpr int BLOCKS = SIDES * RB * MB;
     constexpr int RED = FW * BLOCKS * 1024;
     constexpr int RING = FW * D * STAGE;
     static_assert((D - 1) * NI < 64, "vmcnt range");
-    static_assert(MB <= 2, "the scales of a stage are one copy: a lane a token, two for the weights");
+    static_assert(MB <= 4, "a lane a token for its scale");
     __shared__ __attribute__((aligned(1024))) uint8_t lds[RING > RED ? RING : RED];
     __shared__ int last;
 
@@ -133,8 +137,9 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
     // the lane's scale of a stage: tokens first, the weights' in the last lanes
     const float *sc_base;
     int64_t sc_step;
-    if (lane >= 62) {
-        sc_base = a.sw[GATED ? lane - 62 : 0] + (int64_t)nb * KB;
+    const float *const sw_base = a.sw[GATED && (lane & 1)] + (int64_t)nb * KB;
+    if (SC == 1 && lane >= SW) {
+        sc_base = sw_base;
         sc_step = 1;
     } else {
         sc_base = a.sx + min(lane, M - 1);
@@ -174,6 +179,8 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
                 copy16_buf_to_lds<0>(rw[s], vo[p & 1] + (uint32_t)(p * 8 * K), kk);
             }
         copy4_to_lds(sc_base + u * sc_step, at + XB + SIDES * RB * 2048);
+        if (SC == 2)
+            copy4_to_lds(sw_base + u, at + XB + SIDES * RB * 2048 + 256);
     };
     auto compute = [&](int d) __attribute__((always_inline)) {
         const uint8_t *at = own + d * STAGE;
@@ -191,7 +198,7 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
         }
 #pragma unroll
         for (int s = 0; s < SIDES; ++s) {
-            const float sw = sc[62 + s];
+            const float sw = sc[SW + s];
 #pragma unroll
             for (int i = 0; i < RB; ++i) {
                 const v8i wf = frag(at + XB + (s * RB + i) * 2048, fo0, fo1);
@@ -299,7 +306,7 @@ template <bool GATED, int RB, int MB, bool HALF>
 void launch_few(const F8Args &a, const F8Few &f, hipStream_t st)
 {
     // stages as many as about LDS bytes hold
-    constexpr int STAGE = (HALF ? 1024 : MB * 2048) + (GATED ? 2 : 1) * RB * 2048 + 256;
+    constexpr int STAGE = (HALF ? 1024 : MB * 2048) + (GATED ? 2 : 1) * RB * 2048 + (MB <= 3 ? 256 : 512);
     constexpr int D = F8_FEW_LDS / (FW * STAGE) < 8 ? F8_FEW_LDS / (FW * STAGE) < 2 ? 2 : F8_FEW_LDS / (FW * STAGE) : 8;
     const dim3 grid((unsigned)((a.N + 16 * RB - 1) / (16 * RB)), (unsigned)f.splits);
     hipLaunchKernelGGL((f8_few_kernel<GATED, RB, MB, HALF, D>), grid, dim3(64 * FW), 0, st, a, f);
@@ -312,8 +319,12 @@ void launch_tokens(const F8Args &a, const F8Few &f, hipStream_t st)
         launch_few<GATED, RB, 1, true>(a, f, st);
     else if (a.M <= 16)
         launch_few<GATED, RB, 1, false>(a, f, st);
-    else
+    else if (a.M <= 32)
         launch_few<GATED, RB, 2, false>(a, f, st);
+    else if (a.M <= 48)
+        launch_few<GATED, RB, 3, false>(a, f, st);
+    else
+        launch_few<GATED, RB, 4, false>(a, f, st);
 }
 
 template <bool GATED>

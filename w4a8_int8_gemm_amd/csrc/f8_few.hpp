@@ -10,7 +10,7 @@
 
 namespace w4a8 {
 
-constexpr int kF8FewTokens = 32;               // two blocks of 16
+constexpr int kF8FewTokens = 64;               // four blocks of 16
 
 struct F8Few {
     int blocks;                 // blocks of 16 columns a workgroup: 1 or 2
