@@ -419,7 +419,7 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
  * a block of zeros, or so small that s is below 2^-126, gets s = 0 and zero
  * codes; one that holds a value that is not finite gets s = NaN and zero
  * codes, so that its products are NaN and no other block's are.
- * M <= 2^25; K a multiple of 16 (the quantizers: of 8), K <= 2^22.
+ * M <= 2^25, N <= 2^27; K a multiple of 16 (the quantizers: of 8), K <= 2^22.
  * Code, weight, input and output buffers 16-byte aligned, scales 4-byte.
  * ------------------------------------------------------------------------ */
 

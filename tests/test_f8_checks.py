@@ -50,7 +50,8 @@ S = w.Status
     (lambda L: L.f8_gemm(A, A2, A3, A4, A5, 4, 8, (1 << 22) + 16, None, 0, None), S.ERR_SHAPE),
     (lambda L: L.f8_gemm(A, A2, A3, A4, A5, 4, -8, 128, None, 0, None), S.ERR_INVALID_ARG),
     (lambda L: L.f8_gemm(A, A2, A3, A4, A5, (1 << 25) + 1, 8, 128, None, 0, None), S.ERR_INVALID_ARG),
-    (lambda L: L.f8_gemm(A, A2, A3, A4, A5, 1 << 25, 1 << 30, 128, None, 0, None), S.ERR_SHAPE),
+    (lambda L: L.f8_gemm(A, A2, A3, A4, A5, 4, (1 << 27) + 1, 128, None, 0, None), S.ERR_INVALID_ARG),
+    (lambda L: L.f8_gemm(A, A2, A3, A4, A5, 1 << 25, 1 << 27, 128, None, 0, None), S.ERR_SHAPE),
     (lambda L: L.f8_gemm(A, None, A3, A4, A5, 4, 8, 128, None, 0, None), S.ERR_INVALID_ARG),
     (lambda L: L.f8_gemm(A, A2, A3, A4, None, 4, 8, 128, None, 0, None), S.ERR_INVALID_ARG),
     (lambda L: L.f8_gemm(A, A2, MIS, A4, A5, 4, 8, 128, None, 0, None), S.ERR_ALIGNMENT),

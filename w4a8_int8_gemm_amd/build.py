@@ -22,7 +22,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "quantize.hip", "gemm.hip", "gemm_pc.hip", "gemm_skinny.hip", "gemm_rows.hip",
            "mv.hip", "w8a16.hip", "rotary.hip", "kv4_cache.hip", "kv4_attention.hip",
-           "kv4_decode.hip", "kv4_prefill.hip", "f8_quant.hip", "f8_gemm.hip", "f8_few.hip",
+           "kv4_decode.hip", "kv4_prefill.hip", "f8_quant.hip", "f8_plan.hip", "f8_few.hip", "f8_tile.hip",
            "f8_large.hip"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

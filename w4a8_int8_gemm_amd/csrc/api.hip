@@ -216,6 +216,7 @@ uint64_t next_tag()
 // ---- 8-bit floating point
 
 constexpr int64_t kMaxRowsF8 = int64_t(1) << 25;   // rows a launch of one wavefront each can number
+constexpr int64_t kMaxColumnsF8 = int64_t(1) << 27; // columns a launch of 256 threads for 16 can
 
 // The sizes and buffers of a product's operands: x (codes, or fp16 of the
 // same alignment) with or without scales, one or two weights.
@@ -223,7 +224,7 @@ w4a8_status_t check_f8(const char *fn, const void *x, const float *sx, bool need
                        const float *sw, const void *w2, const float *sw2, bool gated, int64_t M,
                        int64_t N, int64_t K)
 {
-    if (M < 0 || N < 0 || K < 0 || M > kMaxRowsF8 || N > kMaxDim)
+    if (M < 0 || N < 0 || K < 0 || M > kMaxRowsF8 || N > kMaxColumnsF8)
         return fail(W4A8_ERR_INVALID_ARG, "%s: sizes out of range (M=%lld N=%lld K=%lld)", fn,
                     (long long)M, (long long)N, (long long)K);
     if (K == 0 || K % 16 != 0 || K > kMaxKGemm)
@@ -256,7 +257,7 @@ F8Args make_f8(const uint8_t *x, const float *sx, const uint8_t *w, const float 
     F8Args a{};
     a.x = x; a.sx = sx;
     a.w[0] = w; a.sw[0] = sw; a.w[1] = w2; a.sw[1] = sw2;
-    a.M = (int)M; a.N = (int)N; a.K = (int)K;
+    a.M = a.sm = (int)M; a.N = a.yn = (int)N; a.K = (int)K;
     return a;
 }
 

@@ -35,22 +35,42 @@ void launch_rmsnorm_quant(NormOut out, const NormArgs &a, hipStream_t st);
 
 struct F8Args {
     const uint8_t *x;           // e4m3 [M, K]
-    const float *sx;            // [ceil(K / 128), M]
+    const float *sx;            // [ceil(K / 128)] rows of M scales, sm apart
     const uint8_t *w[2];        // e4m3 [N, K]; the second (up) of the gated product only
     const float *sw[2];         // [ceil(N / 128), ceil(K / 128)]
-    uint16_t *y;                // fp16 [M, N], or null:
-    uint8_t *yq;                // e4m3 [M, N] with
-    float *ys;                  // scales [ceil(N / 128), M]
+    uint16_t *y;                // fp16, rows of N values yn apart, or null:
+    uint8_t *yq;                // e4m3, likewise, with
+    float *ys;                  // scales [ceil(N / 128)] rows of M, sm apart
     int M, N, K;
+    int sm, yn;                 // M and N of the whole call, of which this may be a part
     int gelu;                   // the gated product's activation: 0 silu, 1 gelu (tanh form)
     int num_cu;
 };
-// The kernel for the sizes: the simple one, for few tokens (with a workspace of
-// f8_workspace() bytes and the call's tag among its counters), for large outputs.
+
+// What several workgroups of one launch leave for the last of them: sums of 128
+// columns in f8_few.hip's and f8_tile.hip's kernels.
+struct F8Parts {
+    int splits;                 // ranges of K
+    uint64_t tag;               // of the call among the counters
+    uint64_t *counters;         // one for each 128 columns, kCounterStride apart
+    float *sums;                // [ceil(N / 128)][splits][M][128]
+};
+
+// Bytes of workspace (f8_plan.hip); the product on checked arguments, by the
+// kernels that suit its sizes.
 size_t f8_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool quantize);
-size_t f8_workspace_any(int64_t M, int64_t K);     // a product's, not gated, for every N
+size_t f8_workspace_any(int64_t M, int64_t K);     // the largest of a product's, not gated, over all N
 void launch_f8(const F8Args &a, bool gated, uint64_t tag, void *workspace, hipStream_t st);
-void launch_f8_few(const F8Args &a, bool gated, uint64_t tag, void *workspace, hipStream_t st);
+
+// The kernels.  Few tokens: at most kF8FewTokens.  Tiles: kF8Tiles' shapes.
+constexpr int kF8FewTokens = 64;
+void launch_f8_few(const F8Args &a, bool gated, const F8Parts &f, hipStream_t st);
+struct F8Tile {
+    int tokens, columns;
+};
+constexpr int kF8TileShapes = 5;
+constexpr F8Tile kF8Tiles[kF8TileShapes] = {{64, 64}, {64, 128}, {96, 128}, {128, 64}, {128, 128}};
+void launch_f8_tile(const F8Args &a, bool gated, int shape, const F8Parts &f, hipStream_t st);
 void launch_f8_large(const F8Args &a, bool gated, hipStream_t st);
 
 }  // namespace w4a8

@@ -4,8 +4,8 @@
 // With few tokens a product is bound by reading its weights, so what counts is
 // how many of their bytes are on the way at any time:
 //
-//  * A workgroup owns 16 RB columns (of the gated pair: the same columns of
-//    both weights) and all tokens, and its four waves take the blocks of 128
+//  * A workgroup owns 16 columns (of the gated pair: the same columns of both
+//    weights) and all tokens, and its four waves take the blocks of 128
 //    of K in turn.  A wave copies its own blocks straight into its own part of
 //    LDS, D - 1 of them ahead of the one it multiplies: no barriers until the
 //    waves' sums meet at the end, in fixed order.  A copy takes eight whole
@@ -15,9 +15,7 @@
 //    alone do not fill the chip -- the workgroups leave fp32 sums in the
 //    workspace, and the last to arrive for 128 columns finishes them, parts in
 //    order, so that the result does not depend on who is last.
-#include "f8_few.hpp"
-#include "f8_device.hpp"
-#include "arrivals.hpp"
+#include "f8_join.hpp"
 #include "lds_copy.hpp"
 
 namespace w4a8 {
@@ -26,73 +24,10 @@ namespace {
 
 constexpr int FW = 4;                          // waves
 
-// Where a workgroup's sums go when others are needed: [128 columns' block]
-// [split][side][token][128] floats, a counter for each block before them.
-__device__ __forceinline__ float *few_slot(const F8Args &a, const F8Few &f, int nb, int split, int side, int sides)
-{
-    return f.sums + ((((int64_t)nb * f.splits + split) * sides + side) * a.M) * 128;
-}
-
-// The 128 columns of block nb from all parts: 32 lanes a token, four columns each.
-template <bool GATED>
-__device__ __forceinline__ void few_join(const F8Args &a, const F8Few &f, int nb)
-{
-    const int c4 = 4 * (threadIdx.x & 31);
-    const int sides = GATED && f.splits > 1 ? 2 : 1;
-    const int n = nb * 128 + c4;
-    for (int m = threadIdx.x >> 5; m < a.M; m += 8) {
-        float v[2][4] = {};
-        if (n < a.N) {
-            for (int p = 0; p < f.splits; ++p)
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    if (s < sides) {
-                        const float *src = few_slot(a, f, nb, p, s, sides) + m * 128 + c4;
-                        const float2 x = load_shared(src), y = load_shared(src + 2);
-                        v[s][0] += x.x, v[s][1] += x.y, v[s][2] += y.x, v[s][3] += y.y;
-                    }
-        }
-        if (GATED && sides == 2)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                v[0][r] = f8_activation(v[0][r], a.gelu) * v[1][r];
-        if (!GATED || a.y) {
-            uint16_t *p = a.y + (int64_t)m * a.N + n;
-            if (n + 4 <= a.N && (a.N & 3) == 0)
-                *reinterpret_cast<uint2 *>(p) = make_uint2(pack_h2(v[0][0], v[0][1]), pack_h2(v[0][2], v[0][3]));
-            else
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (n + r < a.N)
-                        p[r] = f2h(v[0][r]);
-            continue;
-        }
-        uint32_t t = 0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            t = max(t, n + r < a.N ? abs_bits(v[0][r]) : 0u);
-        t = group_max_u32<16>(t);
-        t = max(t, (uint32_t)__shfl_xor((int)t, 16));
-        float s, r;
-        f8_block_scale(t, s, r);
-        if (c4 == 0)
-            a.ys[(int64_t)nb * a.M + m] = s;
-        const uint32_t d = f8_codes4(v[0][0], v[0][1], v[0][2], v[0][3], s, r);
-        uint8_t *p = a.yq + (int64_t)m * a.N + n;
-        if (n + 4 <= a.N && (a.N & 3) == 0)
-            *reinterpret_cast<uint32_t *>(p) = d;
-        else
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (n + e < a.N)
-                    p[e] = (uint8_t)(d >> (8 * e));
-    }
-}
-
 // MB blocks of 16 tokens; HALF: at most 8 tokens, of which only as many rows
 // are copied (the other rows of the block repeat them and are dropped).
-template <bool GATED, int RB, int MB, bool HALF, int D>
-__global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
+template <bool GATED, int MB, bool HALF, int D>
+__global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Parts f)
 {
     constexpr int SIDES = GATED ? 2 : 1;
     constexpr int XB = HALF ? 1024 : MB * 2048;
@@ -100,9 +35,9 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
     // where the tokens need all lanes a copy of their own for the weights'
     constexpr int SC = MB <= 3 ? 1 : 2;
     constexpr int SW = MB <= 3 ? 62 : 64;                   // where the weights' lie
-    constexpr int STAGE = XB + SIDES * RB * 2048 + SC * 256;
-    constexpr int NI = XB / 1024 + SIDES * RB * 2 + SC;     // copies of a stage
-    constexpr int BLOCKS = SIDES * RB * MB;
+    constexpr int STAGE = XB + SIDES * 2048 + SC * 256;
+    constexpr int NI = XB / 1024 + SIDES * 2 + SC;     // copies of a stage
+    constexpr int BLOCKS = SIDES * MB;
     constexpr int RED = FW * BLOCKS * 1024;
     constexpr int RING = FW * D * STAGE;
     static_assert((D - 1) * NI < 64, "vmcnt range");
@@ -114,7 +49,7 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
     const int KB = (K + 127) >> 7;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int n0 = (int)blockIdx.x * 16 * RB, nb = n0 >> 7;
+    const int n0 = (int)blockIdx.x * 16, nb = n0 >> 7;
     const int split = (int)blockIdx.y;
     const bool shared = f.splits > 1 || (GATED && !a.y);    // the result is finished by the last workgroup
     if (shared && threadIdx.x == 0)
@@ -131,7 +66,7 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
     v4i rw[SIDES];
 #pragma unroll
     for (int s = 0; s < SIDES; ++s)
-        rw[s] = make_rsrc(a.w[s] + (int64_t)n0 * K, (uint32_t)(min(16 * RB, N - n0) * K));
+        rw[s] = make_rsrc(a.w[s] + (int64_t)n0 * K, (uint32_t)(min(16, N - n0) * K));
     uint8_t *const own = lds + wave * D * STAGE;
     const uint32_t own_at = (uint32_t)__builtin_amdgcn_readfirstlane((int)lds_addr(own));
     // the lane's scale of a stage: tokens first, the weights' in the last lanes
@@ -143,7 +78,7 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
         sc_step = 1;
     } else {
         sc_base = a.sx + min(lane, M - 1);
-        sc_step = M;
+        sc_step = a.sm;
     }
 
     const int lr = lane & 15, lh = lane >> 4;
@@ -153,7 +88,7 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
     const int hr = lr & 7;
     const int ho0 = hr * 128 + 16 * (c0 ^ hr), ho1 = hr * 128 + 16 * ((c0 ^ 1) ^ hr);
 
-    float acc[SIDES][RB][MB][4] = {};
+    float acc[SIDES][MB][4] = {};
 
     auto copy = [&](int d, int t) __attribute__((always_inline)) {
         const bool live = t < nt;
@@ -174,13 +109,13 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
 #pragma unroll
         for (int s = 0; s < SIDES; ++s)
 #pragma unroll
-            for (int p = 0; p < 2 * RB; ++p) {
-                set_m0(at + XB + (s * 2 * RB + p) * 1024);
+            for (int p = 0; p < 2; ++p) {
+                set_m0(at + XB + (s * 2 + p) * 1024);
                 copy16_buf_to_lds<0>(rw[s], vo[p & 1] + (uint32_t)(p * 8 * K), kk);
             }
-        copy4_to_lds(sc_base + u * sc_step, at + XB + SIDES * RB * 2048);
+        copy4_to_lds(sc_base + u * sc_step, at + XB + SIDES * 2048);
         if (SC == 2)
-            copy4_to_lds(sw_base + u, at + XB + SIDES * RB * 2048 + 256);
+            copy4_to_lds(sw_base + u, at + XB + SIDES * 2048 + 256);
     };
     auto compute = [&](int d) __attribute__((always_inline)) {
         const uint8_t *at = own + d * STAGE;
@@ -188,7 +123,7 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
             const v4i x = *reinterpret_cast<const v4i *>(p + o0), y = *reinterpret_cast<const v4i *>(p + o1);
             return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
         };
-        const float *sc = reinterpret_cast<const float *>(at + XB + SIDES * RB * 2048);
+        const float *sc = reinterpret_cast<const float *>(at + XB + SIDES * 2048);
         v8i xf[MB];
         float sx[MB];
 #pragma unroll
@@ -199,17 +134,14 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
 #pragma unroll
         for (int s = 0; s < SIDES; ++s) {
             const float sw = sc[SW + s];
+            const v8i wf = frag(at + XB + s * 2048, fo0, fo1);
 #pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const v8i wf = frag(at + XB + (s * RB + i) * 2048, fo0, fo1);
+            for (int j = 0; j < MB; ++j) {
+                const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[j], v4f{0, 0, 0, 0},
+                                                                               0, 0, 0, 0, 0, 0);
 #pragma unroll
-                for (int j = 0; j < MB; ++j) {
-                    const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf, xf[j], v4f{0, 0, 0, 0},
-                                                                                   0, 0, 0, 0, 0, 0);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[s][i][j][r] = fmaf(p[r], sx[j] * sw, acc[s][i][j][r]);
-                }
+                for (int r = 0; r < 4; ++r)
+                    acc[s][j][r] = fmaf(p[r], sx[j] * sw, acc[s][j][r]);
             }
         }
     };
@@ -236,25 +168,21 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
         if (t + d < nt)
             compute(d);
 
-    // the waves' sums meet in LDS; wave w finishes the blocks i % 4 == w
+    // the waves' sums meet in LDS; wave w finishes the tokens 16 w .. + 15
     lds_barrier();                                    // every wave is done with its stages
     v4f *red = reinterpret_cast<v4f *>(lds);
 #pragma unroll
     for (int s = 0; s < SIDES; ++s)
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < MB; ++j)
-                red[(wave * BLOCKS + (s * RB + i) * MB + j) * 64 + lane] =
-                    v4f{acc[s][i][j][0], acc[s][i][j][1], acc[s][i][j][2], acc[s][i][j][3]};
+        for (int j = 0; j < MB; ++j)
+            red[(wave * BLOCKS + s * MB + j) * 64 + lane] = v4f{acc[s][j][0], acc[s][j][1], acc[s][j][2], acc[s][j][3]};
     lds_barrier();
-    const int sides = GATED && f.splits > 1 ? 2 : 1;
-    for (int q = wave; q < RB * MB; q += FW) {
-        const int i = q / MB, j = q % MB;
+    const int m = 16 * wave + lr, n = n0 + 4 * lh;
+    if (wave < MB && m < M && n < N) {
         v4f v[SIDES];
 #pragma unroll
         for (int s = 0; s < SIDES; ++s) {
-            const int b = (s * RB + i) * MB + j;
+            const int b = s * MB + wave;
             v[s] = red[b * 64 + lane];
 #pragma unroll
             for (int y = 1; y < FW; ++y) {
@@ -262,92 +190,85 @@ __global__ __launch_bounds__(64 * FW) void f8_few_kernel(F8Args a, F8Few f)
                 v[s] = v4f{v[s][0] + u[0], v[s][1] + u[1], v[s][2] + u[2], v[s][3] + u[3]};
             }
         }
-        const int m = 16 * j + lr, n = n0 + 16 * i + 4 * lh;
-        if (m >= M || n >= N)
-            continue;
         if constexpr (GATED) {
-            if (sides == 1)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    v[0][r] = f8_activation(v[0][r], a.gelu) * v[1][r];
-        }
-        if (shared) {
-            for (int s = 0; s < sides; ++s) {
-                float *dst = few_slot(a, f, nb, split, s, sides) + m * 128 + (n & 127);
-                const v4f u = s == 0 ? v[0] : v[SIDES - 1];
-                store_shared(dst, u[0], u[1]);
-                store_shared(dst + 2, u[2], u[3]);
-            }
-            continue;
-        }
-        uint16_t *p = a.y + (int64_t)m * N + n;
-        if (n + 4 <= N && (N & 3) == 0)
-            *reinterpret_cast<uint2 *>(p) = make_uint2(pack_h2(v[0][0], v[0][1]), pack_h2(v[0][2], v[0][3]));
-        else
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                if (n + r < N)
-                    p[r] = f2h(v[0][r]);
+                v[0][r] = f8_activation(v[0][r], a.gelu) * v[1][r];
+        }
+        if (shared) {
+            float *dst = f8_slot(a, f, nb, split) + m * 128 + (n & 127);
+            store_shared(dst, v[0][0], v[0][1]);
+            store_shared(dst + 2, v[0][2], v[0][3]);
+        } else {
+            uint16_t *p = a.y + (int64_t)m * a.yn + n;
+            if (n + 4 <= N && (a.yn & 3) == 0)
+                *reinterpret_cast<uint2 *>(p) = make_uint2(pack_h2(v[0][0], v[0][1]), pack_h2(v[0][2], v[0][3]));
+            else
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (n + r < N)
+                        p[r] = f2h(v[0][r]);
+        }
     }
     if (!shared)
         return;
     __builtin_amdgcn_s_waitcnt(0);                    // this wave's stores are complete
     __syncthreads();
     if (threadIdx.x == 0) {
-        const int chunks = (min(128, N - nb * 128) + 16 * RB - 1) / (16 * RB);
+        const int chunks = (min(128, N - nb * 128) + 15) / 16;
         last = arrive(f.counters + (int64_t)nb * kCounterStride, chunks * f.splits) ? 1 : 0;
     }
     __syncthreads();
     if (last)
-        few_join<GATED>(a, f, nb);
+        f8_join(a, f, nb);
 }
 
-template <bool GATED, int RB, int MB, bool HALF>
-void launch_few(const F8Args &a, const F8Few &f, hipStream_t st)
+template <bool GATED, int MB, bool HALF>
+void launch_few(const F8Args &a, const F8Parts &f, hipStream_t st)
 {
-    // stages as many as about LDS bytes hold
-    constexpr int STAGE = (HALF ? 1024 : MB * 2048) + (GATED ? 2 : 1) * RB * 2048 + (MB <= 3 ? 256 : 512);
-    constexpr int D = F8_FEW_LDS / (FW * STAGE) < 8 ? F8_FEW_LDS / (FW * STAGE) < 2 ? 2 : F8_FEW_LDS / (FW * STAGE) : 8;
-    const dim3 grid((unsigned)((a.N + 16 * RB - 1) / (16 * RB)), (unsigned)f.splits);
-    hipLaunchKernelGGL((f8_few_kernel<GATED, RB, MB, HALF, D>), grid, dim3(64 * FW), 0, st, a, f);
-}
-
-template <bool GATED, int RB>
-void launch_tokens(const F8Args &a, const F8Few &f, hipStream_t st)
-{
-    if (a.M <= 8)
-        launch_few<GATED, RB, 1, true>(a, f, st);
-    else if (a.M <= 16)
-        launch_few<GATED, RB, 1, false>(a, f, st);
-    else if (a.M <= 32)
-        launch_few<GATED, RB, 2, false>(a, f, st);
-    else if (a.M <= 48)
-        launch_few<GATED, RB, 3, false>(a, f, st);
+    constexpr int STAGE = (HALF ? 1024 : MB * 2048) + (GATED ? 2 : 1) * 2048 + (MB <= 3 ? 256 : 512);
+    constexpr int NI = STAGE / 1024 + (MB <= 3 ? 1 : 2);
+    // stages as many as the LDS holds of the workgroups that a compute unit gets at once
+    constexpr auto depth = [](int per_cu) {
+        int d = 156 * 1024 / per_cu / (FW * STAGE);
+        d = d < 2 ? 2 : d > 8 ? 8 : d;
+        while ((d - 1) * NI >= 64)
+            --d;
+        return d;
+    };
+    const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)f.splits);
+    const int64_t groups = (int64_t)grid.x * grid.y;
+    if (groups <= a.num_cu)
+        hipLaunchKernelGGL((f8_few_kernel<GATED, MB, HALF, depth(1)>), grid, dim3(64 * FW), 0, st, a, f);
+    else if (groups <= 2 * a.num_cu)
+        hipLaunchKernelGGL((f8_few_kernel<GATED, MB, HALF, depth(2)>), grid, dim3(64 * FW), 0, st, a, f);
     else
-        launch_few<GATED, RB, 4, false>(a, f, st);
+        hipLaunchKernelGGL((f8_few_kernel<GATED, MB, HALF, depth(3)>), grid, dim3(64 * FW), 0, st, a, f);
 }
 
 template <bool GATED>
-void launch_rows(const F8Args &a, const F8Few &f, hipStream_t st)
+void launch_tokens(const F8Args &a, const F8Parts &f, hipStream_t st)
 {
-    if (f.blocks == 1)
-        launch_tokens<GATED, 1>(a, f, st);
+    if (a.M <= 8)
+        launch_few<GATED, 1, true>(a, f, st);
+    else if (a.M <= 16)
+        launch_few<GATED, 1, false>(a, f, st);
+    else if (a.M <= 32)
+        launch_few<GATED, 2, false>(a, f, st);
+    else if (a.M <= 48)
+        launch_few<GATED, 3, false>(a, f, st);
     else
-        launch_tokens<GATED, 2>(a, f, st);
+        launch_few<GATED, 4, false>(a, f, st);
 }
 
 }  // namespace
 
-void launch_f8_few(const F8Args &a, bool gated, uint64_t tag, void *workspace, hipStream_t st)
+void launch_f8_few(const F8Args &a, bool gated, const F8Parts &f, hipStream_t st)
 {
-    F8Few f = f8_few_plan(a.M, a.N, a.K, gated, gated && !a.y);
-    f.tag = tag;
-    f.counters = static_cast<uint64_t *>(workspace);
-    f.sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + f8_few_counter_bytes(a.N));
     if (gated)
-        launch_rows<true>(a, f, st);
+        launch_tokens<true>(a, f, st);
     else
-        launch_rows<false>(a, f, st);
+        launch_tokens<false>(a, f, st);
 }
 
 }  // namespace w4a8

@@ -133,7 +133,7 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
     };
     // waves 0-3: x's scales of 64 tokens; wave 4 (and 6): the first half's of
     // w, wave 5 (and 7): the second's, in every lane
-    const int64_t sc_step = group == 0 ? M : 1;
+    const int64_t sc_step = group == 0 ? a.sm : 1;
     const uint32_t sc_mask = group == 0 ? 63 : 0;
     auto copy_scales = [&]() __attribute__((always_inline)) {
         uint32_t l = (uint32_t)lane & sc_mask;
@@ -273,7 +273,17 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
             phase_barrier();
         int m0, n0;
         tile_origin(tile, m0, n0);
-        f8_store_tile<GATED, 4, 4>(a, acc, m0 + wm * 64, n0 + group * 64, n0, 128, lane, group, wm * 64, top);
+        const int mw = m0 + wm * 64, nw = n0 + group * 64;
+        if constexpr (GATED) {
+            f8_gate(a, acc[0], acc[1]);
+            if (a.y)
+                f8_store_half(a, acc[0], mw, nw, lane);
+            else
+                f8_store_f8(a, acc[0], mw, nw, n0 >> 7, lane, group, wm * 64, top);
+        } else {
+            f8_store_half(a, acc[0], mw, nw, lane);
+            f8_store_half(a, acc[1], mw, nw + 128, lane);
+        }
     }
     wait_vmcnt<0>();                                  // no copy may still be writing LDS at the end
 }

@@ -1,0 +1,145 @@
+// Which kernels a product in 8-bit floating point runs with, by its sizes.
+#include "f8.hpp"
+#include "kv4.hpp"
+
+namespace w4a8 {
+
+namespace {
+
+// Ranges of K in the kernel for few tokens: where 16 columns a workgroup leave
+// three quarters of the chip idle, K is cut in up to four.  64 x 1024 x 14336
+// 14.5 us in one range, 11.1 in four; 1 x 256 x 14336 7.1 and 6.0; but 1 x 2560
+// x 10240 8.1 in one, 10.0 in two: the parts' meeting takes 3 to 4 us.
+int few_splits(int64_t N, int64_t K, bool gated)
+{
+    const int64_t groups = (N + 15) / 16, blocks = (K + 127) / 128;
+    if (gated || groups > 64 || blocks < 64)
+        return 1;
+    return groups > 32 ? 2 : 4;
+}
+
+bool few(int64_t M, int64_t N)
+{
+    // Above 32 tokens each workgroup's copy of x outweighs its weights: 64 x 64
+    // tiles read it a quarter as often, once there are enough of them.  64
+    // tokens: 64 tiles (4096 columns, K 4096) 12.0 us against 8.0 here, 160
+    // (10240, 2560) 13.3 against 16.8, 448 (28672, 4096) 31.8 against 50.
+    return M <= 32 || (M <= kF8FewTokens && (N + 63) / 64 < 128);
+}
+
+size_t counter_bytes(int64_t N) { return kv4_counter_bytes((N + 127) / 128, 1); }
+
+int splits_of(int64_t M, int64_t N, int64_t K, bool gated)
+{
+    return few(M, N) ? few_splits(N, K, gated) : 1;
+}
+
+// Microseconds, as a model: kernels for one to 256 tokens are bound by their
+// copies into LDS, one of 1 KiB taking 14.1 ns of a compute unit (16.3 ns a
+// workgroup where two share one), or by the latency of the stages on the way;
+// a stage of a large tile takes 0.96 to 1.1 us with the share of the chip that
+// is busy.  Fitted to 128 shapes (65 to 3000 tokens, 1024 to 14336 columns and
+// K, weights from HBM) with every kernel: the choice is 0.4 % slower than the
+// best on average, 8 % at most.
+constexpr double kStart = 5.5;
+
+double tile_time(int shape, int64_t M, int64_t N, int64_t K, bool gated, int num_cu)
+{
+    const F8Tile t = kF8Tiles[shape];
+    const int64_t stages = (K + 127) / 128;
+    const int64_t groups = ((M + t.tokens - 1) / t.tokens) * ((N + t.columns - 1) / t.columns);
+    const int copies = (t.tokens + (gated ? 2 : 1) * t.columns) / 8 + 4;
+    const int stage = (t.tokens + (gated ? 2 : 1) * t.columns) * 128 + 1024;
+    const int all = 157 * 1024 / stage, half = 78 * 1024 / stage;
+    const int deep = all < 8 ? all : 8;
+    const double alone = 0.0141 * copies, wait = 0.97 / (deep - 1);
+    if (groups <= num_cu) {
+        const double w = wait * (0.5 + 0.5 * (double)groups / num_cu);
+        return kStart + stages * (alone > w ? alone : w);
+    }
+    if (half < 2)
+        return kStart + stages * (alone > wait ? alone : wait) * ((groups + num_cu - 1) / num_cu);
+    const double two = 2 * 0.0163 * copies;
+    const int64_t rest = groups % (2 * num_cu);
+    return kStart + stages * ((groups / (2 * num_cu)) * two + (rest > num_cu ? 0.9 * two : rest > 0 ? alone : 0.0));
+}
+
+double large_time(int64_t M, int64_t N, int64_t K, bool gated, int num_cu)
+{
+    const int64_t tiles = ((M + 255) / 256) * ((N + (gated ? 127 : 255)) / (gated ? 128 : 256));
+    const int64_t rounds = (tiles + num_cu - 1) / num_cu;
+    return kStart + rounds * (((K + 127) / 128) * (0.96 + 0.15 * (double)tiles / ((double)num_cu * rounds)) + 2.7);
+}
+
+// The best tile shape, or kF8TileShapes for the large kernel.
+int best_shape(int64_t M, int64_t N, int64_t K, bool gated, bool quantize, int num_cu, double *time)
+{
+    int best = kF8TileShapes;
+    *time = large_time(M, N, K, gated, num_cu);
+    for (int i = 0; i < kF8TileShapes; ++i) {
+        // e4m3 output: a workgroup holds the 128 columns of a scale (64 tokens
+        // and fewer can meet in the workspace)
+        if (quantize && kF8Tiles[i].columns < 128)
+            continue;
+        // a launch of 2^32 threads would wrap
+        if (((M + 63) / 64) * ((N + 63) / 64) >= (1 << 24))
+            continue;
+        const double t = tile_time(i, M, N, K, gated, num_cu);
+        if (t < *time) {
+            *time = t;
+            best = i;
+        }
+    }
+    return best;
+}
+
+void launch_shape(const F8Args &a, bool gated, int shape, const F8Parts &f, hipStream_t st)
+{
+    if (shape < kF8TileShapes)
+        launch_f8_tile(a, gated, shape, f, st);
+    else
+        launch_f8_large(a, gated, st);
+}
+
+}  // namespace
+
+size_t f8_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool quantize)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || M > kF8FewTokens)
+        return 0;
+    const int splits = splits_of(M, N, K, gated);
+    if (splits == 1 && !quantize)
+        return 0;
+    return counter_bytes(N) + (size_t)((N + 127) / 128) * splits * (size_t)M * 128 * sizeof(float);
+}
+
+size_t f8_workspace_any(int64_t M, int64_t K)
+{
+    size_t most = 0;
+    for (int64_t N : {512, 1024})                  // the widest outputs cut in four and in two
+        most = f8_workspace(M, N, K, false, false) > most ? f8_workspace(M, N, K, false, false) : most;
+    return most;
+}
+
+void launch_f8(const F8Args &a, bool gated, uint64_t tag, void *workspace, hipStream_t st)
+{
+    const bool quantize = gated && !a.y;
+    F8Parts f;
+    f.splits = splits_of(a.M, a.N, a.K, gated);
+    f.tag = tag;
+    f.counters = static_cast<uint64_t *>(workspace);
+    f.sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + counter_bytes(a.N));
+    if (few(a.M, a.N)) {
+        launch_f8_few(a, gated, f, st);
+        return;
+    }
+    if (a.M <= kF8FewTokens) {
+        launch_f8_tile(a, gated, 0, f, st);
+        return;
+    }
+    double time;
+    const int shape = best_shape(a.M, a.N, a.K, gated, quantize, a.num_cu, &time);
+    launch_shape(a, gated, shape, f, st);
+}
+
+}  // namespace w4a8
