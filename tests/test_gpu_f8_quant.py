@@ -242,3 +242,19 @@ def test_empty_and_other_streams(torch_gpu):
     torch.cuda.current_stream().wait_stream(side)
     for a, b in zip(want, got):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_norm_of_more_rows_than_a_launch_has(torch_gpu):
+    """2^21 rows a launch; the rows behind are those of the next."""
+    import torch
+    import w4a8_int8_gemm_amd as w
+    m, k = (1 << 21) + 3, 16
+    x = torch.zeros(m, k, dtype=torch.float16, device="cuda")
+    x[-5:] = torch.arange(1, 81, device="cuda").view(5, 16).half()
+    gain = torch.ones(k, dtype=torch.float16, device="cuda")
+    for mode in (w.Mode.F8, w.Mode.W8A8_PC):
+        q, s = w.rmsnorm_quant(mode, x, gain)
+        a, b = w.rmsnorm_quant(mode, x[-5:].contiguous(), gain)
+        assert torch.equal(q[-5:].view(torch.uint8), a.view(torch.uint8))
+        assert torch.equal(s.flatten()[-5:], b.flatten())
+        assert not q[:-5].view(torch.uint8).any() and not s.flatten()[:-5].any()

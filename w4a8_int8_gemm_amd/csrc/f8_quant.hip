@@ -115,9 +115,180 @@ __device__ __forceinline__ uint32_t int8_codes4(const float *v, float s, float r
     return pack_i8x4(c[0], c[1], c[2], c[3]);
 }
 
-// One wavefront a row, the row read three times (from cache after the first).
+// x + residual in fp32.
+__device__ __forceinline__ Eight norm_sum(uint4 x, uint4 r)
+{
+    Eight h = widen(x);
+    const Eight t = widen(r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        h.v[i] += t.v[i];
+    return h;
+}
+
+__device__ __forceinline__ void norm_squares(const Eight &h, float &ss)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        ss = fmaf(h.v[i], h.v[i], ss);
+}
+
+// 1 / sqrt(mean of the squares + eps); 0 for a row of zeros, whose values are zero with any eps.
+__device__ __forceinline__ float norm_inverse(float ss, int K, float eps)
+{
+    return ss == 0.0f ? 0.0f : 1.0f / sqrtf(ss / (float)K + eps);
+}
+
+__device__ __forceinline__ Eight norm_value(const Eight &h, uint4 gain, float inv)
+{
+    const Eight g = widen(gain);
+    Eight y;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        y.v[i] = (h.v[i] * inv) * g.v[i];
+    return y;
+}
+
+// The largest |v| as bits; a row whose squares' sum is not finite gives NaN.
+__device__ __forceinline__ uint32_t norm_largest(const Eight &y, bool finite)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = max(m, abs_bits(y.v[i]));
+    return finite ? m : 0x7fc00000u;
+}
+
+template <NormOut OUT> __device__ __forceinline__ void norm_scale(uint32_t m, float &s, float &r)
+{
+    if (OUT == NormOut::F8) {
+        f8_block_scale(m, s, r);
+        return;
+    }
+    s = m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(m) / 127.0f;
+    s = s < 0x1p-126f ? 0.0f : s;
+    r = s > 0.0f ? 1.0f / s : 0.0f;
+}
+
+template <NormOut OUT> __device__ __forceinline__ uint2 norm_codes(const Eight &y, float s, float r)
+{
+    if (OUT == NormOut::F8)
+        return make_uint2(f8_codes4(y.v[0], y.v[1], y.v[2], y.v[3], s, r),
+                          f8_codes4(y.v[4], y.v[5], y.v[6], y.v[7], s, r));
+    return make_uint2(int8_codes4(y.v, s, r), int8_codes4(y.v + 4, s, r));
+}
+
+// Lanes that own a slice (eight values a lane), and where its scale goes.
+template <NormOut OUT> constexpr int kSliceLanes = OUT == NormOut::INT8_64 ? 8 : 16;
+template <NormOut OUT> __device__ __forceinline__ float *norm_scale_at(const NormArgs &a, int64_t row, int chunk)
+{
+    const int g = chunk / kSliceLanes<OUT>;
+    return a.scale + (OUT == NormOut::F8 ? (int64_t)g * a.M + row : row * (int64_t)(a.K / (8 * kSliceLanes<OUT>)) + g);
+}
+
+__device__ __forceinline__ void norm_store_sum(const NormArgs &a, int64_t row, int c, const Eight &h)
+{
+    if (a.sum)
+        reinterpret_cast<uint4 *>(a.sum + row * (int64_t)a.K)[c] =
+            make_uint4(pack_h2(h.v[0], h.v[1]), pack_h2(h.v[2], h.v[3]), pack_h2(h.v[4], h.v[5]),
+                       pack_h2(h.v[6], h.v[7]));
+}
+
+// A workgroup a row, as many waves as it fills with CPL chunks of eight values
+// a lane, all in registers: the row is read once.  Its sum of squares and, for
+// int8 rows, its largest value meet over the lanes and then in LDS.
+//
+// Bound by memory: 7 bytes a value with a residual, 3 without, of which 4516 x
+// 4096 take 28.0 us (4.6 TB/s; a copy of 2 GiB runs at 4.95) and 19.3 (2.9, with
+// the vector unit about half busy).  Four waves a row in registers against one
+// wave a row that reads it again for each step: 40.4 and 19.8 us, and 1 x 4096
+// 9.3 against 3.5.
+constexpr int kNormWaves = 16;
+template <NormOut OUT, int CPL>
+__global__ __launch_bounds__(64 * kNormWaves) void rmsnorm_quant_kernel(NormArgs a, int64_t first_row)
+{
+    __shared__ float sums[kNormWaves];
+    __shared__ uint32_t tops[kNormWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = (int)blockDim.x >> 6;
+    const int64_t row = first_row + blockIdx.x;
+    const int K = a.K, nch = K >> 3;
+    const int first = (int)threadIdx.x;                    // chunk j of the lane: first + 64 waves j
+    const uint4 *xr = reinterpret_cast<const uint4 *>(a.x + row * (int64_t)K);
+    const uint4 *gr = reinterpret_cast<const uint4 *>(a.gain);
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    Eight h[CPL];
+    float ss = 0.0f;
+    {
+        uint4 x[CPL], r[CPL];
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const int c = first + 64 * waves * j;
+            x[j] = c < nch ? load_nt(xr + c) : none;
+            r[j] = none;
+        }
+        if (a.residual) {
+            const uint4 *rr = reinterpret_cast<const uint4 *>(a.residual + row * (int64_t)K);
+#pragma unroll
+            for (int j = 0; j < CPL; ++j) {
+                const int c = first + 64 * waves * j;
+                r[j] = c < nch ? load_nt(rr + c) : none;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            h[j] = norm_sum(x[j], r[j]);
+            norm_squares(h[j], ss);
+        }
+    }
+    ss = wave_sum(ss);
+    if (lane == 0)
+        sums[wave] = ss;
+    __syncthreads();
+    ss = sums[0];
+    for (int i = 1; i < waves; ++i)
+        ss += sums[i];
+    const float inv = norm_inverse(ss, K, a.eps);
+    const bool finite = ss < INFINITY;
+    float s = 0.0f, r = 0.0f;
+    if (OUT == NormOut::INT8_ROW) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+            const int c = first + 64 * waves * j;
+            if (c < nch)
+                norm_store_sum(a, row, c, h[j]);
+            h[j] = norm_value(h[j], c < nch ? gr[c] : none, inv);
+            top = max(top, norm_largest(h[j], finite));
+        }
+        top = group_max_u32<64>(top);
+        if (lane == 0)
+            tops[wave] = top;
+        __syncthreads();
+        for (int i = 0; i < waves; ++i)
+            top = max(top, tops[i]);
+        norm_scale<OUT>(top, s, r);
+        if (threadIdx.x == 0)
+            a.scale[row] = s;
+    }
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+        const int c = first + 64 * waves * j;
+        if (OUT != NormOut::INT8_ROW) {
+            if (c < nch)
+                norm_store_sum(a, row, c, h[j]);
+            h[j] = norm_value(h[j], c < nch ? gr[c] : none, inv);
+            norm_scale<OUT>(group_max_u32<kSliceLanes<OUT>>(norm_largest(h[j], finite)), s, r);
+            if (c < nch && lane % kSliceLanes<OUT> == 0)
+                *norm_scale_at<OUT>(a, row, c) = s;
+        }
+        if (c < nch)
+            reinterpret_cast<uint2 *>(a.q + row * (int64_t)K)[c] = norm_codes<OUT>(h[j], s, r);
+    }
+}
+
+// Longer rows: one wavefront a row, which is read again for each step (from cache).
 template <NormOut OUT>
-__global__ __launch_bounds__(256) void rmsnorm_quant_kernel(NormArgs a)
+__global__ __launch_bounds__(256) void rmsnorm_quant_long_kernel(NormArgs a)
 {
     const int lane = threadIdx.x & 63;
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -125,99 +296,70 @@ __global__ __launch_bounds__(256) void rmsnorm_quant_kernel(NormArgs a)
         return;
     const int K = a.K, nch = K >> 3;
     const uint4 *xr = reinterpret_cast<const uint4 *>(a.x + row * (int64_t)K);
-    const uint4 *rr = reinterpret_cast<const uint4 *>(a.residual + (a.residual ? row * (int64_t)K : 0));
+    const uint4 *rr = a.residual ? reinterpret_cast<const uint4 *>(a.residual + row * (int64_t)K) : nullptr;
     const uint4 *gr = reinterpret_cast<const uint4 *>(a.gain);
-    auto load = [&](int c) __attribute__((always_inline)) {
-        Eight h = widen(xr[c]);
-        if (a.residual) {
-            const Eight t = widen(rr[c]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                h.v[i] += t.v[i];
-        }
-        return h;
-    };
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    auto load = [&](int c) __attribute__((always_inline)) { return norm_sum(xr[c], rr ? rr[c] : none); };
     float ss = 0.0f;
-    for (int c = lane; c < nch; c += 64) {
-        const Eight h = load(c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            ss = fmaf(h.v[i], h.v[i], ss);
-    }
+    for (int c = lane; c < nch; c += 64)
+        norm_squares(load(c), ss);
     ss = wave_sum(ss);
-    const float inv = 1.0f / sqrtf(ss / (float)K + a.eps);
+    const float inv = norm_inverse(ss, K, a.eps);
     const bool finite = ss < INFINITY;
-    auto normed = [&](const Eight &h, int c) __attribute__((always_inline)) {
-        const Eight g = widen(gr[c]);
-        Eight y;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            y.v[i] = ss == 0.0f ? 0.0f : (h.v[i] * inv) * g.v[i];
-        return y;
-    };
-    auto largest = [&](const Eight &y) __attribute__((always_inline)) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            m = max(m, abs_bits(y.v[i]));
-        return finite ? m : 0x7fc00000u;
-    };
-    constexpr float kMax = OUT == NormOut::F8 ? kF8Max : 127.0f;
-    auto scale_of = [&](uint32_t m, float &s, float &r) __attribute__((always_inline)) {
-        if (OUT == NormOut::F8) {
-            f8_block_scale(m, s, r);
-        } else {
-            s = m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(m) / kMax;
-            s = s < 0x1p-126f ? 0.0f : s;
-            r = s > 0.0f ? 1.0f / s : 0.0f;
-        }
-    };
-    uint32_t row_max = 0;
     float s = 0.0f, r = 0.0f;
     if (OUT == NormOut::INT8_ROW) {
+        uint32_t top = 0;
         for (int c = lane; c < nch; c += 64)
-            row_max = max(row_max, largest(normed(load(c), c)));
-        scale_of(group_max_u32<64>(row_max), s, r);
+            top = max(top, norm_largest(norm_value(load(c), gr[c], inv), finite));
+        norm_scale<OUT>(group_max_u32<64>(top), s, r);
         if (lane == 0)
             a.scale[row] = s;
     }
     for (int base = 0; base < nch; base += 64) {
         const int c = base + lane;
-        const bool valid = c < nch;
         Eight h{}, y{};
-        if (valid) {
+        if (c < nch) {
             h = load(c);
-            y = normed(h, c);
+            y = norm_value(h, gr[c], inv);
         }
         if (OUT != NormOut::INT8_ROW) {
-            constexpr int kLanes = OUT == NormOut::INT8_64 ? 8 : 16;
-            scale_of(group_max_u32<kLanes>(valid ? largest(y) : 0u), s, r);
-            if (valid && lane % kLanes == 0) {
-                const int g = c / kLanes;
-                if (OUT == NormOut::F8)
-                    a.scale[(int64_t)g * a.M + row] = s;
-                else
-                    a.scale[row * (int64_t)(nch / kLanes) + g] = s;
-            }
+            norm_scale<OUT>(group_max_u32<kSliceLanes<OUT>>(norm_largest(y, finite)), s, r);
+            if (c < nch && lane % kSliceLanes<OUT> == 0)
+                *norm_scale_at<OUT>(a, row, c) = s;
         }
-        if (!valid)
-            continue;
-        uint2 codes;
-        if (OUT == NormOut::F8)
-            codes = make_uint2(f8_codes4(y.v[0], y.v[1], y.v[2], y.v[3], s, r),
-                               f8_codes4(y.v[4], y.v[5], y.v[6], y.v[7], s, r));
-        else
-            codes = make_uint2(int8_codes4(y.v, s, r), int8_codes4(y.v + 4, s, r));
-        reinterpret_cast<uint2 *>(a.q + row * (int64_t)K)[c] = codes;
-        if (a.sum)
-            reinterpret_cast<uint4 *>(a.sum + row * (int64_t)K)[c] =
-                make_uint4(pack_h2(h.v[0], h.v[1]), pack_h2(h.v[2], h.v[3]), pack_h2(h.v[4], h.v[5]),
-                           pack_h2(h.v[6], h.v[7]));
+        if (c < nch) {
+            reinterpret_cast<uint2 *>(a.q + row * (int64_t)K)[c] = norm_codes<OUT>(y, s, r);
+            norm_store_sum(a, row, c, h);
+        }
     }
 }
 
-}  // namespace
+template <NormOut OUT, int CPL> void launch_rows(const NormArgs &a, hipStream_t st)
+{
+    const unsigned waves = (a.K + 512 * CPL - 1) / (512 * CPL);
+    // a launch of 2^32 threads would wrap
+    constexpr int64_t kRowsALaunch = 1 << 21;
+    for (int64_t row = 0; row < a.M; row += kRowsALaunch) {
+        const int64_t rows = a.M - row < kRowsALaunch ? a.M - row : kRowsALaunch;
+        hipLaunchKernelGGL((rmsnorm_quant_kernel<OUT, CPL>), dim3((unsigned)rows), dim3(64 * waves), 0, st, a, row);
+    }
+}
 
+// One chunk a lane where rows are few (256 x 4096 5.3 us, with two 6.2) or
+// short (4516 x 512 6.4 and 7.1), two where there are many (4516 x 4096 30.1 and
+// 28.0, 4516 x 1024 10.8 and 10.1) or they need more than 16 waves.
+template <NormOut OUT> void launch_norm(const NormArgs &a, hipStream_t st)
+{
+    const int K = a.K;
+    if (K > 1024 * kNormWaves)
+        hipLaunchKernelGGL(rmsnorm_quant_long_kernel<OUT>, dim3((unsigned)((a.M + 3) / 4)), dim3(256), 0, st, a);
+    else if (K <= 512 || (a.M <= 1024 && K <= 512 * kNormWaves))
+        launch_rows<OUT, 1>(a, st);
+    else
+        launch_rows<OUT, 2>(a, st);
+}
+
+}  // namespace
 
 void launch_quantize_act_f8(const uint16_t *x, int64_t rows, int K, uint8_t *q, float *scale,
                             hipStream_t st)
@@ -237,12 +379,11 @@ void launch_quantize_weight_f8(const uint16_t *w, int64_t N, int K, uint8_t *q, 
 
 void launch_rmsnorm_quant(NormOut out, const NormArgs &a, hipStream_t st)
 {
-    const dim3 grid((unsigned)((a.M + 3) / 4)), block(256);
     switch (out) {
-    case NormOut::INT8_ROW: hipLaunchKernelGGL(rmsnorm_quant_kernel<NormOut::INT8_ROW>, grid, block, 0, st, a); return;
-    case NormOut::INT8_64: hipLaunchKernelGGL(rmsnorm_quant_kernel<NormOut::INT8_64>, grid, block, 0, st, a); return;
-    case NormOut::INT8_128: hipLaunchKernelGGL(rmsnorm_quant_kernel<NormOut::INT8_128>, grid, block, 0, st, a); return;
-    case NormOut::F8: hipLaunchKernelGGL(rmsnorm_quant_kernel<NormOut::F8>, grid, block, 0, st, a); return;
+    case NormOut::INT8_ROW: launch_norm<NormOut::INT8_ROW>(a, st); return;
+    case NormOut::INT8_64: launch_norm<NormOut::INT8_64>(a, st); return;
+    case NormOut::INT8_128: launch_norm<NormOut::INT8_128>(a, st); return;
+    case NormOut::F8: launch_norm<NormOut::F8>(a, st); return;
     }
 }
 
