@@ -42,6 +42,7 @@ int splits_of(int64_t M, int64_t N, int64_t K, bool gated)
 // K, weights from HBM) with every kernel: the choice is 0.4 % slower than the
 // best on average, 8 % at most.
 constexpr double kStart = 5.5;
+constexpr double kSecond = 2.0;         // what of it a second launch right behind the first does not take
 
 double tile_time(int shape, int64_t M, int64_t N, int64_t K, bool gated, int num_cu)
 {
@@ -137,9 +138,63 @@ void launch_f8(const F8Args &a, bool gated, uint64_t tag, void *workspace, hipSt
         launch_f8_tile(a, gated, 0, f, st);
         return;
     }
+    // Whole rounds of large tiles over the chip, and what is left of the tokens
+    // or of the columns by the kernel that suits it, where that is faster than
+    // a last round that leaves most of the chip idle.
     double time;
     const int shape = best_shape(a.M, a.N, a.K, gated, quantize, a.num_cu, &time);
-    launch_shape(a, gated, shape, f, st);
+    const int columns = gated ? 128 : 256;
+    const int64_t tm = (a.M + 255) / 256, tn = (a.N + columns - 1) / columns;
+    int64_t best_m = 0, best_n = 0;
+    int best_rest = 0;
+    for (int64_t rounds = tm * tn / a.num_cu; rounds > 0 && rounds >= tm * tn / a.num_cu - 1; --rounds) {
+        const int64_t rows = rounds * a.num_cu / tn, cols = rounds * a.num_cu / tm;
+        double rest;
+        if (rows > 0 && rows < tm) {
+            const int s = best_shape(a.M - 256 * rows, a.N, a.K, gated, quantize, a.num_cu, &rest);
+            rest += large_time(256 * rows, a.N, a.K, gated, a.num_cu) - kSecond;
+            if (rest < time) {
+                time = rest;
+                best_m = 256 * rows, best_n = 0, best_rest = s;
+            }
+        }
+        if (cols > 0 && cols < tn) {
+            const int s = best_shape(a.M, a.N - columns * cols, a.K, gated, quantize, a.num_cu, &rest);
+            rest += large_time(a.M, columns * cols, a.K, gated, a.num_cu) - kSecond;
+            if (rest < time) {
+                time = rest;
+                best_m = 0, best_n = columns * cols, best_rest = s;
+            }
+        }
+    }
+    if (best_m + best_n == 0) {
+        launch_shape(a, gated, shape, f, st);
+        return;
+    }
+    F8Args first = a, second = a;
+    if (best_m > 0) {
+        first.M = (int)best_m;
+        second.M = (int)(a.M - best_m);
+        second.x += best_m * a.K;
+        second.sx += best_m;
+        if (a.y)
+            second.y += best_m * a.yn;
+        else
+            second.yq += best_m * a.yn, second.ys += best_m;
+    } else {
+        first.N = (int)best_n;
+        second.N = (int)(a.N - best_n);
+        for (int i = 0; i < (gated ? 2 : 1); ++i) {
+            second.w[i] += best_n * a.K;
+            second.sw[i] += best_n / 128 * ((a.K + 127) / 128);
+        }
+        if (a.y)
+            second.y += best_n;
+        else
+            second.yq += best_n, second.ys += best_n / 128 * a.sm;
+    }
+    launch_f8_large(first, gated, st);
+    launch_shape(second, gated, best_rest, f, st);
 }
 
 }  // namespace w4a8
