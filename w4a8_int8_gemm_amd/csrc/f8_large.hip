@@ -13,20 +13,15 @@ constexpr int LBM = 256, LBN = 256;            // tokens and weight rows of a ti
 constexpr int LXB = LBM * 128, LWB = LBN * 128;
 constexpr int LSB = LXB + LWB;                 // 64 KiB a stage of 128 bytes of K; two stages
 
-// Workgroup barrier without waits or fences of its own: the kernel waits for
-// its LDS reads and copies before it.
-__device__ __forceinline__ void phase_barrier()
+// Workgroup barrier without waits of its own: the kernel waits for its copies
+// before it, and what it has read is used before the place is copied over.
+__device__ __forceinline__ void stage_barrier()
 {
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-}
-
-__device__ __forceinline__ void wait_lds()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));   // lgkmcnt(0)
-    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
 }
 
 // At most N of the wave's copies may still be on their way.
@@ -37,7 +32,7 @@ template <int N> __device__ __forceinline__ void wait_copies()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <bool GATED>
+template <bool GATED, bool TAIL>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
 {
@@ -107,29 +102,34 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
             set_tile();
         }
     };
-    // A lane's offset in a block of even (par 0) or odd number; chunks past the
-    // row's end (the last stage of a K that 128 does not divide) read zeros.
-    // Formed each time, not kept in registers.
-    auto lane_offset = [&](int par, int k0) __attribute__((always_inline)) {
-        int ch = chunk0;
-        asm volatile("" : "+v"(ch));
-        const int c = ch ^ (16 * par);
-        return (uint32_t)((lane >> 3) * K + c) | (k0 + c >= K ? 0x80000000u : 0u);
+    // The lane's offsets of the wave's four blocks of x and two of each half of
+    // w.  TAIL (128 does not divide K): chunks past the row's end in the last
+    // stage read zeros, by an offset past the resource.
+    uint32_t xo[4], wo[2], past[2] = {0, 0};
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        xo[p] = (uint32_t)((wave * 32 + p * 8 + (lane >> 3)) * K + (chunk0 ^ (16 * (p & 1))));
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+        wo[p] = (uint32_t)((wave * 16 + p * 8 + (lane >> 3)) * K + (chunk0 ^ (16 * p)));
+    if (TAIL)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            past[p] = (chunk0 ^ (16 * p)) >= (K & 127) ? 0x80000000u : 0u;
+    auto copy16 = [&](v4i r, uint32_t at, uint32_t offset, int par, int stage) __attribute__((always_inline)) {
+        set_m0(at);
+        if (TAIL)
+            offset |= stage == KB - 1 ? past[par] : 0u;
+        copy16_buf_to_lds<0>(r, offset, (uint32_t)(stage * 128));
     };
     auto copy_x = [&](int p) __attribute__((always_inline)) {         // p = 0 .. 3
-        const int blk = wave * 4 + p, k0 = cur_s * 128;
-        set_m0(ring_at + cur_buf * LSB + blk * 1024);
-        copy16_buf_to_lds<0>(rx, lane_offset(p & 1, k0) + (uint32_t)(blk * 8 * K), (uint32_t)k0);
+        copy16(rx, ring_at + cur_buf * LSB + (wave * 4 + p) * 1024, xo[p], p & 1, cur_s);
     };
     auto copy_w0 = [&](int p) __attribute__((always_inline)) {        // p = 0, 1
-        const int blk = wave * 2 + p, k0 = cur_s * 128;
-        set_m0(ring_at + cur_buf * LSB + LXB + blk * 1024);
-        copy16_buf_to_lds<0>(rw0, lane_offset(p, k0) + (uint32_t)(blk * 8 * K), (uint32_t)k0);
+        copy16(rw0, ring_at + cur_buf * LSB + LXB + (wave * 2 + p) * 1024, wo[p], p, cur_s);
     };
     auto copy_w1 = [&](int p) __attribute__((always_inline)) {        // of the stage before the cursor's
-        const int blk = wave * 2 + p, k0 = w1_s * 128;
-        set_m0(ring_at + (cur_buf ^ 1) * LSB + LXB + 16384 + blk * 1024);
-        copy16_buf_to_lds<0>(rw1_now, lane_offset(p, k0) + (uint32_t)(blk * 8 * K), (uint32_t)k0);
+        copy16(rw1_now, ring_at + (cur_buf ^ 1) * LSB + LXB + 16384 + (wave * 2 + p) * 1024, wo[p], p, w1_s);
     };
     // waves 0-3: x's scales of 64 tokens; wave 4 (and 6): the first half's of
     // w, wave 5 (and 7): the second's, in every lane
@@ -143,49 +143,102 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
     };
 
     // ---- fragments: lane l reads row l % 16; of the eight 16-byte chunks of a
-    // stage lane group h takes 0 1, 2 3, 5 4, 7 6
+    // stage lane group h takes 0 1, 2 3, 5 4, 7 6.  One LDS address for each of
+    // a lane's two chunks, turned to the other buffer each stage; rows and
+    // halves are immediate offsets.
     const int lr = lane & 15, lh = lane >> 4;
     const int c0 = lh == 0 ? 0 : lh == 1 ? 2 : lh == 2 ? 5 : 7;
     const int sw8 = (lr & 7) ^ (lr >> 3);
-    const int fo0 = lr * 128 + 16 * (c0 ^ sw8), fo1 = lr * 128 + 16 * ((c0 ^ 1) ^ sw8);
-    auto read_frag = [&](const uint8_t *rows) __attribute__((always_inline)) {
-        const v4i p = *reinterpret_cast<const v4i *>(rows + fo0), q = *reinterpret_cast<const v4i *>(rows + fo1);
-        return __builtin_shufflevector(p, q, 0, 1, 2, 3, 4, 5, 6, 7);
+    typedef __attribute__((address_space(3))) const uint8_t lds_bytes;
+    typedef __attribute__((address_space(3))) const v4i lds_v4i;
+    typedef __attribute__((address_space(3))) const float lds_float;
+    uint32_t xa[2], wa[2], sa = scales_at + (uint32_t)(wm * 64 + lr) * 4, ga = scales_at + 1024;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const uint32_t in = (uint32_t)(lr * 128 + 16 * ((c0 ^ q) ^ sw8));
+        xa[q] = ring_at + wm * 8192 + in;
+        wa[q] = ring_at + LXB + group * 8192 + in;
+    }
+    auto read16 = [&](uint32_t at, int offset) __attribute__((always_inline)) {
+        return *reinterpret_cast<lds_v4i *>(reinterpret_cast<lds_bytes *>(at) + offset);
+    };
+    auto read_frag = [&](const uint32_t (&at)[2], int offset) __attribute__((always_inline)) {
+        return __builtin_shufflevector(read16(at[0], offset), read16(at[1], offset), 0, 1, 2, 3, 4, 5, 6, 7);
     };
 
     float acc[2][4][4][4];
     v8i xf[4], wf[4];
     v4f pr[4];
-    float sc[2][4];
+    float sc[2][4], sx[4], sw[2];
+    auto read_float = [&](uint32_t at, int offset) __attribute__((always_inline)) {
+        return *reinterpret_cast<lds_float *>(reinterpret_cast<lds_bytes *>(at) + offset);
+    };
+    auto read_scales = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            sx[j] = read_float(sa, 64 * j);
+        sw[0] = read_float(ga, 0);
+        sw[1] = read_float(ga, 256);
+    };
+    uint32_t to_ring = LSB, to_scales = 2048;         // from this buffer to the other
 
-    // sixteen products of one half, each folded three products later; `copy`
-    // runs between them
-    auto compute = [&](auto HALF, auto copy) __attribute__((always_inline)) {
+    // Product t = 0 .. 31 of a stage: half t / 16 of w, its block t / 4 % 4, x's
+    // block t % 4.  Each is folded three products later, the last three in the
+    // stage that follows.
+    auto fold = [&](int u) __attribute__((always_inline)) {
+        const int h = u >> 4, i = (u >> 2) & 3, j = u & 3;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            acc[h][i][j][r] = fmaf(pr[j][r], sc[h][j], acc[h][i][j][r]);
+    };
+    auto half = [&](auto HALF) __attribute__((always_inline)) {
         constexpr int h = decltype(HALF)::value;
 #pragma unroll
-        for (int t = 0; t < 16 + 3; ++t) {
-            if (t < 16)
-                pr[t & 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[t >> 2], xf[t & 3], v4f{0, 0, 0, 0},
-                                                                             0, 0, 0, 0, 0, 0);
+        for (int q = 0; q < 16; ++q) {
+            const int t = 16 * h + q, i = q >> 2, j = q & 3;
+            v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wf[i], xf[j], v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
-            if (t >= 3) {
-                const int u = t - 3;
+            fold((t + 29) & 31);
+            pr[j] = p;
+            // what the products no longer need makes room for what comes next
+            if (h == 0) {
+                if (j == 3)
+                    wf[i] = read_frag(wa, 16384 + 2048 * i);
+                if (q == 3) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    acc[h][u >> 2][u & 3][r] = fmaf(pr[u & 3][r], sc[h][u & 3], acc[h][u >> 2][u & 3][r]);
+                    for (int k = 0; k < 4; ++k)
+                        sc[1][k] = sx[k] * sw[1];
+                }
+                if (q == 1 || q == 9)
+                    copy_w1(q >> 3);
+            } else {
+                if (j == 3)
+                    wf[i] = read_frag(wa, 2048 * i);
+                if (i == 3)
+                    xf[j] = read_frag(xa, 2048 * j);
+                if (q == 0)
+                    read_scales();
+                if (q % 2 == 1 && q < 8)
+                    copy_x(q >> 1);
+                if (q == 9 || q == 11)
+                    copy_w0((q - 9) >> 1);
+                if (q == 13)
+                    copy_scales();
             }
-            if (t < 16)
-                copy(t);
             __builtin_amdgcn_sched_barrier(0);
         }
-        // the sums are formed here, not where the compiler next needs them
+    };
+    // the sums are formed here, not where the compiler next needs them
+    auto settle = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float *v = acc[h][i][j];
-                asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]));
-            }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float *v = acc[h][i][j];
+                    asm volatile("" : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]));
+                }
     };
 
     set_tile();
@@ -205,8 +258,13 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
     copy_w0(1);
     copy_scales();
     wait_vmcnt<9>();                                  // the first stage's x, w0 and scales
-    phase_barrier();
-    int b = 0;
+    stage_barrier();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        xf[i] = read_frag(xa, 2048 * i);
+        wf[i] = read_frag(wa, 2048 * i);
+    }
+    read_scales();
     for (int tile = wl; tile < total; tile += G) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -217,60 +275,31 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         acc[h][i][j][r] = 0.0f;
-        if (group == 1)
-            phase_barrier();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            pr[j] = v4f{0, 0, 0, 0};
+            sc[1][j] = 0.0f;
+        }
 #pragma clang loop unroll(disable)
         for (int s = 0; s < KB; ++s) {
-            const uint8_t *buf = ring + b * LSB;
-            const uint8_t *xb = buf + wm * 64 * 128, *wb = buf + LXB + group * 64 * 128;
-            float sx[4], sw[2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                xf[i] = read_frag(xb + i * 2048);
-                wf[i] = read_frag(wb + i * 2048);
-            }
+            wait_copies<7>();                         // this stage's second half of w
+            stage_barrier();
+            advance();
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                sx[j] = scales[b][0][wm * 64 + 16 * j + lr];
-            sw[0] = scales[b][1][0];
-            sw[1] = scales[b][1][64];
-            __builtin_amdgcn_sched_barrier(0);
-            advance();
-            copy_w1(0);
-            wait_lds();
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sc[h][j] = sx[j] * sw[h];
-            wait_copies<8>();                         // this stage's second half of w
-            phase_barrier();
-            compute(std::integral_constant<int, 0>(), [&](int t) __attribute__((always_inline)) {
-                if (t == 4)
-                    copy_w1(1);
-            });
-            phase_barrier();
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                wf[i] = read_frag(wb + 16384 + i * 2048);
-            __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                copy_x(p);
-            wait_lds();
-            wait_copies<6>();                         // the next stage's x, first half of w and scales
-            phase_barrier();
-            compute(std::integral_constant<int, 1>(), [&](int t) __attribute__((always_inline)) {
-                if (t == 2 || t == 6)
-                    copy_w0(t >> 2);
-                if (t == 10)
-                    copy_scales();
-            });
-            phase_barrier();
-            b ^= 1;
+                sc[0][j] = sx[j] * sw[0];
+            half(std::integral_constant<int, 0>());
+            wait_copies<2>();                         // the next stage's x, first half of w and scales
+            stage_barrier();
+            xa[0] += to_ring, xa[1] += to_ring, wa[0] += to_ring, wa[1] += to_ring;
+            sa += to_scales, ga += to_scales;
+            to_ring = -to_ring, to_scales = -to_scales;
+            half(std::integral_constant<int, 1>());
+            settle();
         }
-        if (group == 0)
-            phase_barrier();
+        fold(29);
+        fold(30);
+        fold(31);
         int m0, n0;
         tile_origin(tile, m0, n0);
         const int mw = m0 + wm * 64, nw = n0 + group * 64;
@@ -295,8 +324,11 @@ static void launch_large(const F8Args &a, hipStream_t st)
 {
     const int tiles_m = (a.M + LBM - 1) / LBM, tiles_n = (a.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
     const int64_t tiles = (int64_t)tiles_m * tiles_n;
-    const int grid = (int)(tiles < a.num_cu ? tiles : a.num_cu);
-    hipLaunchKernelGGL(f8_gemm_large_kernel<GATED>, dim3(grid), dim3(512), 0, st, a, tiles_m, tiles_n, 4);
+    const dim3 grid((unsigned)(tiles < a.num_cu ? tiles : a.num_cu));
+    if (a.K % 128 == 0)
+        hipLaunchKernelGGL((f8_gemm_large_kernel<GATED, false>), grid, dim3(512), 0, st, a, tiles_m, tiles_n, 4);
+    else
+        hipLaunchKernelGGL((f8_gemm_large_kernel<GATED, true>), grid, dim3(512), 0, st, a, tiles_m, tiles_n, 4);
 }
 
 void launch_f8_large(const F8Args &a, bool gated, hipStream_t st)
