@@ -15,32 +15,11 @@ import functools
 import torch
 
 from . import ops
-from ._lib import CacheStruct, check, lib
-from .ops import _need, _shaped
+from ._lib import CacheStruct, lib
+from .ops import _call, _need, _shaped
 
 # A decode step calls these for microseconds of GPU work each, so the checks are
-# kept short: pointers go to ctypes as integers, the stream is torch's current
-# one as a number, and the device is only switched when it is not the current.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _stream(index):
-    if _raw_stream is not None:
-        return _raw_stream(index)
-    return torch.cuda.current_stream(index).cuda_stream
-
-
-def _call(index, fn, *args):
-    """fn(*args, stream) with device `index` current."""
-    if torch.cuda.current_device() == index:
-        status = fn(*args, _stream(index))
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, _stream(index))
-    if status:
-        check(status)
-
-
+# kept short (and see ops._call).
 _LARGEST = 2 ** 31 - 1
 
 

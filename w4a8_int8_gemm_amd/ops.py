@@ -38,7 +38,7 @@ def _need(t, dtype, name, ndim, like=None):
 def _shaped(t, dtype, shape, name, like):
     """t must be a contiguous `dtype` tensor of exactly `shape` on like's device."""
     _need(t, dtype, name, len(shape), like)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -64,6 +64,29 @@ def _p(t):
 
 def _st(t):
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+
+
+# The library is called with pointers as integers, torch's current stream as a
+# number, and the device only switched when it is not the current one: where the
+# GPU's work takes microseconds, the rest of a call should not.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(index):
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _call(index, fn, *args):
+    """fn(*args, stream) with device `index` current."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _stream(index))
+    if status:
+        check(status)
 
 
 def is_available() -> bool:
@@ -124,9 +147,8 @@ def w8a8_gemm_pc(xq, x_scale, wq, w_scale, out=None):
     _shaped(x_scale, torch.float32, (M,), "x_scale", xq)
     _shaped(w_scale, torch.float32, (N,), "w_scale", xq)
     out = _out(out, (M, N), torch.float16, xq, "out")
-    with torch.cuda.device(xq.device):
-        check(lib().w8a8_gemm_pc(_p(xq), _p(x_scale), _p(wq), _p(w_scale), _p(out), M, N, K,
-                                 _st(xq)))
+    _call(xq.get_device(), lib().w8a8_gemm_pc, xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+          out.data_ptr(), M, N, K)
     return out
 
 
@@ -137,9 +159,8 @@ def w8a8_gemm_pg(xq, x_scale, wq, w_scale, group_size: int, out=None):
     _shaped(x_scale, torch.float32, (M, G), "x_scale", xq)
     _shaped(w_scale, torch.float32, (N, G), "w_scale", xq)
     out = _out(out, (M, N), torch.float16, xq, "out")
-    with torch.cuda.device(xq.device):
-        check(lib().w8a8_gemm_pg(_p(xq), _p(x_scale), _p(wq), _p(w_scale), group_size, _p(out),
-                                 M, N, K, _st(xq)))
+    _call(xq.get_device(), lib().w8a8_gemm_pg, xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+          group_size, out.data_ptr(), M, N, K)
     return out
 
 
@@ -150,9 +171,8 @@ def w4a8_gemm(xq, x_scale, w4, w_scale, group_size: int, out=None):
     _shaped(x_scale, torch.float32, (M,), "x_scale", xq)
     _shaped(w_scale, torch.float32, (N, G), "w_scale", xq)
     out = _out(out, (M, N), torch.float16, xq, "out")
-    with torch.cuda.device(xq.device):
-        check(lib().w4a8_gemm(_p(xq), _p(x_scale), _p(w4), _p(w_scale), group_size, _p(out),
-                              M, N, K, _st(xq)))
+    _call(xq.get_device(), lib().w4a8_gemm, xq.data_ptr(), x_scale.data_ptr(), w4.data_ptr(), w_scale.data_ptr(),
+          group_size, out.data_ptr(), M, N, K)
     return out
 
 
@@ -236,9 +256,8 @@ def linear(mode, x, w, w_scale, group_size: int = 0, workspace=None, out=None):
         if workspace.numel() < need:
             raise ValueError(f"workspace has {workspace.numel()} bytes, {need} needed")
     out = _out(out, (M, N), torch.float16, x, "out")
-    with torch.cuda.device(x.device):
-        check(lib().linear(int(mode), _p(x), M, K, _p(w), _p(w_scale), group_size, N, _p(out),
-                           _p(workspace), workspace.numel(), _st(x)))
+    _call(x.get_device(), lib().linear, int(mode), x.data_ptr(), M, K, w.data_ptr(), w_scale.data_ptr(), group_size, N,
+          out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -249,9 +268,8 @@ def linear_noalloc(mode, x, w, w_scale, group_size: int = 0, out=None):
     mode = Mode(mode)
     M, N, K = _linear_shapes(mode, x, w, w_scale, group_size)
     out = _out(out, (M, N), torch.float16, x, "out")
-    with torch.cuda.device(x.device):
-        check(lib().linear_noalloc(int(mode), _p(x), M, K, _p(w), _p(w_scale), group_size, N,
-                                   _p(out), _st(x)))
+    _call(x.get_device(), lib().linear_noalloc, int(mode), x.data_ptr(), M, K, w.data_ptr(), w_scale.data_ptr(),
+          group_size, N, out.data_ptr())
     return out
 
 
