@@ -178,9 +178,10 @@ w4a8_status_t w4a8_mv(const w4a8_f16 *x, const uint8_t *w4, const float *w_scale
                       int32_t group_size, w4a8_f16 *y, int64_t N, int64_t K,
                       w4a8_stream_t stream);
 
-/* Bytes of device workspace linear() needs for these sizes (int8 codes and
- * fp32 scales of the activations, each 256-byte aligned).  0 when M == 0, and
- * for M == 1 with K <= 32768 (the matrix-vector paths need none). */
+/* Bytes of device workspace linear() needs for these sizes (codes and fp32
+ * scales of the activations, each 256-byte aligned, and in the F8 mode what
+ * f8_gemm needs for any N).  0 when M == 0, and outside the F8 mode for M == 1
+ * with K <= 32768 (the matrix-vector paths need none). */
 size_t linear_workspace_size(w4a8_mode_t mode, int64_t M, int64_t K, int32_t group_size);
 
 /* The whole layer with path selection ([P2] path selection): M == 1 runs the
@@ -190,7 +191,8 @@ size_t linear_workspace_size(w4a8_mode_t mode, int64_t M, int64_t K, int32_t gro
  * What linear accepts does not depend on M: the GEMM's rules.
  * x fp16 [M, K]; w is int8 [N, K] (PC, PG) or packed uint8 [N, K/2] (W4A8);
  * w_scale as the mode's GEMM takes it; group_size is ignored in PC mode.
- * W4A8_MODE_F8 (group_size ignored): quantize_act_f8 then f8_gemm for every M.
+ * W4A8_MODE_F8 (group_size ignored): quantize_act_f8 then f8_gemm for every M,
+ * w uint8 [N, K] e4m3 codes.
  * workspace: device buffer of at least linear_workspace_size() bytes, 256-byte
  * aligned (may be NULL when that size is 0). */
 w4a8_status_t linear(w4a8_mode_t mode, const w4a8_f16 *x, int64_t M, int64_t K, const void *w,
@@ -478,8 +480,8 @@ typedef enum {
  * nonzero for the output in e4m3. */
 size_t f8_gemm_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t quantize);
 
-/* The first half of a gated feed-forward block, both products, the activation
- * and the multiplication in one kernel:
+/* The first half of a gated feed-forward block, the activation and the
+ * multiplication on both products' sums before they leave the kernel:
  *     v[m, n] = act(g[m, n]) * u[m, n]
  * with g and u the sums of f8_gemm (before their rounding to fp16) of xq with
  * w_gate [N, K] and w_up [N, K].  Either y fp16 [M, N] = fp16(v), yq and

@@ -1,5 +1,33 @@
-// The products in 8-bit floating point for large outputs: 256 x 256 tiles,
-// eight waves in two groups that take turns at the matrix unit (gfx950).
+// The products in 8-bit floating point for large outputs (gfx950): y = sum over
+// blocks b of 128 of K of (sx[b, m] sw[n / 128, b]) (x_b . w_b), 256 x 256 tiles
+// of it by eight waves, of the gated pair 256 x 128 of both.
+//
+// Bound by the matrix unit, which may not wait: a 16 x 16 x 128 product is 32
+// cycles of it, and its sums' scales change with each, so that each is folded
+// into fp32 sums by four multiply-adds.  A loop of only these two, operands in
+// registers, takes 40 cycles a product (3810 TFLOP/s over the chip, 4770 without
+// the folds); here it is 46, with copies, reads and barriers, and the clock
+// falls to 1.84 GHz under the load.  What that takes:
+//  * A wave owns 64 tokens x 64 columns of each half of the tile: 32 products a
+//    stage from 12 fragments, all 128 sums and the fragments in registers.  A
+//    wave with half the columns would read half as much again from LDS.
+//  * A product is issued, then the fold of the third before it, whose result
+//    is there; fragments are replaced as soon as their last product is issued
+//    and the copies spread between, two stages of 64 KiB, so that no stretch
+//    waits for LDS.  Two barriers a stage: behind the wait for a stage's second
+//    half of w, and for the next stage's x and first half.  They keep the two
+//    waves of a SIMD within a half stage of each other and no closer; fixed
+//    turns between them cost more than they gave (8192^3 456 us, with the
+//    fragments read one stage ahead 466; without any 429).
+//  * Resources, offsets and places are held, not recomputed: 470 us otherwise.
+//  * The stages of all of a workgroup's tiles are one stream, so the next
+//    tile's first stages are on their way while the last one's sums are stored.
+//  * Tiles in bands of four along the tokens, neighbours on one XCD: of its L2 a
+//    band shares the weights.  Bands of 1, 2, 4, 8 and 16 take 400, 384, 381, 382
+//    and 389 us (gated, 4516 x 12288 x 4096).
+// 8192^3 429 us (2560 TFLOP/s; the library's product with one scale for the
+// whole operand 459), gated 4516 x 12288 x 4096 380 us (2394), 4096 x 4096 x 12288
+// 166 us (2490), 4096 x 8192 x 2560 77 us (2220).
 #include "f8.hpp"
 #include "f8_device.hpp"
 #include "f8_store.hpp"
