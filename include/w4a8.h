@@ -422,7 +422,8 @@ w4a8_status_t kv4_attention(const w4a8_f16 *q, int64_t q_stride, int64_t T, int3
  * codes; one that holds a value that is not finite gets s = NaN and zero
  * codes, so that its products are NaN and no other block's are.
  * M <= 2^25, N <= 2^27; K a multiple of 16 (the quantizers: of 8), K <= 2^22.
- * Code, weight, input and output buffers 16-byte aligned, scales 4-byte.
+ * Code, weight, input and output buffers 16-byte aligned, scales 4-byte.  No
+ * output may overlap an input, except where it is said.
  * ------------------------------------------------------------------------ */
 
 /* x fp16 [M, K] -> xq uint8 [M, K], x_scale fp32 [KB, M].  K % 8 == 0. */

@@ -258,3 +258,16 @@ def test_norm_of_more_rows_than_a_launch_has(torch_gpu):
         assert torch.equal(q[-5:].view(torch.uint8), a.view(torch.uint8))
         assert torch.equal(s.flatten()[-5:], b.flatten())
         assert not q[:-5].view(torch.uint8).any() and not s.flatten()[:-5].any()
+
+
+def test_activations_of_more_runs_than_a_launch_has(torch_gpu):
+    """Rows of two runs of 512 values, one more than a launch numbers: each run's wavefront takes both."""
+    import torch
+    import w4a8_int8_gemm_amd as w
+    m, k = (1 << 24) + 3, 520
+    x = torch.zeros(m, k, dtype=torch.float16, device="cuda")
+    x[-5:] = torch.randn(5, k, device="cuda").half()
+    q, s = w.quantize_act_f8(x)
+    a, b = w.quantize_act_f8(x[-5:].contiguous())
+    assert torch.equal(q[-5:].view(torch.uint8), a.view(torch.uint8)) and torch.equal(s[:, -5:], b)
+    assert not q[:-5].view(torch.uint8).any() and not s[:, :-5].any()

@@ -9,7 +9,7 @@
 // stage's fragments read while one is multiplied.  With 64 columns and e4m3
 // output two workgroups share a scale; they meet as those of f8_few.hip do.
 //
-// 517 x 4096 x 4096 17.2 us (1010 TFLOP/s; 24.1 with its quantizer), 300 x 5120 x
+// 517 x 4096 x 4096 17.2 us (1010 TFLOP/s; 20.9 with its quantizer), 300 x 5120 x
 // 2560 10.8 us and the gated pair 301 x 5121 x 2560 16.5 (960 TFLOP/s): 5.5 us of
 // each are a launch's start and end, the rest 0.28 to 0.5 us a stage, the rate
 // at which a compute unit's copies arrive.
