@@ -58,8 +58,11 @@ def check(shim, M, N, K, gated, quantize, num_cu):
                 assert need >= nb * splits * m * 512 + nb * 8, what
         elif kind == TILE:
             bm, bn = TILES[shape]
-            assert splits == 1 or not quantize, what
-            assert -(-m // bm) * -(-n // bn) * 256 < 1 << 32, what
+            tiles = -(-m // bm) * -(-n // bn)
+            assert tiles * splits * 256 < 1 << 32, what
+            if splits > 1:                                 # every part's sums of every tile, and the counters
+                assert len(launches) == 1 and M > 64 and splits <= -(-K // 128) and not (quantize and bn < 128), what
+                assert need >= splits * tiles * bm * bn * 4 * (1 + gated) + tiles * 8, what
             if quantize and bn < 128:                      # two workgroups a scale: one tile of tokens only
                 assert m <= bm and need >= nb * m * 512 + nb * 8, what
         else:
@@ -89,7 +92,7 @@ def test_ends_of_the_ranges(shim):
 
 def test_workspace_for_any_columns(shim):
     """linear's workspace does not know N: the most that any N needs."""
-    for M in (1, 2, 16, 33, 64, 65, 5000):
+    for M in (1, 2, 16, 33, 64, 65, 128, 300, 5000, 16384, 16385):
         for K in (16, 8064, 8080, 14336, 1 << 20):
             most = max(shim.shim_workspace(M, N, K, 0, 0) for N in list(range(1, 3000)) + [8128, 8129, 10240, 1 << 20])
             assert shim.shim_workspace_any(M, K) >= most
@@ -104,11 +107,13 @@ def test_gpu_sizes_reach_every_kernel(shim):
                 seen.add("tokens" if launches[1][3] else "columns")
             for kind, shape, splits, *_ in launches:
                 seen.add({FEW: ("few", splits), TILE: ("tile", shape), LARGE: "large"}[kind])
+                if kind == TILE and splits > 1:
+                    seen.add("parts")
             if launches[0][0] == LARGE and len(launches) == 1:
                 seen.add("large alone")
         return seen
 
-    every = {("few", 1), "large", "large alone", "tokens", "columns"}
+    every = {("few", 1), "parts", "large", "large alone", "tokens", "columns"}
     assert reached(PRODUCTS, 0, 0) >= every | {("few", 2), ("few", 4)} | {("tile", i) for i in range(5)}
     assert reached(GATED, 1, 0) >= every | {("tile", i) for i in range(5)}
     assert reached(GATED, 1, 1) >= every | {("tile", i) for i in (0, 1, 2, 4)}

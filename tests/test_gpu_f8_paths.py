@@ -149,8 +149,9 @@ def test_long_k():
         check_half(w.f8_gemm(*data), *product(*data))
 
 
-# sizes whose workgroups meet in the workspace: K in four, K in two, two workgroups a scale
-MEET = [(5, 500, 8208, False), (17, 1000, 8320, False), (3, 1030, 1040, True), (33, 8250, 272, True)]
+# sizes whose workgroups meet in the workspace: K in four, K in two, two workgroups a scale, K in parts
+MEET = [(5, 500, 8208, False), (17, 1000, 8320, False), (3, 1030, 1040, True), (33, 8250, 272, True),
+        (300, 200, 4112, False), (130, 300, 4112, True)]
 
 
 def run(data, is_gated, ws, out=None):
@@ -176,7 +177,7 @@ def test_one_workspace_for_all_whatever_it_holds():
             ws.random_(0, 256)
         else:
             ws.fill_(fill)
-        for i in (0, 2, 1, 3, 3, 0, 2, 2, 1):
+        for i in (0, 2, 5, 1, 4, 3, 3, 4, 0, 5, 2, 2, 1):
             assert torch.equal(run(sets[i], MEET[i][3], ws), want[i])
     # no byte behind what was asked for is touched
     for d, c in zip(sets, MEET):
@@ -203,13 +204,13 @@ def test_two_graphs_over_one_workspace():
             out = run(d, c[3], ws), run(d, c[3], ws)
         graphs.append((graph, out))
     for turn in range(6):
-        for i in (0, 1, 2, 3, 3, 1, 0, 0, 2):
+        for i in (0, 1, 5, 2, 4, 3, 3, 1, 4, 0, 5, 0, 2):
             graphs[i][0].replay()
             if turn % 2:
-                assert torch.equal(run(sets[3 - i], MEET[3 - i][3], ws), want[3 - i])
+                assert torch.equal(run(sets[5 - i], MEET[5 - i][3], ws), want[5 - i])
             if turn == 5:
                 ws.random_(0, 256)                         # between calls it may hold anything
-        for i in range(4):
+        for i in range(len(MEET)):
             graphs[i][0].replay()
             torch.cuda.synchronize()
             for out in graphs[i][1]:

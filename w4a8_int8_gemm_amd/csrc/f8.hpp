@@ -47,13 +47,13 @@ struct F8Args {
     int num_cu;
 };
 
-// What several workgroups of one launch leave for the last of them: sums of 128
-// columns in f8_few.hip's and f8_tile.hip's kernels.
+// What several workgroups of one launch leave for the last of them: the sums of
+// 128 columns, or (f8_tile.hip with K in parts) those of a tile.
 struct F8Parts {
     int splits;                 // ranges of K
     uint64_t tag;               // of the call among the counters
-    uint64_t *counters;         // one for each 128 columns, kCounterStride apart
-    float *sums;                // [ceil(N / 128)][splits][M][128]
+    uint64_t *counters;         // one for each 128 columns or tile, kCounterStride apart
+    float *sums;                // [ceil(N / 128)][splits][M][128], or [splits][tiles][sums of a tile]
 };
 
 // Bytes of workspace (f8_plan.hip); the product on checked arguments, by the

@@ -42,7 +42,19 @@ int splits_of(int64_t M, int64_t N, int64_t K, bool gated)
 // K, weights from HBM) with every kernel: the choice is 0.4 % slower than the
 // best on average, 8 % at most.
 constexpr double kStart = 5.5;
+constexpr double kMeet = 3.0, kMeetByte = 1.5e-5;       // parts of K: their meeting, and each byte of a part's sums
 constexpr double kSecond = 2.0;         // what of it a second launch right behind the first does not take
+
+// A stage of a workgroup where each has a compute unit of its own.
+double stage_time(int shape, bool gated, int64_t groups, int num_cu)
+{
+    const F8Tile t = kF8Tiles[shape];
+    const int copies = (t.tokens + (gated ? 2 : 1) * t.columns) / 8 + 4;
+    const int stage = (t.tokens + (gated ? 2 : 1) * t.columns) * 128 + 1024;
+    const int all = 157 * 1024 / stage, deep = all < 8 ? all : 8;
+    const double alone = 0.0141 * copies, wait = 0.97 / (deep - 1) * (0.5 + 0.5 * (double)groups / num_cu);
+    return alone > wait ? alone : wait;
+}
 
 double tile_time(int shape, int64_t M, int64_t N, int64_t K, bool gated, int num_cu)
 {
@@ -54,10 +66,8 @@ double tile_time(int shape, int64_t M, int64_t N, int64_t K, bool gated, int num
     const int all = 157 * 1024 / stage, half = 78 * 1024 / stage;
     const int deep = all < 8 ? all : 8;
     const double alone = 0.0141 * copies, wait = 0.97 / (deep - 1);
-    if (groups <= num_cu) {
-        const double w = wait * (0.5 + 0.5 * (double)groups / num_cu);
-        return kStart + stages * (alone > w ? alone : w);
-    }
+    if (groups <= num_cu)
+        return kStart + stages * stage_time(shape, gated, groups, num_cu);
     if (half < 2)
         return kStart + stages * (alone > wait ? alone : wait) * ((groups + num_cu - 1) / num_cu);
     const double two = 2 * 0.0163 * copies;
@@ -94,6 +104,45 @@ int best_shape(int64_t M, int64_t N, int64_t K, bool gated, bool quantize, int n
     return best;
 }
 
+// Where more than 64 tokens' tiles leave half of the chip idle or more, K in
+// `splits` parts, a workgroup each, that meet in the workspace, if the model
+// says so: 128 x 4096 x 14336 37.8 us in one part, 24.5 in four; 111 x 776 x 6880
+// 18.8 and 10.9; 1272 x 183 x 10224 28.2 and 15.3; but 303 x 2991 x 5520 18.1 in
+// one.  Parts under eight stages are not worth their start.  Of the sizes
+// alone, as the workspace is, for the 256 compute units of the chip.
+struct Cut {
+    int shape, splits;
+    int64_t tiles;
+    size_t bytes;                                          // of one part's sums
+};
+constexpr int kCutCUs = 256;
+
+Cut cut_of(int64_t M, int64_t N, int64_t K, bool gated, bool quantize)
+{
+    Cut best = {0, 1, 0, 0};
+    const int64_t blocks = (K + 127) / 128;
+    if (M <= kF8FewTokens || blocks < 16 || (M + 127) / 128 > kCutCUs / 2 || (N + 127) / 128 > kCutCUs / 2)
+        return best;
+    double time;
+    best_shape(M, N, K, gated, quantize, kCutCUs, &time);
+    for (int i = 0; i < kF8TileShapes; ++i) {
+        const F8Tile t = kF8Tiles[i];
+        if (quantize && t.columns < 128)
+            continue;
+        const int64_t tiles = ((M + t.tokens - 1) / t.tokens) * ((N + t.columns - 1) / t.columns);
+        const int64_t size = (gated ? 2 : 1) * t.tokens * t.columns * (int)sizeof(float);      // of a part's sums of a tile
+        for (int s = 2; s <= 8 && s * tiles <= kCutCUs && blocks / s >= 8; ++s) {
+            const double cut = kStart + (double)((blocks + s - 1) / s) * stage_time(i, gated, s * tiles, kCutCUs) +
+                               kMeet + (s + 1) * (double)size * kMeetByte;
+            if (cut < time) {
+                time = cut;
+                best = {i, s, tiles, (size_t)(tiles * size)};
+            }
+        }
+    }
+    return best;
+}
+
 void launch_shape(const F8Args &a, bool gated, int shape, const F8Parts &f, hipStream_t st)
 {
     if (shape < kF8TileShapes)
@@ -106,8 +155,12 @@ void launch_shape(const F8Args &a, bool gated, int shape, const F8Parts &f, hipS
 
 size_t f8_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool quantize)
 {
-    if (M <= 0 || N <= 0 || K <= 0 || M > kF8FewTokens)
+    if (M <= 0 || N <= 0 || K <= 0)
         return 0;
+    if (M > kF8FewTokens) {
+        const Cut c = cut_of(M, N, K, gated, quantize);
+        return c.splits == 1 ? 0 : kv4_counter_bytes(c.tiles, 1) + c.splits * c.bytes;
+    }
     const int splits = splits_of(M, N, K, gated);
     if (splits == 1 && !quantize)
         return 0;
@@ -116,6 +169,10 @@ size_t f8_workspace(int64_t M, int64_t N, int64_t K, bool gated, bool quantize)
 
 size_t f8_workspace_any(int64_t M, int64_t K)
 {
+    if (M > kF8FewTokens)                          // at most as many 128 x 128 tiles as compute units
+        return (K + 127) / 128 < 16 || (M + 127) / 128 > kCutCUs / 2
+                   ? 0
+                   : kv4_counter_bytes(kCutCUs, 1) + (size_t)kCutCUs * 128 * 128 * sizeof(float);
     size_t most = 0;
     for (int64_t N : {512, 1024})                  // the widest outputs cut in four and in two
         most = f8_workspace(M, N, K, false, false) > most ? f8_workspace(M, N, K, false, false) : most;
@@ -136,6 +193,13 @@ void launch_f8(const F8Args &a, bool gated, uint64_t tag, void *workspace, hipSt
     }
     if (a.M <= kF8FewTokens) {
         launch_f8_tile(a, gated, 0, f, st);
+        return;
+    }
+    const Cut cut = cut_of(a.M, a.N, a.K, gated, quantize);
+    if (cut.splits > 1) {
+        f.splits = cut.splits;
+        f.sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + kv4_counter_bytes(cut.tiles, 1));
+        launch_f8_tile(a, gated, cut.shape, f, st);
         return;
     }
     // Whole rounds of large tiles over the chip, and what is left of the tokens

@@ -8,6 +8,7 @@
 // together, up to D - 1 of them on the way, one barrier a stage, the next
 // stage's fragments read while one is multiplied.  With 64 columns and e4m3
 // output two workgroups share a scale; they meet as those of f8_few.hip do.
+// Where the tiles are few, workgroups take parts of K.
 //
 // 517 x 4096 x 4096 17.2 us (1010 TFLOP/s; 20.9 with its quantizer), 300 x 5120 x
 // 2560 10.8 us and the gated pair 301 x 5121 x 2560 16.5 (960 TFLOP/s): 5.5 us of
@@ -40,6 +41,9 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(F8Args a, F8Parts f, int t
 
     const int M = a.M, N = a.N, K = a.K;
     const int KB = (K + 127) >> 7;
+    // this workgroup's range of K
+    const int split = (int)blockIdx.y;
+    const int k_first = (int)((int64_t)KB * split / f.splits), k_end = (int)((int64_t)KB * (split + 1) / f.splits);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wm = wave % WM, wn = wave / WM;
@@ -57,6 +61,8 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(F8Args a, F8Parts f, int t
     const bool shared = GATED && RS < 128 && !a.y;         // one tile of tokens: launch_f8()
     if (shared && threadIdx.x == 0)
         announce(f.counters + (int64_t)nb * kCounterStride, f.tag);
+    if (f.splits > 1 && threadIdx.x == 0)
+        announce(f.counters + (int64_t)id * kCounterStride, f.tag);
 
     const int crow = lane >> 3;
     const int chunk0 = 16 * ((lane & 7) ^ crow);
@@ -79,9 +85,9 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(F8Args a, F8Parts f, int t
     };
     const int xblk = wave * (XC / 4), wblk = wave * (WC / 4);
     auto stage_of = [&](int slot, int t) __attribute__((always_inline)) {
-        const bool live = t < KB;
+        const bool live = t < k_end;
         Stage g;
-        g.u = live ? t : 0;
+        g.u = live ? t : k_first;
         g.k0 = (uint32_t)(g.u * 128);
         g.at = ring_at + (uint32_t)(slot * STAGE);
         const int end = live ? K - (int)g.k0 : 0;          // bytes of a row from this stage on
@@ -191,7 +197,7 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(F8Args a, F8Parts f, int t
 
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-        const Stage g = stage_of(d, d);
+        const Stage g = stage_of(d, k_first + d);
 #pragma unroll
         for (int p = 0; p < NI; ++p)
             copy(g, p);
@@ -203,12 +209,67 @@ __global__ __launch_bounds__(256) void f8_tile_kernel(F8Args a, F8Parts f, int t
 #pragma unroll
     for (int q = 0; q < READS; ++q)
         read(f0, 0, q);
-    for (int t = 0; t < KB; t += 2) {
+    for (int t = k_first; t < k_end; t += 2) {
         step(f0, f1, slot, t);
-        if (t + 1 < KB)
+        if (t + 1 < k_end)
             step(f1, f0, slot, t + 1);
     }
     wait_vmcnt<0>();                                       // no copy may still be writing LDS at the end
+
+    // K in parts: each leaves its sums as its threads hold them, the last to
+    // arrive adds them up in their order and goes on as the only one
+    if (f.splits > 1) {
+        constexpr int SUMS = SIDES * NB * MB * 4 * 256;
+        const int64_t tiles = gridDim.x;
+        float *const at = f.sums + (int64_t)id * SUMS + 2 * threadIdx.x;
+#pragma unroll
+        for (int s = 0; s < SIDES; ++s)
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int j = 0; j < MB; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        store_shared(at + split * tiles * SUMS + (((s * NB + i) * MB + j) * 2 + h) * 512,
+                                     acc[s][i][j][2 * h], acc[s][i][j][2 * h + 1]);
+        __builtin_amdgcn_s_waitcnt(0);                     // this wave's stores are complete
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = arrive(f.counters + (int64_t)id * kCounterStride, f.splits) ? 1 : 0;
+        __syncthreads();
+        if (!last)
+            return;
+#pragma unroll
+        for (int s = 0; s < SIDES; ++s)
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int j = 0; j < MB; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[s][i][j][r] = 0.0f;
+        for (int p = 0; p < f.splits; ++p) {
+            const float *from = at + p * tiles * SUMS;
+#pragma unroll
+            for (int s = 0; s < SIDES; ++s)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    float2 v[MB][2];
+#pragma unroll
+                    for (int j = 0; j < MB; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            v[j][h] = load_shared(from + (((s * NB + i) * MB + j) * 2 + h) * 512);
+#pragma unroll
+                    for (int j = 0; j < MB; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            acc[s][i][j][2 * h] += v[j][h].x;
+                            acc[s][i][j][2 * h + 1] += v[j][h].y;
+                        }
+                }
+        }
+    }
 
     const int mw = m0 + wm * MB * 16, nw = n0 + wn * NB * 16;
     if constexpr (GATED)
@@ -250,7 +311,7 @@ void launch_tile(const F8Args &a, const F8Parts &f, hipStream_t st)
     constexpr int STAGE = (BM + (GATED ? 2 : 1) * RS) * 128 + 1024;
     constexpr int NI = (BM + (GATED ? 2 : 1) * RS) / 32 + 1;
     const int tiles_m = (a.M + BM - 1) / BM;
-    const dim3 grid((unsigned)(tiles_m * ((a.N + RS - 1) / RS)));
+    const dim3 grid((unsigned)(tiles_m * ((a.N + RS - 1) / RS)), (unsigned)f.splits);
     // stages as many as half of a compute unit's LDS holds, or where the grid
     // has one workgroup for each (or half holds fewer than two), all of it
     constexpr auto depth = [](int bytes) {
@@ -260,7 +321,7 @@ void launch_tile(const F8Args &a, const F8Parts &f, hipStream_t st)
         return d;
     };
     constexpr int ALL = depth(157 * 1024), PART = depth(78 * 1024) < 2 ? ALL : depth(78 * 1024);
-    if ((int)grid.x <= a.num_cu)
+    if ((int64_t)grid.x * grid.y <= a.num_cu)
         hipLaunchKernelGGL((f8_tile_kernel<GATED, WM, WN, MB, NB, ALL>), grid, dim3(256), 0, st, a, f, tiles_m);
     else
         hipLaunchKernelGGL((f8_tile_kernel<GATED, WM, WN, MB, NB, PART>), grid, dim3(256), 0, st, a, f, tiles_m);
