@@ -72,6 +72,11 @@ S = w.Status
     # linear in the F8 mode
     (lambda L: L.linear(3, A, 4, 256, A2, A3, 0, 8, A4, None, 0, None), S.ERR_WORKSPACE),
     (lambda L: L.linear(3, A, 4, 256, A2, A3, 0, 8, A4, P(4096 + 16), 1 << 30, None), S.ERR_WORKSPACE),
+    (lambda L: L.f8_gemm(A, A2, A3, A4, A, 5, 500, 8208, None, 0, None), S.ERR_WORKSPACE),
+    (lambda L: L.f8_gemm(A, A2, A3, A4, A, 300, 200, 4112, None, 0, None), S.ERR_WORKSPACE),
+    (lambda L: L.f8_gemm(A, A2, A3, A4, A, 300, 200, 4112, A, L.f8_gemm_workspace_size(300, 200, 4112) - 1, None),
+     S.ERR_WORKSPACE),
+    (lambda L: L.f8_gemm_gated(A, A2, A3, A4, A3, A4, 0, 130, 300, 4112, None, A, A2, None, 0, None), S.ERR_WORKSPACE),
     (lambda L: L.linear(3, A, 4, 264, A2, A3, 0, 8, A4, A5, 1 << 30, None), S.ERR_SHAPE),
     (lambda L: L.linear(3, A, 4, 256, A2, A3, 0, 8, None, A5, 1 << 30, None), S.ERR_INVALID_ARG),
     (lambda L: L.linear(3, A, 0, 256, A2, A3, 0, 8, A4, None, 0, None), S.OK),
