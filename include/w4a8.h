@@ -181,7 +181,10 @@ w4a8_status_t w4a8_mv(const w4a8_f16 *x, const uint8_t *w4, const float *w_scale
 /* Bytes of device workspace linear() needs for these sizes (codes and fp32
  * scales of the activations, each 256-byte aligned, and in the F8 mode what
  * f8_gemm needs for any N).  0 when M == 0, and outside the F8 mode for M == 1
- * with K <= 32768 (the matrix-vector paths need none). */
+ * with K <= 32768 (the matrix-vector paths need none).  A call in the F8 mode
+ * asks for what its own N needs, which may be less: the M * K bytes of codes and
+ * 4 * M * ceil(K / 128) of scales, each rounded up to 256, and
+ * f8_gemm_workspace_size(M, N, K). */
 size_t linear_workspace_size(w4a8_mode_t mode, int64_t M, int64_t K, int32_t group_size);
 
 /* The whole layer with path selection ([P2] path selection): M == 1 runs the
@@ -193,8 +196,8 @@ size_t linear_workspace_size(w4a8_mode_t mode, int64_t M, int64_t K, int32_t gro
  * w_scale as the mode's GEMM takes it; group_size is ignored in PC mode.
  * W4A8_MODE_F8 (group_size ignored): quantize_act_f8 then f8_gemm for every M,
  * w uint8 [N, K] e4m3 codes.
- * workspace: device buffer of at least linear_workspace_size() bytes, 256-byte
- * aligned (may be NULL when that size is 0). */
+ * workspace: device buffer of at least linear_workspace_size() bytes (F8: or the
+ * call's own need, see there), 256-byte aligned (may be NULL when that is 0). */
 w4a8_status_t linear(w4a8_mode_t mode, const w4a8_f16 *x, int64_t M, int64_t K, const void *w,
                      const float *w_scale, int32_t group_size, int64_t N, w4a8_f16 *y,
                      void *workspace, size_t workspace_bytes, w4a8_stream_t stream);
@@ -202,16 +205,18 @@ w4a8_status_t linear(w4a8_mode_t mode, const w4a8_f16 *x, int64_t M, int64_t K, 
 /* linear() for callers that cannot allocate device memory (code under HIP
  * graph capture, tight serving loops, harnesses that forbid allocation): the
  * same argument rules, kernels and results as linear(), without a workspace
- * argument.  The activations' int8 codes and fp32 scales are kept in a
- * static device array of 64 MiB (2^26 bytes) that the library holds on each
- * GPU it runs on until the process ends; its device address is looked up
- * once per GPU.  A call whose linear_workspace_size() exceeds 64 MiB returns
- * W4A8_ERR_WORKSPACE before anything is launched (use linear() with a
+ * argument.  The activations' codes and fp32 scales, and in the F8 mode the
+ * workspace of f8_gemm, are kept in a static device array of 64 MiB (2^26 bytes)
+ * that the library holds on each GPU it runs on until the process ends; its
+ * device address is looked up once per GPU.  A call that needs more than 64 MiB
+ * (linear_workspace_size(); in the F8 mode what its own N needs, see there)
+ * returns W4A8_ERR_WORKSPACE before anything is launched (use linear() with a
  * workspace instead).  The call allocates nothing.  Every call on one GPU
  * shares that GPU's array and overwrites it: calls that overlap on one GPU
  * (different streams or threads) race, so the caller must order them, e.g.
  * on one stream.  Nothing in the array has to start at zero -- each call
- * writes the codes and scales it then reads. */
+ * writes the codes, scales and sums it then reads, and the counters of an F8
+ * product take whatever they hold for another call's. */
 w4a8_status_t linear_noalloc(w4a8_mode_t mode, const w4a8_f16 *x, int64_t M, int64_t K,
                              const void *w, const float *w_scale, int32_t group_size, int64_t N,
                              w4a8_f16 *y, w4a8_stream_t stream);

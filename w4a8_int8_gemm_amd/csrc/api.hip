@@ -272,18 +272,19 @@ w4a8_status_t run_f8(const char *fn, F8Args a, bool gated, void *workspace, w4a8
 }
 
 // linear()'s workspace in the F8 mode: codes, scales, and what the product
-// needs whatever N is.
+// needs, of N columns or (N < 0: the query does not know N) of any.
 struct F8Linear {
     size_t codes, scales, product;
-    F8Linear(int64_t M, int64_t K)
+    F8Linear(int64_t M, int64_t K, int64_t N = -1)
         : codes(align256((size_t)M * (size_t)K)),
           scales(align256((size_t)M * (size_t)((K + 127) / 128) * sizeof(float))),
-          product(f8_workspace_any(M, K)) {}
+          product(N < 0 ? f8_workspace_any(M, K) : f8_workspace(M, N, K, false, false)) {}
     size_t bytes() const { return codes + scales + product; }
 };
 
-// ---- the static scratch of linear_noalloc(): the activations' int8 codes
-// and fp32 scales live in this device array instead of a caller workspace.
+// ---- the static scratch of linear_noalloc(): the activations' codes and
+// fp32 scales, and in the F8 mode what its product needs, live in this device
+// array instead of a caller workspace.
 // Each device the library runs on holds its own copy (placed when the code
 // object is loaded there) until the process ends.  Host code never passes
 // the array's name to a kernel (on the host it only names the symbol): the
@@ -430,7 +431,7 @@ w4a8_status_t linear_run(const char *fn, w4a8_mode_t mode, const w4a8_f16 *x, in
     const int32_t act_gs = (mode == W4A8_MODE_W8A8_PG) ? group_size : 0;
     w4a8_status_t st;
     if (mode == W4A8_MODE_F8) {
-        const F8Linear ws(M, K);
+        const F8Linear ws(M, K, N);
         st = check_workspace(fn, ws.bytes(), workspace, workspace_bytes);
         if (st != W4A8_OK)
             return st;
@@ -746,7 +747,8 @@ w4a8_status_t linear_noalloc(w4a8_mode_t mode, const w4a8_f16 *x, int64_t M, int
     w4a8_status_t st = check_linear(fn, mode, x, M, K, w, w_scale, group_size, N, y, &empty);
     if (st != W4A8_OK || empty)
         return st == W4A8_OK ? ok() : st;
-    const size_t need = linear_workspace_size(mode, M, K, group_size);
+    const size_t need = mode == W4A8_MODE_F8 ? F8Linear(M, K, N).bytes()
+                                             : linear_workspace_size(mode, M, K, group_size);
     if (need > kScratchBytes)
         return fail(W4A8_ERR_WORKSPACE, "%s: M=%lld, K=%lld need %zu bytes of scratch; the "
                     "static array holds %zu (call linear() with a workspace)", fn, (long long)M,

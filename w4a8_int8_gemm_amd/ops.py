@@ -243,12 +243,21 @@ def _linear_shapes(mode, x, w, w_scale, group_size):
     return M, N, K
 
 
+def _linear_need(mode, M, N, K, group_size):
+    """Bytes that this call needs: in the F8 mode those of its own N, not of any."""
+    if mode != Mode.F8:
+        return linear_workspace_size(mode, M, K, group_size)
+    codes, scales = M * K, 4 * M * ((K + 127) // 128)
+    return (codes + 255) // 256 * 256 + (scales + 255) // 256 * 256 + int(lib().f8_gemm_workspace_size(M, N, K))
+
+
 def linear(mode, x, w, w_scale, group_size: int = 0, workspace=None, out=None):
     """The whole layer: the mode's matrix-vector kernel when M == 1 (the int8 modes), else quantize +
-    GEMM.  Mode.F8 takes the weights of quantize_weight_f8."""
+    GEMM.  Mode.F8 takes the weights of quantize_weight_f8.  workspace: of linear_workspace_size bytes
+    (Mode.F8: as few as this N needs do)."""
     mode = Mode(mode)
     M, N, K = _linear_shapes(mode, x, w, w_scale, group_size)
-    need = linear_workspace_size(mode, M, K, group_size)
+    need = _linear_need(mode, M, N, K, group_size)
     if workspace is None:
         workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=x.device)
     else:
