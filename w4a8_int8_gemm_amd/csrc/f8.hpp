@@ -30,8 +30,9 @@ struct NormArgs {
     int64_t M;
     int K;
     float eps;
+    float lift, unlift;         // the launcher's (norm_inverse)
 };
-void launch_rmsnorm_quant(NormOut out, const NormArgs &a, hipStream_t st);
+void launch_rmsnorm_quant(NormOut out, NormArgs a, hipStream_t st);
 
 struct F8Args {
     const uint8_t *x;           // e4m3 [M, K]

@@ -17,19 +17,25 @@ namespace w4a8 {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 
-// A block's scale and its reciprocal from the largest |v|, as bits.
+// A block's scale and its reciprocal (f8_reciprocal) from the largest |v|, as
+// bits.  SMALL: s may lie below 2^-90 (of fp16 values it is 0 or above 2^-33).
+template <bool SMALL = true>
 __device__ __forceinline__ void f8_block_scale(uint32_t amax_bits, float &s, float &r)
 {
     s = amax_bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : f8_scale(__uint_as_float(amax_bits));
-    r = s > 0.0f ? 1.0f / s : 0.0f;      // zero codes for s = 0 and s = NaN
+    r = SMALL ? f8_reciprocal(s) : s > 0.0f ? 1.0f / s : 0.0f;
 }
 
 // Four values' codes in one dword, the first lowest.  With r = 0 the codes
 // are 0 whatever the values are.
+template <bool SMALL = true>
 __device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d, float s, float r)
 {
     if (r == 0.0f)
         return 0u;
+    if (SMALL && __builtin_expect(r < 0.0f, 0)) {
+        a *= kF8Lift, b *= kF8Lift, c *= kF8Lift, d *= kF8Lift, s *= kF8Lift, r = -r;
+    }
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(f8_quotient(a, s, r), f8_quotient(b, s, r), 0, false);
     w = __builtin_amdgcn_cvt_pk_fp8_f32(f8_quotient(c, s, r), f8_quotient(d, s, r), w, true);
     return (uint32_t)w;

@@ -11,8 +11,8 @@ namespace {
 // The codes of a 16-byte chunk of fp16 values.
 __device__ __forceinline__ uint2 f8_chunk8(uint4 v, float s, float r)
 {
-    return make_uint2(f8_codes4(lo_h2f(v.x), hi_h2f(v.x), lo_h2f(v.y), hi_h2f(v.y), s, r),
-                      f8_codes4(lo_h2f(v.z), hi_h2f(v.z), lo_h2f(v.w), hi_h2f(v.w), s, r));
+    return make_uint2(f8_codes4<false>(lo_h2f(v.x), hi_h2f(v.x), lo_h2f(v.y), hi_h2f(v.y), s, r),
+                      f8_codes4<false>(lo_h2f(v.z), hi_h2f(v.z), lo_h2f(v.w), hi_h2f(v.w), s, r));
 }
 
 // The largest |x| of fp16 values, as fp16 bits, to fp32 bits: infinities and
@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256) void quant_act_f8_kernel(const uint16_t *__res
         const uint4 v = valid ? xr[c] : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t m = group_max_u32<16>(absmax_bits8(v));
         float s, r;
-        f8_block_scale(amax_h2f_bits(m), s, r);
+        f8_block_scale<false>(amax_h2f_bits(m), s, r);
         if (!valid)
             continue;
         if ((lane & 15) == 0)
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(256) void quant_weight_f8_kernel(const uint16_t *__
     __syncthreads();
     m = max(max(top[0], top[1]), max(top[2], top[3]));
     float s, r;
-    f8_block_scale(amax_h2f_bits(m), s, r);
+    f8_block_scale<false>(amax_h2f_bits(m), s, r);
     if (threadIdx.x == 0)
         scale[nb * kblocks + kb] = s;
 #pragma unroll
@@ -110,8 +110,9 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-// fl32(v / s) to an int8 code; v is no more than the slice's largest, but the
-// quotient is taken in fp32, so it is clamped as the rule says.
+// fl32(v / s) to an int8 code (f8_quotient's steps and its domain); v is no more
+// than the slice's largest, but the quotient is taken in fp32, so it is clamped
+// as the rule says.
 __device__ __forceinline__ uint32_t int8_codes4(const float *v, float s, float r)
 {
     int c[4];
@@ -140,9 +141,15 @@ __device__ __forceinline__ void norm_squares(const Eight &h, float &ss)
 }
 
 // 1 / sqrt(mean of the squares + eps); 0 for a row of zeros, whose values are zero with any eps.
-__device__ __forceinline__ float norm_inverse(float ss, int K, float eps)
+//
+// Values and their scales are held `lift` times as large, a power of two, and
+// the scales stored without it.  It is 1 up to eps = 2^60: h and the gains are at
+// least 2^-24 where they are not 0 and h is at most 2^17, so the values are at
+// least 2^-48 / (2^34 + eps)^(1/2) and the scales above 2^-90, as f8_quotient
+// takes them.  With a larger eps 2^64 keeps them there.
+__device__ __forceinline__ float norm_inverse(float ss, const NormArgs &a)
 {
-    return ss == 0.0f ? 0.0f : 1.0f / sqrtf(ss / (float)K + eps);
+    return ss == 0.0f ? 0.0f : a.lift / sqrtf(ss / (float)a.K + a.eps);
 }
 
 __device__ __forceinline__ Eight norm_value(const Eight &h, uint4 gain, float inv)
@@ -168,7 +175,7 @@ __device__ __forceinline__ uint32_t norm_largest(const Eight &y, bool finite)
 template <NormOut OUT> __device__ __forceinline__ void norm_scale(uint32_t m, float &s, float &r)
 {
     if (OUT == NormOut::F8) {
-        f8_block_scale(m, s, r);
+        f8_block_scale<false>(m, s, r);
         return;
     }
     s = m >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(m) / 127.0f;
@@ -179,8 +186,8 @@ template <NormOut OUT> __device__ __forceinline__ void norm_scale(uint32_t m, fl
 template <NormOut OUT> __device__ __forceinline__ uint2 norm_codes(const Eight &y, float s, float r)
 {
     if (OUT == NormOut::F8)
-        return make_uint2(f8_codes4(y.v[0], y.v[1], y.v[2], y.v[3], s, r),
-                          f8_codes4(y.v[4], y.v[5], y.v[6], y.v[7], s, r));
+        return make_uint2(f8_codes4<false>(y.v[0], y.v[1], y.v[2], y.v[3], s, r),
+                          f8_codes4<false>(y.v[4], y.v[5], y.v[6], y.v[7], s, r));
     return make_uint2(int8_codes4(y.v, s, r), int8_codes4(y.v + 4, s, r));
 }
 
@@ -253,7 +260,7 @@ __global__ __launch_bounds__(64 * kNormWaves) void rmsnorm_quant_kernel(NormArgs
     ss = sums[0];
     for (int i = 1; i < waves; ++i)
         ss += sums[i];
-    const float inv = norm_inverse(ss, K, a.eps);
+    const float inv = norm_inverse(ss, a);
     const bool finite = ss < INFINITY;
     float s = 0.0f, r = 0.0f;
     if (OUT == NormOut::INT8_ROW) {
@@ -274,7 +281,7 @@ __global__ __launch_bounds__(64 * kNormWaves) void rmsnorm_quant_kernel(NormArgs
             top = max(top, tops[i]);
         norm_scale<OUT>(top, s, r);
         if (threadIdx.x == 0)
-            a.scale[row] = s;
+            a.scale[row] = s * a.unlift;
     }
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
@@ -285,7 +292,7 @@ __global__ __launch_bounds__(64 * kNormWaves) void rmsnorm_quant_kernel(NormArgs
             h[j] = norm_value(h[j], c < nch ? gr[c] : none, inv);
             norm_scale<OUT>(group_max_u32<kSliceLanes<OUT>>(norm_largest(h[j], finite)), s, r);
             if (c < nch && lane % kSliceLanes<OUT> == 0)
-                *norm_scale_at<OUT>(a, row, c) = s;
+                *norm_scale_at<OUT>(a, row, c) = s * a.unlift;
         }
         if (c < nch)
             reinterpret_cast<uint2 *>(a.q + row * (int64_t)K)[c] = norm_codes<OUT>(h[j], s, r);
@@ -310,7 +317,7 @@ __global__ __launch_bounds__(256) void rmsnorm_quant_long_kernel(NormArgs a)
     for (int c = lane; c < nch; c += 64)
         norm_squares(load(c), ss);
     ss = wave_sum(ss);
-    const float inv = norm_inverse(ss, K, a.eps);
+    const float inv = norm_inverse(ss, a);
     const bool finite = ss < INFINITY;
     float s = 0.0f, r = 0.0f;
     if (OUT == NormOut::INT8_ROW) {
@@ -319,7 +326,7 @@ __global__ __launch_bounds__(256) void rmsnorm_quant_long_kernel(NormArgs a)
             top = max(top, norm_largest(norm_value(load(c), gr[c], inv), finite));
         norm_scale<OUT>(group_max_u32<64>(top), s, r);
         if (lane == 0)
-            a.scale[row] = s;
+            a.scale[row] = s * a.unlift;
     }
     for (int base = 0; base < nch; base += 64) {
         const int c = base + lane;
@@ -331,7 +338,7 @@ __global__ __launch_bounds__(256) void rmsnorm_quant_long_kernel(NormArgs a)
         if (OUT != NormOut::INT8_ROW) {
             norm_scale<OUT>(group_max_u32<kSliceLanes<OUT>>(norm_largest(y, finite)), s, r);
             if (c < nch && lane % kSliceLanes<OUT> == 0)
-                *norm_scale_at<OUT>(a, row, c) = s;
+                *norm_scale_at<OUT>(a, row, c) = s * a.unlift;
         }
         if (c < nch) {
             reinterpret_cast<uint2 *>(a.q + row * (int64_t)K)[c] = norm_codes<OUT>(y, s, r);
@@ -387,8 +394,10 @@ void launch_quantize_weight_f8(const uint16_t *w, int64_t N, int K, uint8_t *q, 
                        scale, N, K, kblocks);
 }
 
-void launch_rmsnorm_quant(NormOut out, const NormArgs &a, hipStream_t st)
+void launch_rmsnorm_quant(NormOut out, NormArgs a, hipStream_t st)
 {
+    a.lift = a.eps > 0x1p60f ? kF8Lift : 1.0f;
+    a.unlift = 1.0f / a.lift;
     switch (out) {
     case NormOut::INT8_ROW: launch_norm<NormOut::INT8_ROW>(a, st); return;
     case NormOut::INT8_64: launch_norm<NormOut::INT8_64>(a, st); return;

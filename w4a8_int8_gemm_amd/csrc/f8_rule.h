@@ -9,7 +9,8 @@
 // that every product with it is NaN and no other block is touched.
 //
 // This header is also compiled for the host by the CPU test suite, which
-// checks the corrected quotient against the division for every fp16 input.
+// checks the corrected quotient against the division for every fp16 input and
+// for the fp32 inputs that come nearest to a border.
 #pragma once
 
 #include "quant_rule.h"
@@ -27,12 +28,32 @@ W4A8_HD float f8_scale(float amax)
 }
 
 // fl32(x / s) from r = fl32(1 / s): with t = fl32(x r) the residual t s - x is
-// exact in one fma, and one step of correction gives the division's result
-// for every fp16 x and amax.  In this order of signs a -0 stays -0.
+// taken in one fma, and one step of correction gives the division's result.  In
+// this order of signs a -0 stays -0.
+//
+// That it is the division's result for every fp32 x and s, in steps of the
+// quotient: r is within half a step of 1 / s, so t is within 1.5 of x / s, and
+// the residual is exact if t is within 1, else off by one unit of the product
+// of x's and s's steps.  Before its rounding the corrected value is then off by
+// less than 5 / (2 S), S the 24-bit integer of s, and x / s is never nearer
+// than 1 / (2 S) to the middle of two steps.  The CPU tests try all pairs that
+// lie within 8 / (2 S).  It takes a residual that does not underflow: quotients
+// from 2^-11 on (below 2^-10 every e4m3 code is 0, below 1/2 every int8 code)
+// with s of at least 2^-90; smaller ones are lifted (f8_reciprocal).
 W4A8_HD float f8_quotient(float x, float s, float r)
 {
     const float t = x * r;
     return fmaf(-fmaf(t, s, -x), r, t);
+}
+
+// What the codes of a block take for its scale s: 0, zero codes, for s = 0 and
+// s = NaN; fl32(1 / s); or for s below 2^-90 -fl32(1 / (s 2^64)), whose sign
+// says that both sides of the quotient are to be taken 2^64 times as large.
+constexpr float kF8Exact = 0x1p-90f, kF8Lift = 0x1p64f;
+W4A8_HD float f8_reciprocal(float s)
+{
+    const float r = 1.0f / (s < kF8Exact ? s * kF8Lift : s);
+    return s >= kF8Exact ? r : s > 0.0f ? -r : 0.0f;
 }
 
 }  // namespace w4a8
