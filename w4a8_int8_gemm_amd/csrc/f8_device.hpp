@@ -41,19 +41,12 @@ __device__ __forceinline__ uint32_t f8_codes4(float a, float b, float c, float d
     return (uint32_t)w;
 }
 
-// silu(g) = g / (1 + e^-g); gelu in its tanh form, 0.5 g (1 + tanh z) =
-// g / (1 + e^-2z) with z = sqrt(2 / pi) (g + 0.044715 g^3).  The exponential
-// and the reciprocal are the hardware's (one step of fp32 each, and the
-// rounded argument: about 2^-22 of the result relative for |g| up to 30, far
-// below the output's own rounding); e^-g overflows to infinity for very
-// negative g, which gives -0.
+// The gated product's activation by the hardware's exponential and reciprocal
+// (f8_rule.h has the steps and how far off they are).
 __device__ __forceinline__ float f8_activation(float g, int gelu)
 {
-    float t = g;
-    if (gelu)
-        t = 1.5957691216057308f * fmaf(0.044715f * g, g * g, g);
-    const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * t);
-    return g * __builtin_amdgcn_rcpf(1.0f + e);
+    return f8_activation_steps(
+        g, gelu, [](float x) { return __builtin_amdgcn_exp2f(x); }, [](float x) { return __builtin_amdgcn_rcpf(x); });
 }
 
 }  // namespace w4a8

@@ -56,4 +56,28 @@ W4A8_HD float f8_reciprocal(float s)
     return s >= kF8Exact ? r : s > 0.0f ? -r : 0.0f;
 }
 
+// silu(g) = g / (1 + e^-g); gelu in its tanh form, 0.5 g (1 + tanh z) =
+// g / (1 + e^-2z) with z = sqrt(2 / pi) (g + 0.044715 g^3).
+//
+// How far from these, with u = 2^-24 (half a step of fp32) and an exponential
+// and a reciprocal good to 2 u: the exponent -log2(e) t carries the constant's
+// and the product's rounding, 1.3 u of it, for gelu also t's own: four roundings
+// in the cubic, two in the factor, 6 u.  As a power it is off by that times |t|,
+// and weighs e / (1 + e) in the result.  The sum, the reciprocal, the last
+// product and the exponential's own 2 u are another 6 u.  So, of the result,
+//     silu  (1.3 |g| w + 6) u,  gelu  (7.3 |t| w + 6) u,  w = 1 / (1 + e^t) <= 1:
+// 2^-18.5 for silu at g = -30, 2^-17 for gelu at -5 (t = -16.9) and about half
+// of that with half of t; 2^-21 where g > 0.  Far below the rounding of the output
+// (2^-11, 2^-4) as long as there is a result: below |g| 2^-126 it may be 0 (e^-g
+// overflows to infinity, which gives -0).
+template <typename Exp2, typename Rcp>
+W4A8_HD float f8_activation_steps(float g, int gelu, Exp2 exp2, Rcp rcp)
+{
+    float t = g;
+    if (gelu)
+        t = 1.5957691216057308f * fmaf(0.044715f * g, g * g, g);
+    const float e = exp2(-1.4426950408889634f * t);
+    return g * rcp(1.0f + e);
+}
+
 }  // namespace w4a8
