@@ -984,7 +984,7 @@ w4a8_status_t quantize_act_f8(const w4a8_f16 *x, int64_t M, int64_t K, uint8_t *
                               w4a8_stream_t stream)
 {
     const char *fn = "quantize_act_f8";
-    if (M < 0 || K < 0 || M > kMaxRowsF8 || K > kMaxDim)
+    if (M < 0 || K < 0 || M > kMaxRowsF8 || K > kMaxKGemm)
         return fail(W4A8_ERR_INVALID_ARG, "%s: sizes out of range (M=%lld K=%lld)", fn, (long long)M,
                     (long long)K);
     w4a8_status_t st = check_quant(fn, x, M, K, 0, xq, x_scale, false);
@@ -1003,6 +1003,9 @@ w4a8_status_t quantize_weight_f8(const w4a8_f16 *w, int64_t N, int64_t K, uint8_
                                  w4a8_stream_t stream)
 {
     const char *fn = "quantize_weight_f8";
+    if (N < 0 || K < 0 || N > kMaxDim || K > kMaxKGemm)
+        return fail(W4A8_ERR_INVALID_ARG, "%s: sizes out of range (N=%lld K=%lld)", fn, (long long)N,
+                    (long long)K);
     w4a8_status_t st = check_quant(fn, w, N, K, 0, wq, w_scale, false);
     if (st != W4A8_OK)
         return st;

@@ -378,7 +378,7 @@ void launch_quantize_act_f8(const uint16_t *x, int64_t rows, int K, uint8_t *q, 
                             hipStream_t st)
 {
     constexpr int64_t kWaves = 1 << 25;                    // of 64 threads; a launch of 2^32 threads would wrap
-    int64_t waves = (K + 511) / 512;
+    int64_t waves = ((int64_t)K + 511) / 512;
     if (waves * rows > kWaves)
         waves = kWaves / rows;
     hipLaunchKernelGGL(quant_act_f8_kernel, dim3((unsigned)((rows * waves + 3) / 4)), dim3(256), 0, st, x, q, scale,
