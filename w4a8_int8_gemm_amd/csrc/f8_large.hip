@@ -109,10 +109,13 @@ void f8_gemm_large_kernel(F8Args a, int tiles_m, int tiles_n, int group_m)
         tile_origin(cur_tile, m0, n0);
         cur_m0 = m0;
         rx = make_rsrc(a.x + (int64_t)m0 * K, (uint32_t)(min(LBM, M - m0) * K));
-        const int n1 = GATED ? n0 : n0 + 128;
+        // where the tile has no second half the first takes its place, and its
+        // columns are not stored: an empty resource would leave it to the range
+        // check to sum an offset of K and the lane's without a wrap
+        const int n1 = GATED || n0 + 128 >= N ? n0 : n0 + 128;
         rw0 = make_rsrc(a.w[0] + (int64_t)n0 * K, (uint32_t)(min(128, N - n0) * K));
-        rw1 = make_rsrc(a.w[GATED] + (int64_t)min(n1, N) * K, (uint32_t)(max(0, min(128, N - n1)) * K));
-        const int nb = n0 >> 7, nb1 = GATED ? nb : min(nb + 1, ((N + 127) >> 7) - 1);
+        rw1 = make_rsrc(a.w[GATED] + (int64_t)n1 * K, (uint32_t)(min(128, N - n1) * K));
+        const int nb = n0 >> 7, nb1 = n1 >> 7;
         if (group == 0)
             scp = a.sx + min(m0 + wave * 64, M - 1);
         else
