@@ -102,7 +102,7 @@ __device__ __forceinline__ Eight widen(uint4 u)
              hi_h2f(u.w)}};
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+template <typename T> __device__ __forceinline__ T wave_sum(T v)
 {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
@@ -299,7 +299,9 @@ __global__ __launch_bounds__(64 * kNormWaves) void rmsnorm_quant_kernel(NormArgs
     }
 }
 
-// Longer rows: one wavefront a row, which is read again for each step (from cache).
+// Longer rows: one wavefront a row, which is read again for each step (from
+// cache).  A lane sums up to 2^16 squares: eight at a time in fp32 and those in
+// 64 bits, or a row of 2^22 equal values is off by up to 2e-3 of its sum.
 template <NormOut OUT>
 __global__ __launch_bounds__(256) void rmsnorm_quant_long_kernel(NormArgs a)
 {
@@ -313,10 +315,13 @@ __global__ __launch_bounds__(256) void rmsnorm_quant_long_kernel(NormArgs a)
     const uint4 *gr = reinterpret_cast<const uint4 *>(a.gain);
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
     auto load = [&](int c) __attribute__((always_inline)) { return norm_sum(xr[c], rr ? rr[c] : none); };
-    float ss = 0.0f;
-    for (int c = lane; c < nch; c += 64)
-        norm_squares(load(c), ss);
-    ss = wave_sum(ss);
+    double total = 0.0;
+    for (int c = lane; c < nch; c += 64) {
+        float eight = 0.0f;
+        norm_squares(load(c), eight);
+        total += eight;
+    }
+    const float ss = (float)wave_sum(total);
     const float inv = norm_inverse(ss, a);
     const bool finite = ss < INFINITY;
     float s = 0.0f, r = 0.0f;
