@@ -454,7 +454,8 @@ w4a8_status_t quantize_weight_f8(const w4a8_f16 *w, int64_t N, int64_t K, uint8_
  * rounded to fp16 before it is quantized, and the norm is that of h, not of
  * fp16(h).  The int8 rule is that of quantize_act, with s below 2^-126 taken
  * as 0.  A row that holds a value of h that is not finite (or whose squares'
- * sum is not) gets NaN scales and zero codes, a row of zeros scales of 0.
+ * sum is not) gets NaN scales and zero codes, a row of zeros (under finite gains)
+ * scales of 0.
  * residual_out may be residual or x itself; no other output may overlap an
  * input.  K % 8 == 0, K <= 2^22, M <= 2^25, 0 <= eps <= 2^127. */
 w4a8_status_t rmsnorm_quant(w4a8_mode_t mode, const w4a8_f16 *x, const w4a8_f16 *residual,
@@ -468,8 +469,9 @@ size_t f8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
  *     y[m, n] = fp16( sum_b x_scale[b, m] * w_scale[n / 128, b] * P_b[m, n] ),
  *     P_b[m, n] = sum over k in block b of xq[m, k] * wq[n, k]
  * P_b from the fp8 matrix unit, which adds each group of eight consecutive
- * products to 13 bits below the largest of them; the sum over the blocks is
- * held in fp32, the two scales multiplied in fp32.  y fp16 [M, N]; any M >= 0
+ * products to 13 bits below the largest of them (so that a group may lose up to
+ * 7 * 2^-13 of its largest product, if seven lie that far below it; about 1e-5 of
+ * the result on quantized activations); the sum over the blocks is held in fp32, the two scales multiplied in fp32.  y fp16 [M, N]; any M >= 0
  * and N >= 0.  Same bits for the same call.  workspace: device buffer of
  * f8_gemm_workspace_size() bytes, 256-byte aligned (may be NULL when that is
  * 0), which needs no initial content; calls that overlap need their own. */
