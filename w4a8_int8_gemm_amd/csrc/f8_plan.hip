@@ -34,9 +34,9 @@ int splits_of(int64_t M, int64_t N, int64_t K, bool gated)
     return few(M, N) ? few_splits(N, K, gated) : 1;
 }
 
-// Microseconds, as a model: kernels for one to 256 tokens are bound by their
-// copies into LDS, one of 1 KiB taking 14.1 ns of a compute unit (16.3 ns a
-// workgroup where two share one), or by the latency of the stages on the way;
+// Microseconds, as a model: kernels for one to 256 tokens take the time of their
+// copies into LDS, 14.1 ns for one of 1 KiB by a workgroup that has a compute
+// unit of its own (16.3 where two share one), or of the stages on the way;
 // a stage of a large tile takes 0.96 to 1.1 us with the share of the chip that
 // is busy.  Fitted to 128 shapes (65 to 3000 tokens, 1024 to 14336 columns and
 // K, weights from HBM) with every kernel: the choice is 0.4 % slower than the

@@ -52,8 +52,9 @@ __global__ __launch_bounds__(256) void quant_act_f8_kernel(const uint16_t *__res
     }
 }
 
-// One workgroup a 128 x 128 block: wave w owns rows w, w + 4, ..., four rows a
-// step (16 lanes each).
+// One workgroup a 128 x 128 block, in registers: wave w owns rows 4 w .. 4 w + 3
+// of every sixteen, 16 lanes each.  Bound by memory: 12288 x 4096 27.4 us (5.5
+// TB/s, part of it from the caches), 4096 x 4096 10.0.
 __global__ __launch_bounds__(256) void quant_weight_f8_kernel(const uint16_t *__restrict__ w,
                                                               uint8_t *__restrict__ q,
                                                               float *__restrict__ scale, int64_t N,
@@ -211,9 +212,12 @@ __device__ __forceinline__ void norm_store_sum(const NormArgs &a, int64_t row, i
 // a lane, all in registers: the row is read once.  Its sum of squares and, for
 // int8 rows, its largest value meet over the lanes and then in LDS.
 //
-// Bound by memory: 7 bytes a value with a residual, 3 without, of which 4516 x
-// 4096 take 28.0 us (4.6 TB/s; a copy of 2 GiB runs at 4.95) and 19.3 (2.9, with
-// the vector unit about half busy).  Four waves a row in registers against one
+// Bound by memory: 7 bytes a value with a residual, of which 4516 x 4096 take 27.5
+// us into e4m3 (4.7 TB/s; a copy of 2 GiB runs at 4.95), 26.6 into int8 by rows and
+// 27.5 by groups.  Without one, 3 bytes a value, 18.5 us (3.0 TB/s) and 19.2: a
+// row's load, its meetings and its codes follow one another, and the vector
+// unit is about half busy; a workgroup that has its next row's load on the way
+// has not been tried.  Four waves a row in registers against one
 // wave a row that reads it again for each step: 40.4 and 19.8 us, and 1 x 4096
 // 9.3 against 3.5.
 constexpr int kNormWaves = 16;
@@ -300,8 +304,9 @@ __global__ __launch_bounds__(64 * kNormWaves) void rmsnorm_quant_kernel(NormArgs
 }
 
 // Longer rows: one wavefront a row, which is read again for each step (from
-// cache).  A lane sums up to 2^16 squares: eight at a time in fp32 and those in
-// 64 bits, or a row of 2^22 equal values is off by up to 2e-3 of its sum.
+// cache).  1 x 18432 26 us (1 x 16384, in registers, 5.2), 4516 x 20480 with a
+// residual 237 (2.7 TB/s).  A lane sums up to 2^16 squares: eight at a time in
+// fp32 and those in 64 bits, or the sum of 2^22 is off by up to 2e-3 of it.
 template <NormOut OUT>
 __global__ __launch_bounds__(256) void rmsnorm_quant_long_kernel(NormArgs a)
 {

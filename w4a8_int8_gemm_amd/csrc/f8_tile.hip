@@ -2,18 +2,20 @@
 // tiles, their stages in a deep ring (gfx950).
 //
 // Where the output has too few tiles for the large ones, a workgroup's time is
-// that of bringing its operands into LDS (64 bytes a cycle and compute unit
-// at best) and of the latency of each stage.  So: tiles small enough to fill
+// that of bringing its operands into LDS and of the latency of each stage.  So: tiles small enough to fill
 // the chip, a ring of D stages of 128 bytes of K that the four waves fill
 // together, up to D - 1 of them on the way, one barrier a stage, the next
 // stage's fragments read while one is multiplied.  With 64 columns and e4m3
 // output two workgroups share a scale; they meet as those of f8_few.hip do.
 // Where the tiles are few, workgroups take parts of K.
 //
-// 517 x 4096 x 4096 17.2 us (1010 TFLOP/s; 20.9 with its quantizer), 300 x 5120 x
-// 2560 10.8 us and the gated pair 301 x 5121 x 2560 16.5 (960 TFLOP/s): 5.5 us of
-// each are a launch's start and end, the rest 0.28 to 0.5 us a stage, the rate
-// at which a compute unit's copies arrive.
+// 517 x 4096 x 4096 17.4 us (1000 TFLOP/s; 21 with its quantizer), 300 x 5120 x
+// 2560 11.1 us and the gated pair 301 x 5121 x 2560 17.8 (890 TFLOP/s): 5.5 us of
+// each are a launch's start and end, the rest 0.28 to 0.6 us a stage, in which
+// a workgroup brings 53 to 77 KB/us.  Two on one compute unit bring 125
+// together, so it is not the unit's rate that bounds these, which have one
+// each, but what four waves with a barrier a stage keep on the way; eight
+// waves a workgroup have not been tried.
 #include "f8_join.hpp"
 #include "f8_store.hpp"
 
