@@ -19,10 +19,11 @@
 // From HBM: 1 x 4096 x 12288 12.1 us (4.2 TB/s), gated 1 x 12288 x 4096 to fp16
 // 23.2 (4.3 TB/s) and in 8 bits, with the workgroups' meeting, 24.2, 32 x 4096 x
 // 14336 17.5 (3.4 TB/s), 32 x 10240 x 2560 10.8; that one mostly from the caches
-// 7.8, of which 5 to 6 us are those of any launch with its first copies.  From 33 tokens on a workgroup's copy of x is larger than its
-// weights: 64 x 4096 x 14336 23.9 us (2.5 TB/s).  64 x 64 tiles with K in four
-// read a third of that, but their parts have to meet: 22.4 us there, and 13.3
-// against 8.6 at 64 x 4096 x 4096, 15.7 against 13.3 at K = 7168.
+// 7.8, of which 5 to 6 us are those of any launch with its first copies.  From
+// 33 tokens on a workgroup's copy of x is larger than its weights: 64 x 4096 x
+// 14336 23.9 us (2.5 TB/s).  64 x 64 tiles with K in four read a third of that,
+// but their parts have to meet: 22.4 us there, and 13.3 against 8.6 at 64 x 4096
+// x 4096, 15.7 against 13.3 at K = 7168.
 #include "f8_join.hpp"
 #include "lds_copy.hpp"
 

@@ -2,12 +2,12 @@
 // tiles, their stages in a deep ring (gfx950).
 //
 // Where the output has too few tiles for the large ones, a workgroup's time is
-// that of bringing its operands into LDS and of the latency of each stage.  So: tiles small enough to fill
-// the chip, a ring of D stages of 128 bytes of K that the four waves fill
-// together, up to D - 1 of them on the way, one barrier a stage, the next
-// stage's fragments read while one is multiplied.  With 64 columns and e4m3
-// output two workgroups share a scale; they meet as those of f8_few.hip do.
-// Where the tiles are few, workgroups take parts of K.
+// that of bringing its operands into LDS and of the latency of each stage.  So:
+// tiles small enough to fill the chip, a ring of D stages of 128 bytes of K that
+// the four waves fill together, up to D - 1 of them on the way, one barrier a
+// stage, the next stage's fragments read while one is multiplied.  With 64
+// columns and e4m3 output two workgroups share a scale; they meet as those of
+// f8_few.hip do.  Where the tiles are few, workgroups take parts of K.
 //
 // 517 x 4096 x 4096 17.4 us (1000 TFLOP/s; 21 with its quantizer), 300 x 5120 x
 // 2560 11.1 us and the gated pair 301 x 5121 x 2560 17.8 (890 TFLOP/s): 5.5 us of
